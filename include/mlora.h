@@ -236,6 +236,56 @@ int mlora_linear_fp8w(const void* x, const uint8_t* W_fp8, const float* w_scale,
                       int lora_on, void* y, void* workspace, size_t workspace_bytes,
                       hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The layer with what follows it
+ * ---------------------------------------------------------------------- */
+
+/* Activations of an epilogue. Or-ing MLORA_ACT_GATED in makes it gated. */
+#define MLORA_ACT_NONE 0
+#define MLORA_ACT_RELU 1      /* max(z, 0)                                              */
+#define MLORA_ACT_SILU 2      /* z / (1 + exp(-z))                                      */
+#define MLORA_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2                            */
+#define MLORA_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2      */
+#define MLORA_ACT_GATED 16
+
+/* Bias, activation, gate and residual of a product z [n, d_out]:
+ *
+ *     y = act(z + bias) + residual                                 y [n, d_out]
+ *     y = act(g + bias_g) * (u + bias_u) + residual   (gated)      y [n, d_out / 2]
+ *
+ * where a gated z = [g, u] stacks the gate rows of the weight before its up
+ * rows (W = [W_gate; W_up], the stacking of a fused adapter over gate|up) and
+ * d_out is even. Computed in fp32 on the accumulators, y rounded once. bias
+ * [d_out] and residual (y's shape) are in the element type of x, 16-byte
+ * aligned, NULL for none. residual may be y itself (added in place); it must
+ * not otherwise overlap y. A struct of zeros, or a NULL epilogue, is none. */
+typedef struct {
+  const void* bias;
+  const void* residual;
+  int act;
+} mlora_epilogue_t;
+
+/* mlora_linear, mlora_linear_tokens and mlora_linear_fp8w with an epilogue:
+ * arguments, workspace, results and errors as theirs, y as above, residual in
+ * y's row order (the caller's). With bias, residual and act all absent the
+ * results are theirs bit for bit. Further errors: MLORA_ERR_INVALID_ARG
+ * (unknown act, misaligned bias or residual), MLORA_ERR_SHAPE (gated with an
+ * odd d_out). */
+int mlora_linear_epilogue(const void* x, const void* W, mlora_pool_t pool, const int32_t* seg_start,
+                          const int32_t* seg_adapter, const int32_t* seg_rank, const float* seg_scale,
+                          const int32_t* token_index, int n_tokens, int n_seg, int lora_on,
+                          const mlora_epilogue_t* epilogue, void* y, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+int mlora_linear_tokens_epilogue(const void* x, const void* W, mlora_pool_t pool,
+                                 const int32_t* token_adapter, const float* adapter_scale, int n_tokens,
+                                 int lora_on, const mlora_epilogue_t* epilogue, void* y, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+int mlora_linear_fp8w_epilogue(const void* x, const uint8_t* W_fp8, const float* w_scale, mlora_pool_t pool,
+                               const int32_t* seg_start, const int32_t* seg_adapter, const int32_t* seg_rank,
+                               const float* seg_scale, const int32_t* token_index, int n_tokens, int n_seg,
+                               int lora_on, const mlora_epilogue_t* epilogue, void* y, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
 /* Canonical segmentation of an unsorted batch on the device: tokens grouped
  * by adapter id in ascending id order (-1 first), tokens of one id in
  * ascending batch order. Outputs (device):
@@ -275,6 +325,83 @@ int mlora_token_map(const int32_t* seg_start, const int32_t* seg_adapter, int n_
 int mlora_validate(mlora_pool_t pool, const int32_t* seg_start, const int32_t* seg_adapter,
                    const int32_t* seg_rank, const int32_t* token_index, int n_tokens, int n_seg,
                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Experts: routing, the product of each routed row with its expert's weight,
+ * and the weighted way back
+ *
+ * A layer of n_experts base weights of one shape, of which each token uses
+ * top_k: the base model of a LoRA-served mixture of experts, whose adapters sit
+ * on the shared projections that mlora_linear computes. A batch has n_tokens x
+ * top_k slots (t, j). Grouped by expert they become sorted positions, and the
+ * segments have the layout of the adapter segments above: seg_start
+ * [n_experts + 1] with segment e the positions of expert e, and token_index.
+ *
+ * n_experts in 1 .. MLORA_MAX_EXPERTS, top_k in 1 .. MLORA_MAX_TOP_K and at
+ * most n_experts, at most MLORA_MAX_POSITIONS slots.
+ * ---------------------------------------------------------------------- */
+#define MLORA_MAX_EXPERTS 1024
+#define MLORA_MAX_TOP_K 64
+#define MLORA_MAX_POSITIONS (1 << 23)
+
+/* Bytes of workspace mlora_route needs (0 if a size is out of range). The
+ * workspace needs no initialization and holds nothing between calls. */
+size_t mlora_route_workspace_bytes(int n_tokens, int n_experts, int top_k);
+
+/* Choose top_k experts per token and group the batch by expert.
+ * logits [n_tokens, n_experts] in dtype. Slot (t, j) gets token t's j-th
+ * largest logit, equal ones in expert order. A logit of -inf or NaN is never
+ * chosen: slots it leaves over have expert -1 and weight 0 and no position (a
+ * padded token is a row of -inf). Outputs:
+ *   expert [n_tokens, top_k]    expert id, or -1
+ *   weight [n_tokens, top_k]    fp32: exp(l - m) over the sum of exp(l' - m), m the row's largest
+ *                               logit, the sum over the chosen experts (renormalize = 1: weights
+ *                               add up to 1) or over all of them (0). Infinite logits share it.
+ *   seg_start [n_experts + 1]   first sorted position of each expert; the last entry is the
+ *                               number of positions in use
+ *   token_index [n_tokens top_k]  token of each sorted position, -1 behind the last in use
+ *   position [n_tokens, top_k]  sorted position of each slot, or -1
+ * Positions of one expert are in slot order, so the outputs are unique.
+ * n_tokens = 0 writes seg_start (zeros) only; the other arrays may be NULL.
+ * Errors: MLORA_ERR_DTYPE, MLORA_ERR_SHAPE, MLORA_ERR_INVALID_ARG,
+ * MLORA_ERR_WORKSPACE. */
+int mlora_route(const void* logits, int dtype, int n_tokens, int n_experts, int top_k, int renormalize,
+                int32_t* expert, float* weight, int32_t* token_index, int32_t* seg_start, int32_t* position,
+                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* y[p] = act(W_e x[token_index[p]] + bias_e) for the sorted positions p of
+ * every expert e, gated as mlora_linear_epilogue. x [n_rows, d_in] in dtype;
+ * W [n_experts, d_out, d_in] in dtype or, with w_scale [n_experts, d_out]
+ * (fp32, device), e4m3 codes as mlora_linear_fp8w takes them (dtype bf16, d_in
+ * a multiple of 16). token_index [n_pos], or NULL: position p reads row p of x
+ * (n_rows >= n_pos). y [n_pos, d_out] (gated: d_out / 2); rows behind
+ * seg_start[n_experts] are left as they were. epilogue: bias [n_experts,
+ * d_out] and act; its residual must be NULL (rows of y are positions). NULL:
+ * none. seg_start entries are clamped into [0, n_pos] and token_index into
+ * [0, n_rows). n_pos = 0 does nothing.
+ * Errors: MLORA_ERR_DTYPE, MLORA_ERR_SHAPE, MLORA_ERR_INVALID_ARG. */
+int mlora_experts_linear(const void* x, const void* W, const float* w_scale, int dtype, int n_rows,
+                         int n_experts, int d_in, int d_out, const int32_t* seg_start,
+                         const int32_t* token_index, int n_pos, const mlora_epilogue_t* epilogue, void* y,
+                         hipStream_t stream);
+
+/* Bytes of workspace mlora_experts_combine needs (0 if a size is out of
+ * range). It needs no initialization and holds nothing between calls. */
+size_t mlora_experts_workspace_bytes(int n_tokens, int top_k, int n_experts, int d_out, int dtype);
+
+/* out[t] = residual[t] + sum over j of weight[t, j] (W_e h[p] + bias_e), with
+ * p = position[t, j] and e the expert of p; slots with position -1 add
+ * nothing. h [n_tokens top_k, d_in] by sorted position (mlora_experts_linear's
+ * y; rows behind the last position in use are not read), W and w_scale as
+ * above, bias [n_experts, d_out] and residual [n_tokens, d_out] in dtype or
+ * NULL; residual may be out itself. Products and sums in fp32, slots in order
+ * of j, out rounded once: the result does not vary between runs.
+ * Errors: as mlora_experts_linear, plus MLORA_ERR_WORKSPACE. */
+int mlora_experts_combine(const void* h, const void* W, const float* w_scale, int dtype, int n_tokens,
+                          int top_k, int n_experts, int d_in, int d_out, const int32_t* seg_start,
+                          const int32_t* position, const float* weight, const void* bias,
+                          const void* residual, void* out, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Merged weights

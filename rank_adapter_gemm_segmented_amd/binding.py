@@ -26,6 +26,16 @@ STATUS = {
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
 
+# activations of an epilogue, by name
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_GATED = 16
+
+
+class _Epilogue(ctypes.Structure):
+    """``mlora_epilogue_t``"""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("act", ctypes.c_int)]
+
+
 class MloraError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -59,6 +69,14 @@ def _load() -> ctypes.CDLL:
         "mlora_register_adapter_fused": ([P, I, I, P, P, P, P, P], I),
         "mlora_linear_fp8w": ([P, P, P, P, P, P, P, P, P, I, I, I, P, P, SZ, P], I),
         "mlora_linear_noalloc": ([P, P, P, P, P, P, P, P, I, I, I, P, P], I),
+        "mlora_linear_epilogue": ([P, P, P, P, P, P, P, P, I, I, I, P, P, P, SZ, P], I),
+        "mlora_linear_tokens_epilogue": ([P, P, P, P, P, I, I, P, P, P, SZ, P], I),
+        "mlora_linear_fp8w_epilogue": ([P, P, P, P, P, P, P, P, P, I, I, I, P, P, P, SZ, P], I),
+        "mlora_route_workspace_bytes": ([I, I, I], SZ),
+        "mlora_route": ([P, I, I, I, I, I, P, P, P, P, P, P, SZ, P], I),
+        "mlora_experts_linear": ([P, P, P, I, I, I, I, I, P, P, I, P, P, P], I),
+        "mlora_experts_workspace_bytes": ([I, I, I, I, I], SZ),
+        "mlora_experts_combine": ([P, P, P, I, I, I, I, I, I, P, P, P, P, P, P, P, SZ, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -321,3 +339,206 @@ def merge_adapter(W, pool: Pool, adapter_id: int, scale: float, out=None):
     _check(_lib.mlora_merge_adapter(_ptr(W), _ptr(o), pool.handle, int(adapter_id), float(scale),
                                     _stream()), "mlora_merge_adapter")
     return o
+
+
+# ---- the layer with what follows it -------------------------------------------
+
+def _act_code(act: str, gated: bool) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    return ACTS[act] | (_GATED if gated else 0)
+
+
+def _here(what: str, *tensors):
+    """Every tensor given is contiguous and on the current device: the call
+    runs on that device's current stream."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{what}: tensors must be on the current device")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: tensors must be contiguous")
+
+
+def _epilogue_out(x, rows: int, d_out: int, gated: bool, bias, bias_shape, residual, out):
+    """Checks an epilogue's tensors and returns y."""
+    if gated and d_out % 2:
+        raise ValueError("a gated product needs an even number of weight rows")
+    shape = (rows, d_out // 2 if gated else d_out)
+    if bias is not None and (bias.dtype != x.dtype or tuple(bias.shape) != bias_shape):
+        raise ValueError(f"bias must be {list(bias_shape)} of x's dtype")
+    if residual is not None and (residual.dtype != x.dtype or tuple(residual.shape) != shape):
+        raise ValueError(f"residual must be {list(shape)} of x's dtype")
+    if out is None:
+        return torch.empty(shape, dtype=x.dtype, device=x.device)
+    if out.dtype != x.dtype or tuple(out.shape) != shape:
+        raise ValueError(f"out must be {list(shape)} of x's dtype")
+    return out
+
+
+def linear_epilogue(x, W, pool: Pool, seg_start=None, seg_adapter=None, seg_rank=None, seg_scale=None,
+                    lora_on: int = 1, token_index=None, bias=None, act: str = "none", gated: bool = False,
+                    residual=None, w_scale=None, out=None, workspace=None):
+    """``mlora_linear_epilogue``: act(W x + adapter term + bias) + residual; with
+    ``gated``, W stacks gate over up rows and the result is act(gate) * up +
+    residual. With ``w_scale``, W holds e4m3 codes (``mlora_linear_fp8w_epilogue``).
+    ``residual`` may be ``out`` itself."""
+    if w_scale is None:
+        _check_xw(x, W, pool)
+    else:
+        if x.dtype != torch.bfloat16 or pool.dtype != torch.bfloat16:
+            raise TypeError("x and the pool must be bf16")
+        if W.dtype != torch.uint8 or tuple(W.shape) != (pool.d_out, pool.d_in):
+            raise ValueError("W must be uint8 [d_out, d_in]")
+        if w_scale.dtype != torch.float32 or tuple(w_scale.shape) != (pool.d_out,):
+            raise ValueError("w_scale must be float32 [d_out]")
+        if x.dim() != 2 or x.shape[1] != pool.d_in:
+            raise ValueError("x must be [T, d_in]")
+    if seg_scale is not None and seg_scale.dtype != torch.float32:
+        raise TypeError("seg_scale must be float32")
+    T = x.shape[0]
+    code = _act_code(act, gated)
+    y = _epilogue_out(x, T, pool.d_out, gated, bias, (pool.d_out,), residual, out)
+    _here("linear_epilogue", x, W, w_scale, seg_scale, bias, residual, y, workspace)
+    ws = workspace if workspace is not None else pool.workspace(T)
+    n_seg = seg_adapter.numel() if seg_adapter is not None else 0
+    epi = _Epilogue(_ptr(bias), _ptr(residual), code)
+    meta = (_ptr(_i32(seg_start, "seg_start")), _ptr(_i32(seg_adapter, "seg_adapter")), _ptr(_i32(seg_rank, "seg_rank")),
+            _ptr(seg_scale), _ptr(_i32(token_index, "token_index")), T, n_seg, int(lora_on), ctypes.byref(epi),
+            y.data_ptr(), ws.data_ptr(), ws.numel(), _stream())
+    if w_scale is None:
+        _check(_lib.mlora_linear_epilogue(x.data_ptr(), W.data_ptr(), pool.handle, *meta), "mlora_linear_epilogue")
+    else:
+        _check(_lib.mlora_linear_fp8w_epilogue(x.data_ptr(), W.data_ptr(), w_scale.data_ptr(), pool.handle, *meta),
+               "mlora_linear_fp8w_epilogue")
+    return y
+
+
+def linear_tokens_epilogue(x, W, pool: Pool, token_adapter, adapter_scale, lora_on: int = 1, bias=None,
+                           act: str = "none", gated: bool = False, residual=None, out=None, workspace=None):
+    """``mlora_linear_tokens_epilogue``: ``linear_epilogue`` on an unsorted batch."""
+    _check_xw(x, W, pool)
+    T = x.shape[0]
+    code = _act_code(act, gated)
+    y = _epilogue_out(x, T, pool.d_out, gated, bias, (pool.d_out,), residual, out)
+    if adapter_scale is not None and (adapter_scale.dtype != torch.float32 or adapter_scale.numel() != pool.capacity):
+        raise TypeError("adapter_scale must be float32 [capacity]")
+    if token_adapter is not None and token_adapter.numel() != T:
+        raise ValueError("token_adapter must be [T]")
+    _here("linear_tokens_epilogue", x, W, adapter_scale, bias, residual, y, workspace)
+    ws = workspace if workspace is not None else pool.workspace(T)
+    epi = _Epilogue(_ptr(bias), _ptr(residual), code)
+    _check(_lib.mlora_linear_tokens_epilogue(x.data_ptr(), W.data_ptr(), pool.handle,
+                                             _ptr(_i32(token_adapter, "token_adapter")), _ptr(adapter_scale), T,
+                                             int(lora_on), ctypes.byref(epi), y.data_ptr(), ws.data_ptr(), ws.numel(),
+                                             _stream()), "mlora_linear_tokens_epilogue")
+    return y
+
+
+# ---- experts ---------------------------------------------------------------------
+
+def route_workspace(n_tokens: int, n_experts: int, top_k: int, device="cuda") -> torch.Tensor:
+    """A workspace for ``route`` on up to this many tokens."""
+    n = _lib.mlora_route_workspace_bytes(n_tokens, n_experts, top_k)
+    if n == 0:
+        raise MloraError(STATUS_CODE["MLORA_ERR_SHAPE"], "mlora_route_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None):
+    """``mlora_route``: top-k expert choice of logits [T, E] and its segments.
+    Returns (expert [T, k], weight [T, k], token_index [T k], seg_start [E + 1],
+    position [T, k]); ``out`` is such a tuple to write into."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    code = _dtype_code(logits.dtype)
+    T, E = logits.shape
+    dev = logits.device
+    if not 1 <= top_k <= E:
+        raise MloraError(STATUS_CODE["MLORA_ERR_SHAPE"], "mlora_route")
+    if out is None:
+        out = (torch.empty((T, top_k), dtype=torch.int32, device=dev),
+               torch.empty((T, top_k), dtype=torch.float32, device=dev),
+               torch.empty(T * top_k, dtype=torch.int32, device=dev),
+               torch.empty(E + 1, dtype=torch.int32, device=dev),
+               torch.empty((T, top_k), dtype=torch.int32, device=dev))
+    else:
+        for t, n, dt in zip(out, (T * top_k, T * top_k, T * top_k, E + 1, T * top_k),
+                            (torch.int32, torch.float32, torch.int32, torch.int32, torch.int32)):
+            if t.dtype != dt or t.numel() != n:
+                raise ValueError("out must be (expert, weight, token_index, seg_start, position) of this batch")
+    expert, weight, token_index, seg_start, position = out
+    _here("route", logits, *out, workspace)
+    ws = workspace if workspace is not None else route_workspace(T, E, top_k, dev)
+    _check(_lib.mlora_route(logits.data_ptr(), code, T, E, top_k, int(bool(renormalize)), expert.data_ptr(),
+                            weight.data_ptr(), token_index.data_ptr(), seg_start.data_ptr(), position.data_ptr(),
+                            ws.data_ptr(), ws.numel(), _stream()), "mlora_route")
+    return out
+
+
+def _check_experts(x, W, seg_start, w_scale):
+    """Checks the operands of an expert product; returns (dtype code, E, d_out, d_in)."""
+    code = _dtype_code(x.dtype)
+    if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
+        raise ValueError("x must be [rows, d_in] and W [E, d_out, d_in]")
+    E, d_out, d_in = W.shape
+    if w_scale is None:
+        if W.dtype != x.dtype:
+            raise TypeError("x and W must have one dtype")
+    else:
+        if W.dtype != torch.uint8 or x.dtype != torch.bfloat16:
+            raise TypeError("with w_scale, W must be uint8 and x bf16")
+        if w_scale.dtype != torch.float32 or tuple(w_scale.shape) != (E, d_out):
+            raise ValueError("w_scale must be float32 [E, d_out]")
+    if seg_start.dtype != torch.int32 or seg_start.numel() != E + 1:
+        raise ValueError("seg_start must be int32 [E + 1]")
+    return code, E, d_out, d_in
+
+
+def experts_linear(x, W, seg_start, token_index=None, bias=None, act: str = "none", gated: bool = False,
+                   w_scale=None, out=None):
+    """``mlora_experts_linear``: act(W_e x[token_index[p]] + bias_e) for the sorted
+    positions p of every expert e (``route``'s seg_start and token_index), gated as
+    ``linear_epilogue``. Rows of the result behind seg_start[-1] are not written."""
+    code, E, d_out, d_in = _check_experts(x, W, seg_start, w_scale)
+    n_pos = token_index.numel() if token_index is not None else x.shape[0]
+    y = _epilogue_out(x, n_pos, d_out, gated, bias, (E, d_out), None, out)
+    _here("experts_linear", x, W, seg_start, w_scale, bias, y)
+    epi = _Epilogue(_ptr(bias), None, _act_code(act, gated))
+    _check(_lib.mlora_experts_linear(x.data_ptr(), W.data_ptr(), _ptr(w_scale), code, x.shape[0], E, d_in, d_out,
+                                     seg_start.data_ptr(), _ptr(_i32(token_index, "token_index")), n_pos,
+                                     ctypes.byref(epi), y.data_ptr(), _stream()), "mlora_experts_linear")
+    return y
+
+
+def experts_workspace(n_tokens: int, top_k: int, n_experts: int, d_out: int, dtype: torch.dtype,
+                      device="cuda") -> torch.Tensor:
+    """A workspace for ``experts_combine`` on up to this many tokens."""
+    n = _lib.mlora_experts_workspace_bytes(n_tokens, top_k, n_experts, d_out, _dtype_code(dtype))
+    if n == 0:
+        raise MloraError(STATUS_CODE["MLORA_ERR_SHAPE"], "mlora_experts_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def experts_combine(h, W, seg_start, position, weight, bias=None, residual=None, w_scale=None, out=None,
+                    workspace=None):
+    """``mlora_experts_combine``: residual[t] + sum_j weight[t, j] (W_e h[position[t, j]] + bias_e),
+    with ``route``'s seg_start, position and weight. ``residual`` may be ``out`` itself."""
+    code, E, d_out, d_in = _check_experts(h, W, seg_start, w_scale)
+    if position.dim() != 2 or position.dtype != torch.int32:
+        raise ValueError("position must be int32 [T, k]")
+    T, k = position.shape
+    if weight.dtype != torch.float32 or weight.shape != position.shape:
+        raise ValueError("weight must be float32 [T, k]")
+    if h.shape[0] != T * k:
+        raise ValueError("h must hold a row per slot: [T k, d_in]")
+    y = _epilogue_out(h, T, d_out, False, bias, (E, d_out), residual, out)
+    _here("experts_combine", h, W, seg_start, position, weight, w_scale, bias, residual, y, workspace)
+    ws = workspace if workspace is not None else experts_workspace(T, k, E, d_out, h.dtype, h.device)
+    _check(_lib.mlora_experts_combine(h.data_ptr(), W.data_ptr(), _ptr(w_scale), code, T, k, E, d_in, d_out,
+                                      seg_start.data_ptr(), position.data_ptr(), weight.data_ptr(), _ptr(bias),
+                                      _ptr(residual), y.data_ptr(), ws.data_ptr(), ws.numel(), _stream()),
+           "mlora_experts_combine")
+    return y

@@ -101,8 +101,17 @@ WsLayout ws_layout(const mlora_pool_s* p, int T) {
   L.seg_scale = take(t1 * 4);
   L.n_seg = take(16);
   L.counts = take(t1 * 4);
+  // decode plan: of the d_out rows or, with an even d_out, of a gated call's
+  // virtual rows (up to 30 more), whichever needs more
   int n_tiles = 0, kc = 0, n_chunks = 0;
   decode_plan(p->d_in, p->d_out, &n_tiles, &kc, &n_chunks);
+  size_t part_tiles = (size_t)n_chunks * n_tiles;
+  if (p->d_out % 2 == 0) {
+    int gt = 0, gk = 0, gc = 0;
+    decode_plan(p->d_in, gated_rows(p->d_out), &gt, &gk, &gc);
+    part_tiles = std::max(part_tiles, (size_t)gc * gt);
+    n_chunks = std::max(n_chunks, gc);
+  }
   // shrink partial slices: split-K of the large-T path (at most
   // kMaxShrinkSplit), and at T <= 64 also 8 waves per d_in chunk of the
   // decode stream
@@ -111,7 +120,7 @@ WsLayout ws_layout(const mlora_pool_s* p, int T) {
   L.v_part = take((size_t)splits * T * r_ws_of(p->max_rank) * 4);
   // decode partial tiles, only for token counts the decode path takes
   const size_t tt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-  L.ypart = take(p->dtype == MLORA_BF16 && T <= 64 ? (size_t)n_chunks * n_tiles * 64 * tt * 4 : 0);
+  L.ypart = take(p->dtype == MLORA_BF16 && T <= 64 ? part_tiles * 64 * tt * 4 : 0);
   L.pos_info = take((size_t)T * 16);
   L.v_fin = take((size_t)T * r_ws_of(p->max_rank) * 4);
   L.delta = take(delta_bytes(p, T));
@@ -167,6 +176,32 @@ bool debug_validate() {
   return e && e[0] == '1' && e[1] == 0;
 }
 
+// ---- what follows the layer -------------------------------------------------
+int epi_kind_of(const mlora_epilogue_t* e) {
+  if (!e || (!e->bias && !e->residual && e->act == MLORA_ACT_NONE)) return kEpiNone;
+  return (e->act & MLORA_ACT_GATED) ? kEpiGated : kEpiPlain;
+}
+
+// Host check of an epilogue over d_out rows (null: none).
+int epi_status(const mlora_epilogue_t* e, int d_out) {
+  if (!e) return MLORA_OK;
+  const int act = e->act & ~MLORA_ACT_GATED;
+  if (act < MLORA_ACT_NONE || act > MLORA_ACT_GELU_TANH) return MLORA_ERR_INVALID_ARG;
+  if (!aligned16(e->bias) || !aligned16(e->residual)) return MLORA_ERR_INVALID_ARG;
+  if ((e->act & MLORA_ACT_GATED) && d_out % 2 != 0) return MLORA_ERR_SHAPE;
+  return MLORA_OK;
+}
+
+EpiView epi_view_of(const mlora_epilogue_t* e) {
+  EpiView v{};
+  if (e) {
+    v.bias = e->bias;
+    v.residual = e->residual;
+    v.act = e->act & ~MLORA_ACT_GATED;
+  }
+  return v;
+}
+
 // The adapter term as a dense fp32 tile (k_expand_delta, added by the GEMM
 // before its rounding) instead of the GEMM epilogue's MFMA expand: plain bf16
 // pools of rank <= kDxMaxRank with a dense-term region in the workspace, on
@@ -193,8 +228,10 @@ bool use_dense_expand(const mlora_pool_s* p, const SegView& sv, int T, int lora_
 // Launch the layer on sorted metadata already resident on the device.
 // w_scale != null: W holds FP8 e4m3 codes with a float32 scale per row (bf16
 // pool, split-K decode path only; the caller has checked the shape).
+// epi != null: what follows the layer, already checked (epi_status).
 int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& sv, int T,
-               int lora_on, void* y, char* ws, hipStream_t stream, const float* w_scale = nullptr) {
+               int lora_on, void* y, char* ws, hipStream_t stream, const float* w_scale = nullptr,
+               const mlora_epilogue_t* epi = nullptr) {
   const WsLayout L = ws_layout(pool, T);
   LinearArgs a;
   a.x = x;
@@ -214,6 +251,8 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
   a.delta = nullptr;
   a.gorder = 0;
   a.wnt = 0;
+  a.epi_kind = epi_kind_of(epi);
+  a.epi = epi_view_of(epi);
   if (pool->dtype == MLORA_BF16) {
     const int fp = forced_path();
     // The split-K decode path up to 64 tokens, except on wide layers from 48
@@ -241,7 +280,9 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
       d.v_part = a.v_part;
       d.pos = a.pos_info;
       d.r_ws = a.r_ws;
-      decode_plan(pool->d_in, pool->d_out, &d.n_tiles, &d.kc, &d.n_chunks);
+      d.epi_kind = a.epi_kind;
+      d.epi = a.epi;
+      decode_plan(pool->d_in, a.epi_kind == kEpiGated ? gated_rows(pool->d_out) : pool->d_out, &d.n_tiles, &d.kc, &d.n_chunks);
       d.unit_rows = decode_unit_rows(lora_on ? sv.n_seg : 0, pool->max_rank, d.n_tiles);
       d.w_scale = w_scale;
       if (log_calls())
@@ -257,7 +298,7 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
     one.ks = 1;
     const bool one_chunk = lora_on && ((T <= 16 * a.seg_grid && pool->max_rank <= 16) || shrink_short(one));
     a.ks = one_chunk ? 1 : choose_shrink_split_bf16(pool->d_in, shrink_items_bound(T, a.seg_grid, pool->max_rank));
-    if (fp == 3 && T <= 64) {
+    if (fp == 3 && T <= 64 && a.epi_kind == kEpiNone) {
       if (log_calls())
         log_call("gemv", T, pool, sv, lora_on, a.ks, !lora_on || a.seg_grid <= 0 ? "none" : shrink_short(a) ? "short" : "mfma");
       launch_shrink_bf16(a, stream);
@@ -521,11 +562,13 @@ int mlora_workspace_init(void* workspace, size_t workspace_bytes, hipStream_t st
   return check_launch();
 }
 
-int mlora_linear(const void* x, const void* W, mlora_pool_t pool, const int32_t* seg_start,
-                 const int32_t* seg_adapter, const int32_t* seg_rank, const float* seg_scale,
-                 const int32_t* token_index, int n_tokens, int n_seg, int lora_on, void* y,
-                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+int mlora_linear_epilogue(const void* x, const void* W, mlora_pool_t pool, const int32_t* seg_start,
+                          const int32_t* seg_adapter, const int32_t* seg_rank, const float* seg_scale,
+                          const int32_t* token_index, int n_tokens, int n_seg, int lora_on,
+                          const mlora_epilogue_t* epilogue, void* y, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
   if (!pool) return MLORA_ERR_INVALID_ARG;
+  if (const int st = epi_status(epilogue, pool->d_out)) return st;
   if (lora_on != 0 && lora_on != 1) return MLORA_ERR_INVALID_ARG;
   if (n_tokens < 0 || n_tokens > MLORA_MAX_TOKENS) return MLORA_ERR_SHAPE;
   if (n_tokens == 0) return MLORA_OK;
@@ -551,7 +594,15 @@ int mlora_linear(const void* x, const void* W, mlora_pool_t pool, const int32_t*
       if (st != MLORA_OK) return st;
     }
   }
-  return run_linear(x, W, pool, sv, n_tokens, lora_on, y, (char*)workspace, stream);
+  return run_linear(x, W, pool, sv, n_tokens, lora_on, y, (char*)workspace, stream, nullptr, epilogue);
+}
+
+int mlora_linear(const void* x, const void* W, mlora_pool_t pool, const int32_t* seg_start,
+                 const int32_t* seg_adapter, const int32_t* seg_rank, const float* seg_scale,
+                 const int32_t* token_index, int n_tokens, int n_seg, int lora_on, void* y,
+                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return mlora_linear_epilogue(x, W, pool, seg_start, seg_adapter, seg_rank, seg_scale, token_index, n_tokens,
+                               n_seg, lora_on, nullptr, y, workspace, workspace_bytes, stream);
 }
 
 int mlora_linear_noalloc(const void* x, const void* W, mlora_pool_t pool, const int32_t* seg_start,
@@ -571,13 +622,14 @@ int mlora_linear_noalloc(const void* x, const void* W, mlora_pool_t pool, const 
                       n_seg, lora_on, y, ws, (size_t)MLORA_NOALLOC_SCRATCH_BYTES, stream);
 }
 
-int mlora_linear_fp8w(const void* x, const uint8_t* W_fp8, const float* w_scale, mlora_pool_t pool,
-                      const int32_t* seg_start, const int32_t* seg_adapter, const int32_t* seg_rank,
-                      const float* seg_scale, const int32_t* token_index, int n_tokens, int n_seg,
-                      int lora_on, void* y, void* workspace, size_t workspace_bytes,
-                      hipStream_t stream) {
+int mlora_linear_fp8w_epilogue(const void* x, const uint8_t* W_fp8, const float* w_scale, mlora_pool_t pool,
+                               const int32_t* seg_start, const int32_t* seg_adapter, const int32_t* seg_rank,
+                               const float* seg_scale, const int32_t* token_index, int n_tokens, int n_seg,
+                               int lora_on, const mlora_epilogue_t* epilogue, void* y, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
   if (!pool) return MLORA_ERR_INVALID_ARG;
   if (pool->dtype != MLORA_BF16) return MLORA_ERR_DTYPE;
+  if (const int st = epi_status(epilogue, pool->d_out)) return st;
   if (lora_on != 0 && lora_on != 1) return MLORA_ERR_INVALID_ARG;
   if (n_tokens < 0 || n_tokens > MLORA_MAX_FP8W_TOKENS) return MLORA_ERR_SHAPE;
   if (pool->d_in % 16 != 0) return MLORA_ERR_SHAPE;
@@ -606,7 +658,17 @@ int mlora_linear_fp8w(const void* x, const uint8_t* W_fp8, const float* w_scale,
                                   workspace, workspace_bytes, stream);
     if (st != MLORA_OK) return st;
   }
-  return run_linear(x, W_fp8, pool, sv, n_tokens, lora_on, y, (char*)workspace, stream, w_scale);
+  return run_linear(x, W_fp8, pool, sv, n_tokens, lora_on, y, (char*)workspace, stream, w_scale, epilogue);
+}
+
+int mlora_linear_fp8w(const void* x, const uint8_t* W_fp8, const float* w_scale, mlora_pool_t pool,
+                      const int32_t* seg_start, const int32_t* seg_adapter, const int32_t* seg_rank,
+                      const float* seg_scale, const int32_t* token_index, int n_tokens, int n_seg,
+                      int lora_on, void* y, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+  return mlora_linear_fp8w_epilogue(x, W_fp8, w_scale, pool, seg_start, seg_adapter, seg_rank, seg_scale,
+                                    token_index, n_tokens, n_seg, lora_on, nullptr, y, workspace,
+                                    workspace_bytes, stream);
 }
 
 int mlora_build_segments(const int32_t* token_adapter, const float* adapter_scale, int n_tokens,
@@ -623,11 +685,12 @@ int mlora_build_segments(const int32_t* token_adapter, const float* adapter_scal
   return check_launch();
 }
 
-int mlora_linear_tokens(const void* x, const void* W, mlora_pool_t pool,
-                        const int32_t* token_adapter, const float* adapter_scale, int n_tokens,
-                        int lora_on, void* y, void* workspace, size_t workspace_bytes,
-                        hipStream_t stream) {
+int mlora_linear_tokens_epilogue(const void* x, const void* W, mlora_pool_t pool,
+                                 const int32_t* token_adapter, const float* adapter_scale, int n_tokens,
+                                 int lora_on, const mlora_epilogue_t* epilogue, void* y, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
   if (!pool) return MLORA_ERR_INVALID_ARG;
+  if (const int st = epi_status(epilogue, pool->d_out)) return st;
   if (lora_on != 0 && lora_on != 1) return MLORA_ERR_INVALID_ARG;
   if (n_tokens < 0 || n_tokens > MLORA_MAX_UNSORTED_TOKENS) return MLORA_ERR_SHAPE;
   if (n_tokens == 0) return MLORA_OK;
@@ -658,7 +721,15 @@ int mlora_linear_tokens(const void* x, const void* W, mlora_pool_t pool,
     sv.n_seg_dev = ns;
     sv.n_seg = n_tokens;  // upper bound on the device count
   }
-  return run_linear(x, W, pool, sv, n_tokens, lora_on, y, (char*)workspace, stream);
+  return run_linear(x, W, pool, sv, n_tokens, lora_on, y, (char*)workspace, stream, nullptr, epilogue);
+}
+
+int mlora_linear_tokens(const void* x, const void* W, mlora_pool_t pool,
+                        const int32_t* token_adapter, const float* adapter_scale, int n_tokens,
+                        int lora_on, void* y, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
+  return mlora_linear_tokens_epilogue(x, W, pool, token_adapter, adapter_scale, n_tokens, lora_on, nullptr, y,
+                                      workspace, workspace_bytes, stream);
 }
 
 int mlora_token_map(const int32_t* seg_start, const int32_t* seg_adapter, int n_tokens, int n_seg,

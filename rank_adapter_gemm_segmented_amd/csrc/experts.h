@@ -1,0 +1,82 @@
+// experts.h -- host-side launchers and device-side helpers of the routing and
+// expert kernels (internal to the library).
+#pragma once
+#include "common.h"
+#include "epilogue.h"
+
+namespace mlora {
+
+// ---- routing (kernels_route.hip) ----------------------------------------------
+struct RouteArgs {
+  const void* logits;     // [T, E] bf16 or fp32
+  int T, E, k;
+  int renorm;
+  int32_t* expert;        // [T, k]
+  float* weight;          // [T, k]
+  int32_t* token_index;   // [T k]
+  int32_t* seg_start;     // [E + 1]
+  int32_t* position;      // [T, k]
+  int32_t* hist;          // workspace: slots per expert of every block's tokens [blocks][E]
+  int tpb;                // tokens per block
+};
+size_t route_workspace_bytes(int T, int E);
+void launch_route(const RouteArgs& a, bool bf16, hipStream_t st);
+
+// ---- products per expert (kernels_experts.hip) ----------------------------------
+struct ExpertsArgs {
+  const void* x;                // [n_rows, d_in]
+  const void* W;                // [E, d_out, d_in]
+  const float* w_scale;         // [E, d_out]: W holds e4m3 codes; null: W in x's type
+  void* y;                      // [n_pos, d_y]; fp32 [n_pos, d_out] where f32_out
+  const int32_t* seg_start;     // [E + 1]
+  const int32_t* token_index;   // [n_pos] or null
+  int n_rows, E, d_in, d_out, n_pos;
+  int gated, f32_out;
+  EpiView epi;                  // bias [E, d_out]; no residual
+};
+void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st);
+
+struct CombineArgs {
+  const float* part;            // [n_pos, d_out]
+  const int32_t* position;      // [T, k]
+  const float* weight;          // [T, k]
+  const void* residual;         // [T, d_out] or null
+  void* out;                    // [T, d_out]
+  int T, k, d_out, n_pos;
+};
+void launch_combine(const CombineArgs& a, bool bf16, hipStream_t st);
+
+// Item `item` of a batch cut into runs of at most BT positions per expert:
+// its expert and positions [*p0, *p1), or -1 past the last item. Every wave
+// finds it by itself (64 experts per step: one load pair, a wave scan of the
+// run counts, a ballot), so no barrier precedes the weight loads. Starts are
+// clamped into [0, n_pos]: a lying seg_start drops or repeats positions but
+// never leaves the arrays.
+__device__ __forceinline__ int find_expert(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT, int item,
+                                           int* p0, int* p1) {
+  const int lane = threadIdx.x % kWave;
+  for (int e0 = 0; e0 < E; e0 += kWave) {
+    const int e = min(e0 + lane, E - 1);
+    const int s0 = min(max(seg_start[e], 0), n_pos), s1 = min(max(seg_start[e + 1], 0), n_pos);
+    const int n = e0 + lane < E ? (max(s1 - s0, 0) + BT - 1) / BT : 0;
+    int inc = n;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int up = __shfl_up(inc, off, kWave);
+      if (lane >= off) inc += up;
+    }
+    const unsigned long long m = __ballot(inc > item);
+    if (m) {   // uniform
+      const int l = (int)__builtin_ctzll(m);
+      const int b = __builtin_amdgcn_readlane(s0, l) +
+                    BT * (item - (__builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(n, l)));
+      *p0 = b;
+      *p1 = min(b + BT, __builtin_amdgcn_readlane(s1, l));
+      return e0 + l;
+    }
+    item -= __builtin_amdgcn_readlane(inc, kWave - 1);
+  }
+  return -1;
+}
+
+}  // namespace mlora

@@ -76,7 +76,8 @@ __device__ __forceinline__ u32x4_t e4m3x8_to_bf16x8(uint32_t lo, uint32_t hi) {
 // serve two consecutive k-steps: lane group g = l / 16 of the step pair
 // (2q, 2q + 1) starting at column C takes columns C + 16 g .. + 7 in step 2q
 // and C + 16 g + 8 .. + 15 in step 2q + 1, and reads x at the same columns.
-template <int TT, bool W8>
+// GATED: the items' rows are virtual rows (epilogue.h).
+template <int TT, bool W8, bool GATED>
 __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
   constexpr int NTB = TT / 16;
   constexpr int XP = kDecXPitch;
@@ -163,8 +164,8 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
   const int half_steps = W8 ? (((nks + 1) / 2 + 1) & ~1) : (nks + 1) / 2;
   const int ks_begin = kh ? half_steps : 0;
   const int ks_end = kh ? nks : half_steps;
-  const uint16_t* wrow = W + (long long)min(nrow, d_out - 1) * d_in + k0;
-  const uint8_t* wrow8 = (const uint8_t*)a.W + (long long)min(nrow, d_out - 1) * d_in + k0;
+  const uint16_t* wrow = W + (long long)wrow_of<GATED>(nrow, d_out) * d_in + k0;
+  const uint8_t* wrow8 = (const uint8_t*)a.W + (long long)wrow_of<GATED>(nrow, d_out) * d_in + k0;
   u32x4_t wr[kDecWSteps];
   auto load_w = [&](int s) {
     // steps of the other k-half read the pool's zero block (address select)
@@ -365,8 +366,10 @@ constexpr int kFinUnroll = 8;
 // SL: the pool holds fused adapters over stacked projections (expand only
 // the tile's slice window; a template flag, so plain pools keep a loop that
 // starts at column 0: a run-time start measured 1 us slower)
-template <int TT, bool W8, bool SL>
+// EPI: what follows the layer (kEpiNone: nothing; kEpiPlain, kEpiGated: a.epi).
+template <int TT, bool W8, bool SL, int EPI>
 __global__ __launch_bounds__(256) void k_finish_bf16(DecodeArgs a) {
+  constexpr bool GATED = EPI == kEpiGated;
   constexpr int NTB = TT / 16;
   constexpr int kPre = 2;                // B column groups of 8 prefetched (ranks <= 16)
   const int tile = blockIdx.x / NTB, tb = blockIdx.x % NTB;
@@ -380,7 +383,10 @@ __global__ __launch_bounds__(256) void k_finish_bf16(DecodeArgs a) {
 
   const int t = tb * 16 + (lane % 16);   // this lane's token (sorted position)
   const int tc = min(t, T - 1);
-  const int n = tile * kDecRows + rb * 16 + 4 * (lane / 16);
+  const int nv = tile * kDecRows + rb * 16 + 4 * (lane / 16);   // the lane's 4 rows (virtual when gated)
+  // as rows of W (gated: a run of 4 virtual rows is one of W; runs past the
+  // last feature are not stored)
+  const int n = GATED ? ((nv >> 4) & 1) * (d_out / 2) + gated_feature(nv) : nv;
   int row = a.sv.token_index ? a.sv.token_index[tc] : tc;
   const int4 pe = lora ? a.pos[tc] : make_int4(-1, 0, 0, 0);
 
@@ -414,7 +420,7 @@ __global__ __launch_bounds__(256) void k_finish_bf16(DecodeArgs a) {
     const int ad_ = pe.x, r_ = min(pe.y, a.pv.max_rank);
     const bool live_ = lora && ad_ >= 0 && ad_ < a.pv.capacity && r_ > 0 && t < T;
     int w0 = 0, w1 = r_;
-    if (live_) slice_window(a.pv, tile * kDecRows, min(tile * kDecRows + kDecRows, d_out), r_, &w0, &w1);
+    if (live_ && !GATED) slice_window(a.pv, tile * kDecRows, min(tile * kDecRows + kDecRows, d_out), r_, &w0, &w1);
     int lo = live_ ? (w0 & ~7) : 0x7fffffff, hi = live_ ? min(w1, r_) : 0;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
@@ -458,7 +464,7 @@ __global__ __launch_bounds__(256) void k_finish_bf16(DecodeArgs a) {
   int jb = 0, je = r;
   if constexpr (SL) {
     int w0 = 0, w1 = r;
-    if (live) slice_window(a.pv, tile * kDecRows, min(tile * kDecRows + kDecRows, d_out), r, &w0, &w1);
+    if (live && !GATED) slice_window(a.pv, tile * kDecRows, min(tile * kDecRows + kDecRows, d_out), r, &w0, &w1);
     jb = w0 & ~7;
     je = min(w1, r);
   }
@@ -560,6 +566,56 @@ __global__ __launch_bounds__(256) void k_finish_bf16(DecodeArgs a) {
     }
   }
 
+  if constexpr (EPI != kEpiNone) {
+    // bias, activation, gate and residual in fp32, one rounding. Gated: a
+    // feature's gate row is in an even row block and its up row in the next
+    // one, whose wave hands its sums over through LDS.
+    __shared__ f32x4_t zup[2][kWave];
+    const int d_y = GATED ? d_out / 2 : d_out;
+    const int f = GATED ? gated_feature(nv) : n;         // first of the lane's features
+    if (a.epi.bias) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] += elem_f32<uint16_t>(a.epi.bias, min(n + v, d_out - 1));
+    }
+    if constexpr (GATED) {
+      if (rb & 1) zup[rb / 2][lane] = acc;
+      __syncthreads();
+      if (rb & 1) return;
+    }
+    if (t >= T) return;
+    float o[4] = {acc[0], acc[1], acc[2], acc[3]};
+    activate_n<true>(o, a.epi.act);
+    row = min(max(row, 0), T - 1);
+    const long long at = (long long)row * d_y + f;
+    uint16_t* y = (uint16_t*)a.y;
+    const uint16_t* res = (const uint16_t*)a.epi.residual;
+    const bool vec = f + 3 < d_y && (d_y & 3) == 0;
+    float r4[4] = {0.f, 0.f, 0.f, 0.f};
+    if (res) {
+      if (vec) {
+        const u32x2_t r = *(const u32x2_t*)(res + at);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) r4[v] = __uint_as_float((v & 1) ? (r[v / 2] & 0xffff0000u) : (r[v / 2] << 16));
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) r4[v] = f + v < d_y ? bf16_bits_to_f32(res[at + v]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if constexpr (GATED) o[v] *= zup[rb / 2][lane][v];
+      if (res) o[v] += r4[v];
+    }
+    if (vec) {
+      *(u32x2_t*)(y + at) = u32x2_t{(uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16),
+                                    (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16)};
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (f + v < d_y) y[at + v] = f32_to_bf16_bits(o[v]);
+    }
+    return;
+  }
   if (t >= T) return;
   row = min(max(row, 0), T - 1);
   uint16_t* yr = (uint16_t*)a.y + (long long)row * d_out;
@@ -607,13 +663,20 @@ void decode_plan(int d_in, int d_out, int* n_tiles, int* kc, int* n_chunks) {
   *n_chunks = (d_in + k - 1) / k;
 }
 
+template <int TT, bool W8, int EPI>
+static void launch_decode_epi(const DecodeArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((k_stream_bf16<TT, W8, EPI == kEpiGated>), dim3(a.n_tiles * a.n_chunks), dim3(kDecThreads), 0, st, a);
+  if (a.lora_on && a.pv.n_slices > 0)
+    hipLaunchKernelGGL((k_finish_bf16<TT, W8, true, EPI>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_finish_bf16<TT, W8, false, EPI>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
+}
+
 template <int TT, bool W8>
 static void launch_decode_tt(const DecodeArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_stream_bf16<TT, W8>), dim3(a.n_tiles * a.n_chunks), dim3(kDecThreads), 0, st, a);
-  if (a.lora_on && a.pv.n_slices > 0)
-    hipLaunchKernelGGL((k_finish_bf16<TT, W8, true>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_finish_bf16<TT, W8, false>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
+  if (a.epi_kind == kEpiGated) launch_decode_epi<TT, W8, kEpiGated>(a, st);
+  else if (a.epi_kind == kEpiPlain) launch_decode_epi<TT, W8, kEpiPlain>(a, st);
+  else launch_decode_epi<TT, W8, kEpiNone>(a, st);
 }
 
 void launch_decode_bf16(const DecodeArgs& a, hipStream_t st) {

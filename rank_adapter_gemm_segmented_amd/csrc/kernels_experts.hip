@@ -1,0 +1,254 @@
+// kernels_experts.hip -- products of routed rows with their experts' weights.
+//
+//   y[p] = act(W_e x[row(p)] + b_e)      p in [seg_start[e], seg_start[e + 1])
+//
+// and, for the way back, the fp32 products of every sorted position followed
+// by k_combine: out[t] = residual[t] + sum_j w[t][j] z[position[t][j]].
+//
+// MFMA 16x16 layouts: lane l supplies row l % 16 of either operand; result
+// register v of lane l is row 4 (l / 16) + v, column l % 16. Rows are W rows,
+// columns positions.
+#include <algorithm>
+
+#include "../../include/mlora.h"
+#include "experts.h"
+
+namespace mlora {
+
+__device__ __attribute__((aligned(16))) uint32_t expert_zeros[64];   // read past d_in
+
+__device__ __forceinline__ f32x4_t mfma16e(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+}
+
+// Two e4m3 codes -> two bf16 (exact), as in the decode kernel.
+template <bool HI>
+__device__ __forceinline__ uint32_t e4m3x2_bf16(uint32_t w) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  bf16x2_t r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI);
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ u32x4_t e4m3x8_bf16(uint32_t lo, uint32_t hi) {
+  return u32x4_t{e4m3x2_bf16<false>(lo), e4m3x2_bf16<true>(lo), e4m3x2_bf16<false>(hi), e4m3x2_bf16<true>(hi)};
+}
+
+constexpr int kXBf16 = 0, kXFp8w = 1, kXF32 = 2;   // element types of the streaming kernel
+
+// ---------------------------------------------------------------------------
+// Streaming form, every type: an item is 16 NR (virtual) rows of one expert by
+// up to 16 NTB of its positions, over the whole of d_in. The 8 waves split d_in
+// in units of 128 bytes of a W row (wave w takes units w, w + 8, ...), load W
+// and x straight into MFMA operand registers, and their sums are added in wave
+// order through LDS. W is read once where an expert has at most 16 NTB rows.
+//
+// A unit is two 16-byte loads per row block: lane group g = l / 16 takes bytes
+// 16 g and 64 + 16 g, so a row's 128-byte line is whole within the unit. bf16:
+// a load is one 32-column MFMA operand; FP8: 16 columns, two operands (columns
+// 16 g and 16 g + 8 of the 64); fp32: 4 columns, four 16x16x4 products.
+// ---------------------------------------------------------------------------
+constexpr int kGridY = 32768;   // runs per grid row (y is limited; z takes the rest)
+constexpr int kXsThreads = 512, kXsWaves = kXsThreads / kWave;
+
+template <int TYPE, int NR, int NTB, bool GATED>
+__global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
+  constexpr int EB = TYPE == kXFp8w ? 1 : TYPE == kXF32 ? 4 : 2;   // bytes per W element
+  constexpr int XB = TYPE == kXF32 ? 4 : 2;                        // and per x element
+  constexpr int UC = 128 / EB;                                     // columns per unit
+  constexpr int XL = XB / EB;                                      // x loads per W load
+  __shared__ f32x4_t red[kXsWaves][NR * NTB][kWave];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int l16 = lane % 16, g = lane / 16;
+  const int rt = blockIdx.x;
+  int p0, p1;
+  const int e = find_expert(a.seg_start, a.E, a.n_pos, 16 * NTB, (int)(blockIdx.y + blockIdx.z * kGridY), &p0, &p1);
+  if (e < 0) return;   // uniform: past the last item
+  const int d_in = a.d_in, d_out = a.d_out;
+  const int v0 = rt * 16 * NR;                                     // first (virtual) row
+  auto wrow = [&](int v) { return (long long)e * d_out + wrow_of<GATED>(v, d_out); };
+
+  const char* wp[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) wp[r] = (const char*)a.W + wrow(v0 + 16 * r + l16) * d_in * EB + 16 * g;
+  const char* xp[NTB];
+#pragma unroll
+  for (int t = 0; t < NTB; ++t) {
+    const int p = min(p0 + 16 * t + l16, p1 - 1);                  // (absent positions repeat the last)
+    const int row = a.token_index ? a.token_index[p] : p;
+    xp[t] = (const char*)a.x + (long long)min(max(row, 0), a.n_rows - 1) * d_in * XB + 16 * XL * g;
+  }
+  const char* zeros = (const char*)expert_zeros;
+
+  f32x4_t acc[NR][NTB];
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int t = 0; t < NTB; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  const int nu = (d_in + UC - 1) / UC;
+  for (int u = wave; u < nu; u += kXsWaves) {
+    u32x4_t w[2][NR], x[2][XL][NTB];
+    const int c0 = u * UC;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + h * UC / 2;                               // first column of the load, group 0
+      const bool in = c + 16 / EB * g < d_in;                      // (d_in is a multiple of 16 bytes of W)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) w[h][r] = ld_nt16(sel_addr(in, wp[r] + (long long)c * EB, zeros));
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+#pragma unroll
+        for (int t = 0; t < NTB; ++t) x[h][i][t] = ld16(sel_addr(in, xp[t] + (long long)c * XB + 16 * i, zeros));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int t = 0; t < NTB; ++t) {
+          if constexpr (TYPE == kXBf16) {
+            acc[r][t] = mfma16e(w[h][r], x[h][0][t], acc[r][t]);
+          } else if constexpr (TYPE == kXFp8w) {
+            acc[r][t] = mfma16e(e4m3x8_bf16(w[h][r].x, w[h][r].y), x[h][0][t], acc[r][t]);
+            acc[r][t] = mfma16e(e4m3x8_bf16(w[h][r].z, w[h][r].w), x[h][XL - 1][t], acc[r][t]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[h][r][i]), __uint_as_float(x[h][0][t][i]),
+                                                               acc[r][t], 0, 0, 0);
+          }
+        }
+  }
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int t = 0; t < NTB; ++t) red[wave][r * NTB + t][lane] = acc[r][t];
+  __syncthreads();
+
+  // sums in wave order, then the epilogue: a thread takes 4 consecutive rows
+  // of one position (gated: the gate rows and the up rows of 4 features)
+  constexpr int NB = GATED ? NR / 2 : NR;                          // row blocks of features
+  const int d_y = GATED ? d_out / 2 : d_out;
+  for (int q = tid; q < NB * NTB * kWave; q += kXsThreads) {
+    const int ql = q % kWave, t = (q / kWave) % NTB, b = q / kWave / NTB;
+    const int p = p0 + 16 * t + ql % 16;
+    const int f = (GATED ? v0 / 2 : v0) + 16 * b + 4 * (ql / 16);  // first feature
+    if (p >= p1 || f >= d_y) continue;
+    auto sum = [&](int r, float* z) {                              // row block r
+      f32x4_t s = red[0][r * NTB + t][ql];
+#pragma unroll
+      for (int w = 1; w < kXsWaves; ++w)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) s[v] += red[w][r * NTB + t][ql][v];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const long long n = wrow(v0 + 16 * r + 4 * (ql / 16) + v);
+        z[v] = s[v];
+        if constexpr (TYPE == kXFp8w) z[v] *= a.w_scale[n];
+        if (a.epi.bias) z[v] += TYPE == kXF32 ? elem_f32<float>(a.epi.bias, n) : elem_f32<uint16_t>(a.epi.bias, n);
+      }
+    };
+    float o[4];
+    sum(GATED ? 2 * b : b, o);
+    activate_n<TYPE != kXF32>(o, a.epi.act);
+    if constexpr (GATED) {
+      float u[4];
+      sum(2 * b + 1, u);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) o[v] *= u[v];
+    }
+    const long long at = (long long)p * d_y + f;
+    const bool vec = d_y % 4 == 0;
+    if (TYPE == kXF32 || a.f32_out) {
+      float* y = (float*)a.y + at;
+      if (vec) *(f32x4_t*)y = f32x4_t{o[0], o[1], o[2], o[3]};
+      else
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (f + v < d_y) y[v] = o[v];
+    } else {
+      uint16_t* y = (uint16_t*)a.y + at;
+      if (vec)
+        *(u32x2_t*)y = u32x2_t{(uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16),
+                               (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16)};
+      else
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (f + v < d_y) y[v] = f32_to_bf16_bits(o[v]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Way back: a token's rows weighted, summed in slot order and added to the
+// residual, in fp32, one rounding. A thread takes 4 columns of one token.
+// ---------------------------------------------------------------------------
+template <typename E_>
+__global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
+  const int t = blockIdx.x, c = 4 * (blockIdx.y * 256 + threadIdx.x);
+  if (c >= a.d_out) return;
+  const bool vec = a.d_out % 4 == 0;
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  const long long at = (long long)t * a.d_out + c;
+  for (int j = 0; j < a.k; ++j) {
+    const int p = a.position[(long long)t * a.k + j];
+    const float w = a.weight[(long long)t * a.k + j];
+    if (p < 0 || p >= a.n_pos) continue;   // uniform: no expert in this slot
+    const float* z = a.part + (long long)p * a.d_out + c;
+    if (vec) {
+      const f32x4_t v = *(const f32x4_t*)z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(w, v[i], o[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < a.d_out) o[i] = fmaf(w, z[i], o[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + i < a.d_out) {
+      if (a.residual) o[i] += elem_f32<E_>(a.residual, at + i);
+      if constexpr (sizeof(E_) == 2) ((uint16_t*)a.out)[at + i] = f32_to_bf16_bits(o[i]);
+      else ((float*)a.out)[at + i] = o[i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// Items of a batch cut into runs of BT positions per expert, at most.
+static long long run_bound(const ExpertsArgs& a, int BT) {
+  return (long long)a.n_pos / BT + (a.E < a.n_pos ? a.E : a.n_pos);
+}
+
+template <int TYPE, int NR, int NTB>
+static void launch_stream_n(ExpertsArgs a, hipStream_t st) {
+  const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  const long long runs = run_bound(a, 16 * NTB);
+  const dim3 grid((rows + 16 * NR - 1) / (16 * NR), (unsigned)std::min<long long>(runs, kGridY), (unsigned)((runs + kGridY - 1) / kGridY));
+  if (a.gated) hipLaunchKernelGGL((k_experts_stream<TYPE, NR, NTB, true>), grid, dim3(kXsThreads), 0, st, a);
+  else hipLaunchKernelGGL((k_experts_stream<TYPE, NR, NTB, false>), grid, dim3(kXsThreads), 0, st, a);
+}
+
+template <int TYPE>
+static void launch_stream(const ExpertsArgs& a, hipStream_t st) {
+  const int active = a.E < a.n_pos ? a.E : a.n_pos;
+  if (a.n_pos <= 8 * active) launch_stream_n<TYPE, 4, 1>(a, st);
+  else if (a.n_pos <= 24 * active) launch_stream_n<TYPE, 4, 2>(a, st);
+  else launch_stream_n<TYPE, 4, 4>(a, st);
+}
+
+void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st) {
+  if (a.n_pos <= 0) return;
+  if (!bf16) launch_stream<kXF32>(a, st);
+  else if (a.w_scale) launch_stream<kXFp8w>(a, st);
+  else launch_stream<kXBf16>(a, st);
+}
+
+void launch_combine(const CombineArgs& a, bool bf16, hipStream_t st) {
+  const dim3 grid(a.T, (a.d_out + 1023) / 1024);
+  if (bf16) hipLaunchKernelGGL(k_combine<uint16_t>, grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(k_combine<float>, grid, dim3(256), 0, st, a);
+}
+
+}  // namespace mlora

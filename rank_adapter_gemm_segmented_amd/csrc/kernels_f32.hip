@@ -80,13 +80,21 @@ __global__ __launch_bounds__(256) void k_shrink_f32(LinearArgs a) {
 constexpr int kF32KB = 256;
 constexpr int kF32Feat = 16;
 
+// EPI: what follows the layer. Gated: the 16 rows are 8 features' gate rows,
+// then their up rows, so thread tx + 8 holds the up value of thread tx.
+template <int EPI>
 __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
+  constexpr bool GATED = EPI == kEpiGated;
   __shared__ float Ws[kF32Feat][kF32KB + 1];
   __shared__ float Xs[16][kF32KB + 1];
   const int tid = threadIdx.x;
   const int tx = tid % kF32Feat, ty = tid / kF32Feat;
   const int n0 = blockIdx.x * kF32Feat, p0 = blockIdx.y * 16;
   const int T = a.T, d_in = a.d_in, d_out = a.d_out;
+  // row of W of the tile's row i; rows past the last one are clamped to it
+  auto wrow = [&](int i) {
+    return GATED ? (i >> 3) * (d_out / 2) + min(n0 / 2 + (i & 7), d_out / 2 - 1) : min(n0 + i, d_out - 1);
+  };
   const float* __restrict__ x = (const float*)a.x;
   const float* __restrict__ W = (const float*)a.W;
   float acc = 0.f;
@@ -101,7 +109,7 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
     const int q = tid + 256 * i;
     lr_[i] = q / (kF32KB / 4);
     lc_[i] = 4 * (q % (kF32KB / 4));
-    wsrc[i] = W + (long long)min(n0 + lr_[i], d_out - 1) * d_in + lc_[i];
+    wsrc[i] = W + (long long)wrow(lr_[i]) * d_in + lc_[i];
     int xrow = min(p0 + lr_[i], T - 1);
     if (a.sv.token_index) xrow = min(max(a.sv.token_index[xrow], 0), T - 1);
     xsrc[i] = x + (long long)xrow * d_in + lc_[i];
@@ -114,7 +122,7 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
   auto load = [&](int kb) {
 #pragma unroll
     for (int i = 0; i < N4; ++i) {
-      const bool wok = n0 + lr_[i] < d_out && kb + lc_[i] < d_in;
+      const bool wok = (GATED || n0 + lr_[i] < d_out) && kb + lc_[i] < d_in;
       wreg[i] = wok ? *(const f32x4_t*)(wsrc[i] + kb) : f32x4_t{0.f, 0.f, 0.f, 0.f};
       const bool xok = p0 + lr_[i] < T && kb + lc_[i] < d_in;
       xreg[i] = xok ? *(const f32x4_t*)(xsrc[i] + kb) : f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -135,29 +143,49 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
     for (int kk = 0; kk < kF32KB; ++kk) acc = fmaf(Ws[tx][kk], Xs[ty][kk], acc);
     __syncthreads();
   }
-  const int n = n0 + tx;
-  if (n >= d_out || p >= T) return;
+  const int n = GATED ? wrow(tx) : n0 + tx;
+  if (!GATED && (n >= d_out || p >= T)) return;
   const SegView& sv = a.sv;
   float val = acc;
   const int ad = pe4.y, r = min(pe4.z, a.pv.max_rank);
   if (a.lora_on && ad >= 0 && ad < a.pv.capacity && r > 0) {
     const float* Bb = (const float*)a.pv.base + (long long)ad * a.pv.slot_elems + a.pv.b_offset;
     const float* bn = Bb + (long long)n * round_up8(r);
-    const float* vp = a.v_part + (long long)p * a.r_ws;
+    const float* vp = a.v_part + (long long)(GATED ? min(p, T - 1) : p) * a.r_ws;
     float lora = 0.f;
     for (int j = 0; j < r; ++j) lora = fmaf(bn[j], vp[j], lora);
     val = fmaf(__int_as_float(pe4.w), lora, val);
   }
+  int f = n, d_y = d_out;                 // y's column and width
+  if constexpr (EPI != kEpiNone) {
+    if (a.epi.bias) val += elem_f32<float>(a.epi.bias, n);
+    if constexpr (GATED) {
+      const float up = __shfl(val, (threadIdx.x % kWave) + 8, kWave);   // (tx >= 8: unused)
+      d_y = d_out / 2;
+      f = n0 / 2 + tx;
+      if (tx >= 8 || f >= d_y || p >= T) return;
+      val = activate<false>(val, a.epi.act) * up;
+    } else {
+      val = activate<false>(val, a.epi.act);
+    }
+  }
   int row = sv.token_index ? sv.token_index[p] : p;
   row = min(max(row, 0), T - 1);
-  ((float*)a.y)[(long long)row * d_out + n] = val;
+  const long long at = (long long)row * d_y + f;
+  if constexpr (EPI != kEpiNone) {
+    if (a.epi.residual) val += elem_f32<float>(a.epi.residual, at);
+  }
+  ((float*)a.y)[at] = val;
 }
 
 void launch_linear_f32(const LinearArgs& a, hipStream_t st) {
   if (a.lora_on && a.seg_grid > 0)
     hipLaunchKernelGGL(k_shrink_f32, dim3(a.seg_grid), dim3(256), 0, st, a);
-  dim3 grid((a.d_out + kF32Feat - 1) / kF32Feat, (a.T + 15) / 16);
-  hipLaunchKernelGGL(k_gemm_f32, grid, dim3(256), 0, st, a);
+  const int rows = a.epi_kind == kEpiGated ? gated_rows(a.d_out) : a.d_out;
+  dim3 grid((rows + kF32Feat - 1) / kF32Feat, (a.T + 15) / 16);
+  if (a.epi_kind == kEpiGated) hipLaunchKernelGGL(k_gemm_f32<kEpiGated>, grid, dim3(256), 0, st, a);
+  else if (a.epi_kind == kEpiPlain) hipLaunchKernelGGL(k_gemm_f32<kEpiPlain>, grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(k_gemm_f32<kEpiNone>, grid, dim3(256), 0, st, a);
 }
 
 }  // namespace mlora

@@ -29,15 +29,13 @@
 #include <type_traits>
 
 #include "common.h"
+#include "gemm_tile.h"
 #include "launch.h"
 
 namespace mlora {
 
 __device__ __forceinline__ f32x4_t mfma16g(u32x4_t a, u32x4_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16_t mfma32g(u32x4_t a, u32x4_t b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -671,106 +669,16 @@ constexpr int kBatch = 8;           // independent loads per thread in bulk LDS 
 constexpr int kEpiRing = 16;        // B operand loads in flight per lane in the expand epilogue
 constexpr int kEpiMaxUnits = 128;   // work units one wave lists per rank chunk (more: further passes)
 
-// LDS address (byte offset in the workgroup's LDS) of a pointer into __shared__ memory
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-
-// Direct global -> LDS load (gfx950 LDS DMA): the wave's 64 lanes each fetch
-// 16 bytes from their own global address and the data lands in LDS, lane l at
-// byte m0 + 16 l, without passing through registers. Issued as inline
-// assembly so that the compiler, which would otherwise wait for every
-// outstanding DMA before any LDS read, leaves the waits to the stage ring
-// below. One wait state separates the M0 write from its use.
-__device__ __forceinline__ void dma16(const void* g, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(m0)
-               : "memory", "m0");
-}
-
-// Wait until at most N of this wave's vector memory operations are in flight,
-// then a workgroup barrier (LDS and scalar counters drained too; nothing else).
-// The same load marked nontemporal, for W rows that the launch reads once
-// (at most two position tiles, which run in the same round): measured on the
-// verify and heterogeneous batches, their LoRA-off passes took 1-2 us less
-// (45.2-46.3 against 47.3-47.8 us, 38.0 against 39.1 us). Where more position
-// tiles re-read a W panel in later rounds (prefill) the mark lost about 10%
-// (gate/up), and the positions' rows, re-read by every row tile, lost 5-18%.
-__device__ __forceinline__ void dma16_nt(const void* g, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(g), "s"(m0)
-               : "memory", "m0");
-}
-
-template <int N>
-__device__ __forceinline__ void vm_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// KB: k per stage (32 or 64). A stage is the tile's BR W rows and its BT
-// positions over KB columns. The stages reach LDS by direct loads into two
-// rings, one for the W rows (NB slots, NB - 1 stages in flight while one is
-// multiplied) and one for the positions (NX slots, NX - 1 in flight). Rows
-// are 2 KB bytes (KB bf16), unpadded, and 16-byte chunk c of row r sits in slot
-// c ^ gswz(r) of the row, so the rows read together by one fragment load fall
-// in distinct LDS banks.
-template <int BR, int BT, int WR, int WT, int NB, int KB, int NX>
-struct GCfg {
-  static constexpr int NWR = BR / WR, NWT = BT / WT;
-  static constexpr int NW = NWR * NWT;
-  static constexpr int NT = NW * kWave;
-  static constexpr int MR = WR / 32, MT = WT / 32;        // 32x32 blocks per wave
-  static constexpr int RB = 2 * KB;                        // bytes per LDS row
-  static constexpr int WSTAGE_B = BR * RB, XSTAGE_B = BT * RB;   // ring slots
-  static constexpr int DPW_W = BR * 2 * KB / 1024 / NW;    // 1 KB loads per wave per stage: W rows
-  static constexpr int DPW_X = BT * 2 * KB / 1024 / NW;    // and positions
-  static constexpr int DPW = DPW_W + DPW_X;
-  static constexpr int XRING = NB * WSTAGE_B;              // byte offset of the position ring
-  static constexpr int MAIN_BYTES = NB * WSTAGE_B + NX * XSTAGE_B;
-  // DMAs a wave has issued after stage st's position DMAs when stage st is
-  // multiplied (its W DMAs were issued earlier still)
-  static constexpr int VMC = (NX - 2) * DPW;
-  // small row tiles get extra LDS so the epilogue stages many segment runs at
-  // once; the y tile of the store passes through the same LDS
-  static constexpr int YT_BYTES = NW * WT * (2 * WR + 16);
-  static constexpr int LDS_BYTES0 = MAIN_BYTES > 96 * 1024 ? MAIN_BYTES : 96 * 1024;
-  static constexpr int LDS_BYTES = LDS_BYTES0 > YT_BYTES ? LDS_BYTES0 : YT_BYTES;
-  static_assert(KB == 32 || KB == 64, "stage depth");
-  static_assert((BR * 2 * KB) % (1024 * NW) == 0 && (BT * 2 * KB) % (1024 * NW) == 0,
-                "each ring's stage splits into whole loads per wave");
-  static_assert(NB >= 2 && NX >= 2 && NB >= NX && VMC <= 63, "ring depths and vmcnt range");
-};
-
-// Slot permutation of row r (depends on r mod 16 only). A fragment read has
-// lane l take row l % 32 at one chunk. gfx950 serves a 16-byte LDS read 16
-// lanes (256 bytes) at a time, so the 16 rows of a lane group must land on
-// 16 distinct 16-byte bank groups modulo 256 bytes. KB = 64: two rows per
-// 256 bytes; rows of equal parity take distinct slots through r >> 1, and
-// the parity flips the slot's top bit. KB = 32: four rows per 256 bytes,
-// separated through r >> 2. Both were checked with the LDS bank-conflict
-// counter on a read-pattern probe (no conflicts), where the plain r & 7 and
-// (r >> 1) & 3 permutations conflicted two ways.
-template <int KB>
-__device__ __forceinline__ int gswz(int r) {
-  return KB == 64 ? (((r >> 1) ^ ((r & 1) << 2)) & 7) : ((r >> 2) & 3);
-}
-
-// Scheduling hint for one k-step: the R fragment reads of the next k-step
-// spread over the M MFMAs of this one (one read, then its share of MFMAs).
-template <int R, int M, int J = 0>
-__device__ __forceinline__ void sched_reads_over_mfma() {
-  if constexpr (J < R) {
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                          // DS read
-    __builtin_amdgcn_sched_group_barrier(0x008, M * (J + 1) / R - M * J / R, 0);  // MFMA
-    sched_reads_over_mfma<R, M, J + 1>();
-  }
-}
-
 // One workgroup per CU (the LDS stages take most of it): the register
 // allocator may then use the whole register file share of its waves (one
 // wave per SIMD for 4 waves, two for 8).
-template <int BR, int BT, int WR, int WT, int NB, int KB, int NX>
+// EPI: kEpiNone stores the layer's result; kEpiPlain and kEpiGated apply
+// a.epi to it first (epilogue.h; gated: the tile's rows are virtual rows).
+template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, int EPI>
 __global__ __launch_bounds__((BR / WR) * (BT / WT) * kWave)
 __attribute__((amdgpu_waves_per_eu((BR / WR) * (BT / WT) / 4, (BR / WR) * (BT / WT) / 4)))
 void k_gemm2(LinearArgs a) {
+  constexpr bool GATED = EPI == kEpiGated;
   using C = GCfg<BR, BT, WR, WT, NB, KB, NX>;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[C::LDS_BYTES / 2];
   __shared__ int4 pinfo[BT];
@@ -779,7 +687,7 @@ void k_gemm2(LinearArgs a) {
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int l32 = lane % 32, kh = 8 * (lane / 32);
   const int T = a.T, d_in = a.d_in, d_out = a.d_out;
-  const int n_rt = (d_out + BR - 1) / BR;
+  const int n_rt = ((GATED ? gated_rows(d_out) : d_out) + BR - 1) / BR;
   // Block order. One round of blocks (a block per CU or fewer): row tiles
   // fastest, so the position tiles of one row tile (n_rt apart, on the same
   // XCD when n_rt % 8 == 0) run together and share that row tile's W in one
@@ -825,7 +733,7 @@ void k_gemm2(LinearArgs a) {
     if (i >= C::DPW_W) r += BR;   // a row of the position slot
     scol[i] = c * 8;
     if (r < BR) {
-      src[i] = W + (long long)min(r0 + r, d_out - 1) * d_in + c * 8;
+      src[i] = W + (long long)wrow_of<GATED>(r0 + r, d_out) * d_in + c * 8;
     } else {
       const int p = min(t0 + r - BR, T - 1);
       int row = a.sv.token_index ? a.sv.token_index[p] : p;
@@ -933,12 +841,17 @@ void k_gemm2(LinearArgs a) {
   // Tiles whose y tile fits the LDS in fp32 add the term while storing y
   // (kDeltaTile, below), where consecutive lanes read consecutive rows of one
   // position; the others add it here, from per-lane 16-byte pieces.
-  constexpr bool kDeltaTile = C::NW * WT * (4 * WR + 16) <= C::LDS_BYTES;
+  // (With an epilogue every tile adds it here.)
+  constexpr bool kDeltaTile = EPI == kEpiNone && C::NW * WT * (4 * WR + 16) <= C::LDS_BYTES;
   constexpr bool kDeltaEarly = !kDeltaTile && C::MR * C::MT <= 4;
   const bool use_delta = a.lora_on && a.delta != nullptr;
   auto delta_ptr = [&](int n, int m, int q) {
     const int p = min(t0 + wt * WT + n * 32 + l32, T - 1);
-    return a.delta + (long long)p * d_out + min(r0 + wr * WR + m * 32 + 8 * q + 4 * (lane / 32), d_out - 4);
+    const int v = r0 + wr * WR + m * 32 + 8 * q + 4 * (lane / 32);
+    // (gated: 4 virtual rows of one half are 4 rows of W, d_out / 2 being a
+    // multiple of 4 where the dense term is used)
+    const int n4 = GATED ? ((v >> 4) & 1) * (d_out / 2) + gated_feature(v) : v;
+    return a.delta + (long long)p * d_out + min(n4, d_out - 4);
   };
   f32x4_t dpre[kDeltaEarly ? C::MT : 1][kDeltaEarly ? C::MR : 1][4];
   if constexpr (kDeltaEarly) {
@@ -1071,7 +984,8 @@ void k_gemm2(LinearArgs a) {
           re = wstart[wave][k + 1];
           const int4 pi = pinfo[rs];
           int w0 = 0, w1 = pi.z;
-          if (pi.y >= 0) slice_window(a.pv, wr0, wr1, pi.z, &w0, &w1);
+          // (gated: the wave's rows lie in every slice)
+          if (pi.y >= 0 && !GATED) slice_window(a.pv, wr0, wr1, pi.z, &w0, &w1);
           lo = max(w0 - jc0, 0) & ~15;
           const int hi = pi.y >= 0 ? min(min(w1, pi.z) - jc0, rc) : 0;
           cnt = hi > lo ? (hi - lo + 15) / 16 : 0;
@@ -1118,7 +1032,7 @@ void k_gemm2(LinearArgs a) {
         // ring overlapped nothing.)
 #pragma unroll
         for (int m = 0; m < C::MR; ++m) {
-          const int row = min(rowb + m * 32 + l32, d_out - 1);
+          const int row = wrow_of<GATED>(rowb + m * 32 + l32, d_out);
           // (nontemporal: a unit's B rows are read by this workgroup alone;
           // the verify pass's LoRA-on call took 3 us less, same bits)
           ring[slot][m] = ld_nt16(sel_addr(live && col < d.w, sb + (long long)row * 16 + kh, zeros));
@@ -1185,6 +1099,11 @@ void k_gemm2(LinearArgs a) {
   constexpr int CPR = WR / 8;                           // 16-byte pieces per row
   static_assert(C::NW * WT * YP <= C::LDS_BYTES, "y tile fits the LDS");
   if (a.lora_on && !a.delta) __syncthreads();          // the expand's LDS reads are done
+  if constexpr (EPI != kEpiNone) {
+    auto row_of = [&](int p) { return a.sv.token_index ? min(max(a.sv.token_index[p], 0), T - 1) : p; };
+    store_epilogue<C, GATED>(acc, (char*)lds, wave, lane, r0 + wr * WR, t0 + wt * WT, T, d_out, a.epi, a.y, row_of);
+    return;
+  }
   uint16_t* __restrict__ y = (uint16_t*)a.y;
   if constexpr (kDeltaTile) {
     if (use_delta) {
@@ -1306,13 +1225,19 @@ int shrink_items_bound(int T, int n_seg_bound, int max_rank) {
 // rounds and read W twice.
 template <int BR, int BT, int WR, int WT, int NB, int KB, int NX>
 static void launch_g(const LinearArgs& a, hipStream_t st, bool grouped_order) {
-  const int n_rt = (a.d_out + BR - 1) / BR, n_tt = (a.T + BT - 1) / BT;
+  const int n_rt = ((a.epi_kind == kEpiGated ? gated_rows(a.d_out) : a.d_out) + BR - 1) / BR;
+  const int n_tt = (a.T + BT - 1) / BT;
   LinearArgs g = a;
   g.gorder = grouped_order && n_tt > 1 && n_rt % 8 == 0 && (long long)n_rt * n_tt > 256;
   if (BR == 256 && n_rt % 4 == 0 && n_tt % 2 == 0 && (long long)n_rt * n_tt <= 256) g.gorder = 2;
   g.wnt = n_tt <= 2;
-  hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX>), dim3(n_rt * n_tt),
-                     dim3(GCfg<BR, BT, WR, WT, NB, KB, NX>::NT), 0, st, g);
+  const dim3 grid(n_rt * n_tt), block(GCfg<BR, BT, WR, WT, NB, KB, NX>::NT);
+  if (a.epi_kind == kEpiGated)
+    hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiGated>), grid, block, 0, st, g);
+  else if (a.epi_kind == kEpiPlain)
+    hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiPlain>), grid, block, 0, st, g);
+  else
+    hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiNone>), grid, block, 0, st, g);
 }
 
 // MLORA_FORCE_SHRINK=mfma keeps the MFMA shrink on short segments too.

@@ -6,6 +6,7 @@
 
 #include "../../include/mlora.h"
 #include "common.h"
+#include "epilogue.h"
 
 namespace mlora {
 
@@ -29,7 +30,12 @@ struct LinearArgs {
                    // 1 XCD-grouped (row tiles per XCD, their position tiles adjacent),
                    // 2 one round in 2-D blocks per XCD (n_rt / 4 x n_tt / 2 tiles)
   int wnt;         // tiled GEMM: stage W rows by nontemporal loads (set by its launcher)
+  // what follows the layer: kEpiNone (nothing; epi is not read), kEpiPlain or kEpiGated
+  int epi_kind;
+  EpiView epi;
 };
+
+constexpr int kEpiNone = 0, kEpiPlain = 1, kEpiGated = 2;
 
 constexpr int kMaxShrinkSplit = 16;
 constexpr int kMaxRankWs = 256;   // largest v row pitch (max_rank rounded up to 16)
@@ -58,6 +64,8 @@ struct DecodeArgs {
   int n_chunks;    // ceil(d_in / kc)
   int unit_rows;   // rank rows per shrink unit (4, 8 or 16)
   const float* w_scale;   // FP8 weight: float32 scale per W row (W holds e4m3 codes); null: bf16 W
+  int epi_kind;           // as in LinearArgs
+  EpiView epi;
 };
 
 // Merge of one adapter into a base weight: W_out = W_in + scale * B A.
