@@ -1,6 +1,8 @@
 // gemm_tile.h -- tiles of the bf16 GEMM kernels: LDS rings fed by direct global
 // -> LDS loads, their layout, and the main loop of the largest tile.
 #pragma once
+#include <utility>
+
 #include "common.h"
 #include "epilogue.h"
 
@@ -53,6 +55,7 @@ __device__ __forceinline__ void vm_barrier() {
 // in distinct LDS banks.
 template <int BR, int BT, int WR, int WT, int NB, int KB, int NX>
 struct GCfg {
+  static constexpr int kBR = BR, kBT = BT, kWR = WR, kWT = WT, kNB = NB, kKB = KB, kNX = NX;
   static constexpr int NWR = BR / WR, NWT = BT / WT;
   static constexpr int NW = NWR * NWT;
   static constexpr int NT = NW * kWave;
@@ -101,6 +104,192 @@ __device__ __forceinline__ void sched_reads_over_mfma() {
     __builtin_amdgcn_sched_group_barrier(0x008, M * (J + 1) / R - M * J / R, 0);  // MFMA
     sched_reads_over_mfma<R, M, J + 1>();
   }
+}
+
+// The rows a wave loads: per stage DPW_W loads of the W ring and DPW_X of the
+// position ring. Load i < DPW_W of wave w fills the W slot's 1 KB chunk
+// J = i NW + w, load DPW_W + i the position slot's chunk J; lane l writes byte
+// 1024 J + 16 l of the slot, i.e. row r, slot l % (KB / 8), and so fetches chunk
+// (slot ^ gswz(r)) of that row. wrow(r) and xrow(r) give the address of the
+// tile's r-th W row and position.
+template <class C>
+struct TileSrc {
+  const uint16_t* src[C::DPW];
+  int scol[C::DPW];
+  template <class WRow, class XRow>
+  __device__ __forceinline__ void set(int wave, int lane, WRow wrow, XRow xrow) {
+#pragma unroll
+    for (int i = 0; i < C::DPW; ++i) {
+      const bool isx = i >= C::DPW_W;
+      const int J = (isx ? i - C::DPW_W : i) * C::NW + wave;
+      const int r = J * (1024 / (2 * C::kKB)) + lane / (C::kKB / 8);
+      scol[i] = ((lane % (C::kKB / 8)) ^ gswz<C::kKB>(r)) * 8;
+      src[i] = (isx ? xrow(r) : wrow(r)) + scol[i];
+    }
+  }
+  // load I of stage st (W rows for I < DPW_W, else positions) into the ring;
+  // columns past d_in read `zeros`, so that every stage has the same count
+  template <int I, bool NT>
+  __device__ __forceinline__ void issue(int st, uint32_t lds0, int wave, int d_in, const void* zeros) const {
+    constexpr bool isx = I >= C::DPW_W;
+    constexpr int j = isx ? I - C::DPW_W : I;
+    const uint32_t slot = isx ? lds0 + C::XRING + (uint32_t)(st % C::kNX) * C::XSTAGE_B
+                              : lds0 + (uint32_t)(st % C::kNB) * C::WSTAGE_B;
+    const uint32_t at = slot + (uint32_t)(j * C::NW + wave) * 1024;
+    const int k0 = st * C::kKB;
+    const void* g = sel_addr(k0 + scol[I] < d_in, src[I] + k0, zeros);
+    if (NT && !isx) dma16_nt(g, at);
+    else dma16(g, at);
+  }
+};
+
+// Main loop of the largest tile: 4 waves, one per SIMD, each 128 x 128 of a 256
+// x 256 tile. A SIMD then has no second wave to cover a barrier or an LDS read
+// with, so the loop is laid out by hand: MFMA by MFMA, with the reads of the
+// next k-step's fragments and the loads of later stages placed between them.
+//
+// Why so large: a wave tile of 128 x 64 reads 6 KB of fragments for 8 MFMAs of
+// 32 cycles, which with the ring's writes is the CU's 128 bytes of LDS per
+// cycle; 128 x 128 reads 8 KB for 16, three quarters of it.
+//
+// The stage boundary lies inside a k-step: when the last k-step's first H MFMAs
+// have issued, every fragment of the stage is in registers, the wave waits
+// for its own loads of the next stage, and past the barrier the next stage is
+// whole and this one's slots are free. The loads of later stages and the first
+// fragments of the next stage then go out under the remaining MFMAs.
+template <class C>
+__device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, const void* zeros, char* lds,
+                                              int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
+  constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = KB / 16;
+  constexpr int MR = C::MR, MT = C::MT, NM = MR * MT, NF = MR + MT;
+  constexpr int H = NM / 4;
+  static_assert(KS % 2 == 0, "fragment sets alternate within a stage");
+  const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  int fcol[KS];
+#pragma unroll
+  for (int kk = 0; kk < KS; ++kk) fcol[kk] = ((kk * 2 + kh) ^ gswz<KB>(l32)) * 16;
+  const int wbase = (wr * C::kWR + l32) * C::RB, xbase = C::XRING + (wt * C::kWT + l32) * C::RB;
+
+  u32x4_t fa[2][MR], fb[2][MT];
+  // fragment f of k-step kk: the first MFMAs' operands first (W 0, positions 0 .. MT - 1, W 1 ..)
+  auto frag = [&](int st, int kk, int set, int f) {
+    if (f == 0 || f > MT) {
+      const int m = f == 0 ? 0 : f - MT;
+      fa[set][m] = *(const u32x4_t*)(lds + (st % NB) * C::WSTAGE_B + wbase + m * 32 * C::RB + fcol[kk]);
+    } else {
+      fb[set][f - 1] = *(const u32x4_t*)(lds + (st % NX) * C::XSTAGE_B + xbase + (f - 1) * 32 * C::RB + fcol[kk]);
+    }
+  };
+  auto load_w = [&](int st) {
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I, false>(st, lds0, wave, d_in, zeros), ...); }
+    (std::make_integer_sequence<int, C::DPW_W>{});
+  };
+  auto load_x = [&](int st) {
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I, false>(st, lds0, wave, d_in, zeros), ...); }
+    (std::make_integer_sequence<int, C::DPW_X>{});
+  };
+  auto mfma = [&](int set, int i) {
+    acc[i / MT][i % MT] = mfma32g(fa[set][i / MT], fb[set][i % MT], acc[i / MT][i % MT]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  const int nst = (d_in + KB - 1) / KB;
+#pragma unroll
+  for (int t = 0; t < NB; ++t) {
+    load_w(t);
+    if (t >= NB - NX) load_x(t - (NB - NX));
+  }
+  vm_barrier<(NX - 1) * C::DPW>();
+#pragma unroll
+  for (int f = 0; f < NF; ++f) frag(0, 0, 0, f);
+  for (int st = 0; st < nst; ++st) {
+#pragma unroll
+    for (int kk = 0; kk + 1 < KS; ++kk) {
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        mfma(kk & 1, i);
+        if (i * NF / NM != (i + 1) * NF / NM) {   // NF reads spread over NM MFMAs
+          frag(st, kk + 1, (kk + 1) & 1, i * NF / NM);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    constexpr int LS = (KS - 1) & 1;
+#pragma unroll
+    for (int i = 0; i < H; ++i) mfma(LS, i);
+    vm_barrier<C::VMC>();
+    __builtin_amdgcn_sched_barrier(0);
+    [&]<int... I>(std::integer_sequence<int, I...>) {
+      ((mfma(LS, H + I),
+        [&] {
+          if constexpr (I < NF) frag(st + 1, 0, 0, I);
+          __builtin_amdgcn_sched_barrier(0);
+          // the loads, as many per MFMA as it takes to issue all of them here
+          constexpr int L0 = I * C::DPW / (NM - H), L1 = (I + 1) * C::DPW / (NM - H);
+          [&]<int... J>(std::integer_sequence<int, J...>) {
+            (s.template issue<L0 + J, false>(L0 + J < C::DPW_W ? st + NB : st + NX, lds0, wave, d_in, zeros), ...);
+          }(std::make_integer_sequence<int, L1 - L0>{});
+          __builtin_amdgcn_sched_barrier(0);
+        }()), ...);
+    }(std::make_integer_sequence<int, NM - H>{});
+  }
+  vm_barrier<0>();   // the ring's last loads (zeros) land before the LDS is reused
+}
+
+// Main loop of the smaller tiles (two waves per SIMD): a barrier per stage, the
+// fragments of k-step kk + 1 read while k-step kk is multiplied.
+template <class C, bool NT>
+__device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, const void* zeros, char* lds,
+                                              int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
+  constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = KB / 16;
+  const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  int fcol[KS];
+#pragma unroll
+  for (int kk = 0; kk < KS; ++kk) fcol[kk] = ((kk * 2 + kh) ^ gswz<KB>(l32)) * 16;
+  auto load_w = [&](int st) {
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I, NT>(st, lds0, wave, d_in, zeros), ...); }
+    (std::make_integer_sequence<int, C::DPW_W>{});
+  };
+  auto load_x = [&](int st) {
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I, NT>(st, lds0, wave, d_in, zeros), ...); }
+    (std::make_integer_sequence<int, C::DPW_X>{});
+  };
+#pragma unroll
+  for (int t = 0; t < NB - 1; ++t) {
+    load_w(t);
+    if (t >= NB - NX) load_x(t - (NB - NX));
+  }
+  const int nst = (d_in + KB - 1) / KB;
+  for (int st = 0; st < nst; ++st) {
+    vm_barrier<C::VMC>();
+    load_w(st + NB - 1);
+    load_x(st + NX - 1);
+    const char* Lw = lds + (st % NB) * C::WSTAGE_B + (wr * C::kWR + l32) * C::RB;
+    const char* Lx = lds + C::XRING + (st % NX) * C::XSTAGE_B + (wt * C::kWT + l32) * C::RB;
+    u32x4_t fa[2][C::MR], fb[2][C::MT];
+    auto frag = [&](int kk) {
+#pragma unroll
+      for (int m = 0; m < C::MR; ++m) fa[kk & 1][m] = *(const u32x4_t*)(Lw + m * 32 * C::RB + fcol[kk]);
+#pragma unroll
+      for (int n = 0; n < C::MT; ++n) fb[kk & 1][n] = *(const u32x4_t*)(Lx + n * 32 * C::RB + fcol[kk]);
+    };
+    frag(0);
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      if (kk + 1 < KS) frag(kk + 1);
+#pragma unroll
+      for (int m = 0; m < C::MR; ++m)
+#pragma unroll
+        for (int n = 0; n < C::MT; ++n) acc[m][n] = mfma32g(fa[kk & 1][m], fb[kk & 1][n], acc[m][n]);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, C::MR + C::MT, 0);
+#pragma unroll
+    for (int kk = 0; kk + 1 < KS; ++kk) sched_reads_over_mfma<C::MR + C::MT, C::MR * C::MT>();
+    __builtin_amdgcn_sched_group_barrier(0x008, C::MR * C::MT, 0);
+  }
+  vm_barrier<0>();
 }
 
 // Store of a wave's accumulators with an epilogue: rows v0 .. v0 + WR - 1
@@ -183,6 +372,49 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
           for (int e = 0; e < 8; ++e)
             if (col + e < d_y) y[at + e] = f32_to_bf16_bits(o[e]);
         }
+      }
+    }
+  }
+}
+
+// Store of a wave's accumulators in fp32, rows v0 .. v0 + WR - 1 by positions
+// p0 .. p0 + WT - 1 below p_end, position p to row p of y, bias added.
+template <class C>
+__device__ __forceinline__ void store_f32(f32x16_t (&acc)[C::MR][C::MT], char* lds, int wave, int lane, int v0, int p0,
+                                          int p_end, int d_out, const uint16_t* bias, float* y) {
+  constexpr int MC = C::MR >= 2 ? C::MR / 2 : 1;   // row blocks per pass through the LDS tile, as store_epilogue
+  constexpr int PITCH = MC * 128 + 16, CPR = MC * 8, PPP = kWave / CPR;
+  static_assert(C::NW * 32 * PITCH <= C::LDS_BYTES, "tile fits the LDS");
+  const int l32 = lane % 32, h = lane / 32, c = lane % CPR;
+  char* tile = lds + wave * 32 * PITCH;
+  const bool vec = d_out % 4 == 0;
+#pragma unroll
+  for (int m0 = 0; m0 < C::MR; m0 += MC) {
+    const int col = v0 + m0 * 32 + 4 * c;
+    float b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = bias ? elem_f32<uint16_t>(bias, min(col + i, d_out - 1)) : 0.f;
+#pragma unroll
+    for (int n = 0; n < C::MT; ++n) {
+#pragma unroll
+      for (int m = 0; m < MC; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(f32x4_t*)(tile + l32 * PITCH + (m * 32 + 8 * q + 4 * h) * 4) =
+              f32x4_t{acc[m0 + m][n][4 * q], acc[m0 + m][n][4 * q + 1], acc[m0 + m][n][4 * q + 2], acc[m0 + m][n][4 * q + 3]};
+#pragma unroll 4
+      for (int tb = 0; tb < 32; tb += PPP) {
+        const int tl = tb + lane / CPR, p = p0 + n * 32 + tl;
+        if (p >= p_end || col >= d_out) continue;
+        f32x4_t z = *(const f32x4_t*)(tile + tl * PITCH + 16 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] += b[i];
+        float* dst = y + (long long)p * d_out + col;
+        if (vec) *(f32x4_t*)dst = z;
+        else
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + i < d_out) dst[i] = z[i];
       }
     }
   }

@@ -12,6 +12,7 @@
 
 #include "../../include/mlora.h"
 #include "experts.h"
+#include "gemm_tile.h"
 
 namespace mlora {
 
@@ -179,6 +180,64 @@ __global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Tiled form (bf16, more rows per expert): a workgroup takes BR (virtual) rows
+// of one expert by a run of up to BT of its positions over the whole of d_in.
+//
+// Block order: block b runs on XCD b % 8, which takes row tiles xcd, xcd + 8, ...
+// and for each of them kRunGroup runs one after another, then the next group:
+// the runs of an expert that are in flight on an XCD share its L2's copy of W,
+// which is read from memory once per group.
+// ---------------------------------------------------------------------------
+constexpr int kRunGroup = 4;
+
+// OUT: 0 bf16 rows, 1 bf16 rows of a gated product, 2 fp32 rows (no activation)
+template <class C, int OUT, bool PIPE>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW / 4, C::NW / 4)))
+void k_experts_tile(ExpertsArgs a, int n_rt) {
+  constexpr bool GATED = OUT == 1;
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS_BYTES];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int nrx = (n_rt + 7) / 8;                        // row tiles per XCD
+  const int j = blockIdx.x >> 3;
+  const int rt = (j / kRunGroup % nrx) * 8 + (blockIdx.x & 7);
+  const int run = j / (kRunGroup * nrx) * kRunGroup + j % kRunGroup;
+  if (rt >= n_rt) return;
+  int p0, p1;
+  const int e = find_expert(a.seg_start, a.E, a.n_pos, C::kBT, run, &p0, &p1);
+  if (e < 0) return;   // uniform: past the last run
+  const int d_in = a.d_in, d_out = a.d_out, r0 = rt * C::kBR;
+  const uint16_t* __restrict__ W = (const uint16_t*)a.W + (long long)e * d_out * d_in;
+  const uint16_t* __restrict__ x = (const uint16_t*)a.x;
+
+  TileSrc<C> src;
+  src.set(wave, lane, [&](int r) { return W + (long long)wrow_of<GATED>(r0 + r, d_out) * d_in; },
+          [&](int r) {
+            const int p = min(p0 + r, p1 - 1);           // (absent positions repeat the last)
+            const int row = a.token_index ? a.token_index[p] : p;
+            return x + (long long)min(max(row, 0), a.n_rows - 1) * d_in;
+          });
+  f32x16_t acc[C::MR][C::MT];
+#pragma unroll
+  for (int m = 0; m < C::MR; ++m)
+#pragma unroll
+    for (int n = 0; n < C::MT; ++n)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.f;
+  if constexpr (PIPE) pipe_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
+  else ring_mainloop<C, false>(src, d_in, expert_zeros, lds, wave, lane, acc);
+
+  const int wr = wave / C::NWT, wt = wave % C::NWT;
+  const int v0 = r0 + wr * C::kWR, pw = p0 + wt * C::kWT;
+  EpiView epi = a.epi;
+  if (epi.bias) epi.bias = (const uint16_t*)epi.bias + (long long)e * d_out;
+  if constexpr (OUT == 2) {
+    store_f32<C>(acc, lds, wave, lane, v0, pw, p1, d_out, (const uint16_t*)epi.bias, (float*)a.y);
+  } else {
+    store_epilogue<C, GATED>(acc, lds, wave, lane, v0, pw, p1, d_out, epi, a.y, [](int p) { return p; });
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Way back: a token's rows weighted, summed in slot order and added to the
 // residual, in fp32, one rounding. A thread takes 4 columns of one token.
 // ---------------------------------------------------------------------------
@@ -238,8 +297,26 @@ static void launch_stream(const ExpertsArgs& a, hipStream_t st) {
   else launch_stream_n<TYPE, 4, 4>(a, st);
 }
 
+template <class C, bool PIPE>
+static void launch_tile(const ExpertsArgs& a, hipStream_t st) {
+  const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  const int n_rt = (rows + C::kBR - 1) / C::kBR;
+  const long long groups = (run_bound(a, C::kBT) + kRunGroup - 1) / kRunGroup;
+  const dim3 grid((unsigned)(8 * ((n_rt + 7) / 8) * kRunGroup * groups)), block(C::NT);
+  if (a.f32_out) hipLaunchKernelGGL((k_experts_tile<C, 2, PIPE>), grid, block, 0, st, a, n_rt);
+  else if (a.gated) hipLaunchKernelGGL((k_experts_tile<C, 1, PIPE>), grid, block, 0, st, a, n_rt);
+  else hipLaunchKernelGGL((k_experts_tile<C, 0, PIPE>), grid, block, 0, st, a, n_rt);
+}
+
+typedef GCfg<256, 256, 128, 128, 5, 32, 5> Tile256;
+typedef GCfg<128, 128, 64, 32, 3, 64, 3> Tile128;
+typedef GCfg<64, 128, 32, 32, 4, 64, 4> Tile64;
+
 void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st) {
   if (a.n_pos <= 0) return;
+  const int mean = a.n_pos / std::min(a.E, a.n_pos);   // positions per expert
+  if (bf16 && !a.w_scale && mean >= 192) return launch_tile<Tile256, true>(a, st);
+  if (bf16 && !a.w_scale && mean >= 64) return launch_tile<Tile128, false>(a, st);
   if (!bf16) launch_stream<kXF32>(a, st);
   else if (a.w_scale) launch_stream<kXFp8w>(a, st);
   else launch_stream<kXBf16>(a, st);
