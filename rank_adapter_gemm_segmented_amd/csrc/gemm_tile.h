@@ -155,8 +155,8 @@ struct TileSrc {
 // The stage boundary lies inside a k-step: when the last k-step's first H MFMAs
 // have issued, every fragment of the stage is in registers, the wave waits
 // for its own loads of the next stage, and past the barrier the next stage is
-// whole and this one's slots are free. The loads of later stages and the first
-// fragments of the next stage then go out under the remaining MFMAs.
+// whole and this one's slots are free. The first fragments of the next stage
+// are read under the remaining MFMAs.
 template <class C>
 __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, const void* zeros, char* lds,
                                               int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
@@ -194,45 +194,65 @@ __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, con
     __builtin_amdgcn_sched_barrier(0);
   };
 
+  // Iteration t of the loop requests W stage t + NB and position stage t + NX
+  // into the slots that stage t has freed, one load per few MFMAs (a burst of
+  // them holds up the wave at issue: 2135 us for the largest case, against
+  // 1992 spread over 24 of a stage's 32 MFMAs and 1995 over all of them): the
+  // first D1 under the rest of stage t's last k-step, the others under stage
+  // t + 1 before its own boundary.
+  constexpr int NS = KS * NM;                            // MFMAs of a stage
+  constexpr int SP = NS * 3 / 4;                         // over which its requests are spread
+  auto upto = [](int i) constexpr { return i >= SP ? C::DPW : i * C::DPW / SP; };
+  constexpr int D1 = upto(NM - H);
+  auto request = [&]<int L0, int N>(int t, std::integral_constant<int, L0>, std::integral_constant<int, N>) {
+    [&]<int... J>(std::integer_sequence<int, J...>) {
+      (s.template issue<L0 + J, false>(L0 + J < C::DPW_W ? t + NB : t + NX, lds0, wave, d_in, zeros), ...);
+    }(std::make_integer_sequence<int, N>{});
+    if constexpr (N > 0) __builtin_amdgcn_sched_barrier(0);
+  };
+  // what is requested after MFMA I of a stage (counted from the boundary before it)
+  auto request_at = [&]<int I>(int t, std::integral_constant<int, I>) {
+    constexpr int L0 = upto(I), L1 = upto(I + 1);
+    request(t, std::integral_constant<int, L0>{}, std::integral_constant<int, L1 - L0>{});
+  };
+  auto each = []<int... I>(std::integer_sequence<int, I...>, auto f) { (f(std::integral_constant<int, I>{}), ...); };
+
   const int nst = (d_in + KB - 1) / KB;
+  // requests of the iterations before the first (of those only that exist:
+  // position stages start NB - NX iterations later), the last one's first part only
 #pragma unroll
-  for (int t = 0; t < NB; ++t) {
-    load_w(t);
-    if (t >= NB - NX) load_x(t - (NB - NX));
+  for (int t = -NB; t < -1; ++t) {
+    load_w(t + NB);
+    if (t + NX >= 0) load_x(t + NX);
   }
-  vm_barrier<(NX - 1) * C::DPW>();
+  request(-1, std::integral_constant<int, 0>{}, std::integral_constant<int, D1>{});
+  vm_barrier<(NX - 2) * C::DPW + D1>();
 #pragma unroll
   for (int f = 0; f < NF; ++f) frag(0, 0, 0, f);
   for (int st = 0; st < nst; ++st) {
-#pragma unroll
-    for (int kk = 0; kk + 1 < KS; ++kk) {
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        mfma(kk & 1, i);
-        if (i * NF / NM != (i + 1) * NF / NM) {   // NF reads spread over NM MFMAs
-          frag(st, kk + 1, (kk + 1) & 1, i * NF / NM);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+    each(std::make_integer_sequence<int, (KS - 1) * NM>{}, [&](auto ic) {
+      constexpr int I = ic.value, kk = I / NM, i = I % NM;
+      mfma(kk & 1, i);
+      if constexpr (i * NF / NM != (i + 1) * NF / NM) {   // NF reads spread over NM MFMAs
+        frag(st, kk + 1, (kk + 1) & 1, i * NF / NM);
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
+      request_at(st - 1, std::integral_constant<int, NM - H + I>{});
+    });
     constexpr int LS = (KS - 1) & 1;
-#pragma unroll
-    for (int i = 0; i < H; ++i) mfma(LS, i);
+    each(std::make_integer_sequence<int, H>{}, [&](auto ic) {
+      mfma(LS, ic.value);
+      request_at(st - 1, std::integral_constant<int, NS - H + ic.value>{});
+    });
     vm_barrier<C::VMC>();
     __builtin_amdgcn_sched_barrier(0);
-    [&]<int... I>(std::integer_sequence<int, I...>) {
-      ((mfma(LS, H + I),
-        [&] {
-          if constexpr (I < NF) frag(st + 1, 0, 0, I);
-          __builtin_amdgcn_sched_barrier(0);
-          // the loads, as many per MFMA as it takes to issue all of them here
-          constexpr int L0 = I * C::DPW / (NM - H), L1 = (I + 1) * C::DPW / (NM - H);
-          [&]<int... J>(std::integer_sequence<int, J...>) {
-            (s.template issue<L0 + J, false>(L0 + J < C::DPW_W ? st + NB : st + NX, lds0, wave, d_in, zeros), ...);
-          }(std::make_integer_sequence<int, L1 - L0>{});
-          __builtin_amdgcn_sched_barrier(0);
-        }()), ...);
-    }(std::make_integer_sequence<int, NM - H>{});
+    each(std::make_integer_sequence<int, NM - H>{}, [&](auto ic) {
+      constexpr int I = ic.value;
+      mfma(LS, H + I);
+      if constexpr (I < NF) frag(st + 1, 0, 0, I);
+      __builtin_amdgcn_sched_barrier(0);
+      request_at(st, ic);
+    });
   }
   vm_barrier<0>();   // the ring's last loads (zeros) land before the LDS is reused
 }
