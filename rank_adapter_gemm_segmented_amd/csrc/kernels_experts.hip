@@ -37,26 +37,34 @@ constexpr int kXBf16 = 0, kXFp8w = 1, kXF32 = 2;   // element types of the strea
 
 // ---------------------------------------------------------------------------
 // Streaming form, every type: an item is 16 NR (virtual) rows of one expert by
-// up to 16 NTB of its positions, over the whole of d_in. The 8 waves split d_in
-// in units of 128 bytes of a W row (wave w takes units w, w + 8, ...), load W
-// and x straight into MFMA operand registers, and their sums are added in wave
-// order through LDS. W is read once where an expert has at most 16 NTB rows.
+// up to 16 NTB of its positions, over the whole of d_in. The NW waves take a
+// contiguous part of d_in each, in units of 128 bytes of a W row, load W and x
+// straight into MFMA operand registers, and their sums are added in wave order
+// through LDS. W is read once where an expert has at most 16 NTB rows.
 //
 // A unit is two 16-byte loads per row block: lane group g = l / 16 takes bytes
 // 16 g and 64 + 16 g, so a row's 128-byte line is whole within the unit. bf16:
 // a load is one 32-column MFMA operand; FP8: 16 columns, two operands (columns
 // 16 g and 16 g + 8 of the 64); fp32: 4 columns, four 16x16x4 products.
+//
+// Bound by W's bytes. One unit per wave is in flight, refilled as it is
+// consumed: the waves resident on a CU (28 of 67 registers) keep 224 KB
+// requested, and a second unit per wave cost as much occupancy as it gave
+// (121 against 113 us, 64 tokens over 64 FP8 experts of 4096 -> 2 x 1024). W is
+// loaded without the nontemporal mark: a line's two halves come by two loads,
+// and the mark lost the first half's line (128 against 113 us). Neighbouring
+// workgroups take neighbouring row tiles, so the card streams W in order
+// (an order that put an expert's runs side by side on an XCD: 119 us).
 // ---------------------------------------------------------------------------
 constexpr int kGridY = 32768;   // runs per grid row (y is limited; z takes the rest)
-constexpr int kXsThreads = 512, kXsWaves = kXsThreads / kWave;
 
-template <int TYPE, int NR, int NTB, bool GATED>
-__global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
+template <int TYPE, int NR, int NTB, int NW, bool GATED>
+__global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
   constexpr int EB = TYPE == kXFp8w ? 1 : TYPE == kXF32 ? 4 : 2;   // bytes per W element
   constexpr int XB = TYPE == kXF32 ? 4 : 2;                        // and per x element
   constexpr int UC = 128 / EB;                                     // columns per unit
   constexpr int XL = XB / EB;                                      // x loads per W load
-  __shared__ f32x4_t red[kXsWaves][NR * NTB][kWave];
+  __shared__ f32x4_t red[NW][NR * NTB][kWave];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int l16 = lane % 16, g = lane / 16;
   const int rt = blockIdx.x;
@@ -67,9 +75,17 @@ __global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
   const int v0 = rt * 16 * NR;                                     // first (virtual) row
   auto wrow = [&](int v) { return (long long)e * d_out + wrow_of<GATED>(v, d_out); };
 
-  const char* wp[NR];
+  // W: a uniform base (gated: one for gate rows and one for up rows) and a
+  // 32-bit offset per lane and row block; rows past the last are clamped to it.
+  // Registers are occupancy here, and occupancy is bytes in flight: with a
+  // 64-bit address per row block the kernel took 108 registers and 127 us.
+  constexpr int NO = GATED ? NR / 2 : NR;                          // distinct row blocks
+  const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out;
+  const char* wbase = (const char*)a.W + ((long long)e * d_out + f0) * d_in * EB;
+  const long long up = (long long)nf * d_in * EB;                  // gated: from a gate row to its up row
+  uint32_t wo[NO];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) wp[r] = (const char*)a.W + wrow(v0 + 16 * r + l16) * d_in * EB + 16 * g;
+  for (int r = 0; r < NO; ++r) wo[r] = (uint32_t)min(16 * r + l16, nf - 1 - f0) * (uint32_t)(d_in * EB) + 16 * g;
   const char* xp[NTB];
 #pragma unroll
   for (int t = 0; t < NTB; ++t) {
@@ -77,7 +93,6 @@ __global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
     const int row = a.token_index ? a.token_index[p] : p;
     xp[t] = (const char*)a.x + (long long)min(max(row, 0), a.n_rows - 1) * d_in * XB + 16 * XL * g;
   }
-  const char* zeros = (const char*)expert_zeros;
 
   f32x4_t acc[NR][NTB];
 #pragma unroll
@@ -85,21 +100,20 @@ __global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
 #pragma unroll
     for (int t = 0; t < NTB; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int nu = (d_in + UC - 1) / UC;
-  for (int u = wave; u < nu; u += kXsWaves) {
-    u32x4_t w[2][NR], x[2][XL][NTB];
-    const int c0 = u * UC;
+  u32x4_t w[2][NR], x[2][XL][NTB];
+  auto load = [&](int u) {                                         // unit u, whole
+    const char* wu = wbase + (long long)u * 128;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int c = c0 + h * UC / 2;                               // first column of the load, group 0
-      const bool in = c + 16 / EB * g < d_in;                      // (d_in is a multiple of 16 bytes of W)
 #pragma unroll
-      for (int r = 0; r < NR; ++r) w[h][r] = ld_nt16(sel_addr(in, wp[r] + (long long)c * EB, zeros));
+      for (int r = 0; r < NR; ++r) w[h][r] = ld16((GATED && (r & 1) ? wu + up : wu) + wo[GATED ? r / 2 : r] + 64 * h);
 #pragma unroll
       for (int i = 0; i < XL; ++i)
 #pragma unroll
-        for (int t = 0; t < NTB; ++t) x[h][i][t] = ld16(sel_addr(in, xp[t] + (long long)c * XB + 16 * i, zeros));
+        for (int t = 0; t < NTB; ++t) x[h][i][t] = ld16(xp[t] + (long long)u * (UC * XB) + h * (UC / 2 * XB) + 16 * i);
     }
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -118,6 +132,33 @@ __global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
                                                                acc[r][t], 0, 0, 0);
           }
         }
+  };
+  const int nu = d_in / UC;                                        // whole units
+  const int ub = nu * wave / NW, ue = nu * (wave + 1) / NW;        // this wave's
+  if (ub < ue) {   // uniform
+    load(ub);
+    for (int u = ub; u + 1 < ue; ++u) {
+      multiply();
+      load(u + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    multiply();
+  }
+  if (nu * UC < d_in && wave == NW - 1) {   // uniform: the columns behind the last whole unit
+    const char* wu = wbase + (long long)nu * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = nu * UC + h * UC / 2 + 16 / EB * g < d_in;   // (d_in is a multiple of 16 bytes of W)
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        w[h][r] = in ? ld16((GATED && (r & 1) ? wu + up : wu) + wo[GATED ? r / 2 : r] + 64 * h) : zero_u32x4();
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+#pragma unroll
+        for (int t = 0; t < NTB; ++t)
+          x[h][i][t] = in ? ld16(xp[t] + (long long)nu * (UC * XB) + h * (UC / 2 * XB) + 16 * i) : zero_u32x4();
+    }
+    multiply();
   }
 #pragma unroll
   for (int r = 0; r < NR; ++r)
@@ -129,7 +170,7 @@ __global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
   // of one position (gated: the gate rows and the up rows of 4 features)
   constexpr int NB = GATED ? NR / 2 : NR;                          // row blocks of features
   const int d_y = GATED ? d_out / 2 : d_out;
-  for (int q = tid; q < NB * NTB * kWave; q += kXsThreads) {
+  for (int q = tid; q < NB * NTB * kWave; q += NW * kWave) {
     const int ql = q % kWave, t = (q / kWave) % NTB, b = q / kWave / NTB;
     const int p = p0 + 16 * t + ql % 16;
     const int f = (GATED ? v0 / 2 : v0) + 16 * b + 4 * (ql / 16);  // first feature
@@ -137,7 +178,7 @@ __global__ __launch_bounds__(kXsThreads) void k_experts_stream(ExpertsArgs a) {
     auto sum = [&](int r, float* z) {                              // row block r
       f32x4_t s = red[0][r * NTB + t][ql];
 #pragma unroll
-      for (int w = 1; w < kXsWaves; ++w)
+      for (int w = 1; w < NW; ++w)
 #pragma unroll
         for (int v = 0; v < 4; ++v) s[v] += red[w][r * NTB + t][ql][v];
 #pragma unroll
@@ -282,21 +323,30 @@ static long long run_bound(const ExpertsArgs& a, int BT) {
   return (long long)a.n_pos / BT + (a.E < a.n_pos ? a.E : a.n_pos);
 }
 
-template <int TYPE, int NR, int NTB>
-static void launch_stream_n(ExpertsArgs a, hipStream_t st) {
+template <int TYPE, int NR, int NTB, int NW>
+static void launch_stream_n(const ExpertsArgs& a, hipStream_t st) {
   const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
   const long long runs = run_bound(a, 16 * NTB);
   const dim3 grid((rows + 16 * NR - 1) / (16 * NR), (unsigned)std::min<long long>(runs, kGridY), (unsigned)((runs + kGridY - 1) / kGridY));
-  if (a.gated) hipLaunchKernelGGL((k_experts_stream<TYPE, NR, NTB, true>), grid, dim3(kXsThreads), 0, st, a);
-  else hipLaunchKernelGGL((k_experts_stream<TYPE, NR, NTB, false>), grid, dim3(kXsThreads), 0, st, a);
+  if (a.gated) hipLaunchKernelGGL((k_experts_stream<TYPE, NR, NTB, NW, true>), grid, dim3(NW * kWave), 0, st, a);
+  else hipLaunchKernelGGL((k_experts_stream<TYPE, NR, NTB, NW, false>), grid, dim3(NW * kWave), 0, st, a);
 }
 
+// Shape of the streaming form. Few items (a token or two): 32 rows and 8 waves
+// each, so that the card is full (one token, two of eight experts of 4096 -> 2
+// x 14336: 79.5 us against 85.6 with 64 rows and 4 waves). Otherwise 64 rows
+// and 4 waves (64 tokens, 64 FP8 experts: 113 us against 134). Positions per
+// item by the mean per expert, with room for uneven ones; FP8 keeps to 16
+// longer, its x operands taking twice the registers per byte of W.
 template <int TYPE>
 static void launch_stream(const ExpertsArgs& a, hipStream_t st) {
-  const int active = a.E < a.n_pos ? a.E : a.n_pos;
-  if (a.n_pos <= 8 * active) launch_stream_n<TYPE, 4, 1>(a, st);
-  else if (a.n_pos <= 24 * active) launch_stream_n<TYPE, 4, 2>(a, st);
-  else launch_stream_n<TYPE, 4, 4>(a, st);
+  const long long active = std::min(a.E, a.n_pos);
+  const long long items = (long long)((a.gated ? gated_rows(a.d_out) : a.d_out) + 63) / 64 * active;
+  const double mean = (double)a.n_pos / active;
+  if (items < 2048 && mean <= 4) launch_stream_n<TYPE, 2, 1, 8>(a, st);
+  else if (mean <= (TYPE == kXFp8w ? 10 : 4)) launch_stream_n<TYPE, 4, 1, 4>(a, st);
+  else if (mean <= 24) launch_stream_n<TYPE, 4, 2, 4>(a, st);
+  else launch_stream_n<TYPE, 4, 4, 4>(a, st);
 }
 
 template <class C, bool PIPE>
