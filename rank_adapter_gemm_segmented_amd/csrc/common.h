@@ -45,6 +45,24 @@ __device__ __forceinline__ u32x4_t ld_nt16(const void* p) {
 }
 __device__ __forceinline__ u32x4_t ld16(const void* p) { return *(const u32x4_t*)p; }
 
+// Eight FP8 e4m3 codes (OCP E4M3: bias 7, subnormals m/8 * 2^-6) -> eight
+// bf16 values, exact: every e4m3 value has at most 4 significant bits and an
+// exponent inside bf16's range. gfx950's scaled conversion turns two codes
+// into two bf16 per instruction (scale 1; checked against the E4M3
+// definition on all 256 codes).
+template <bool HI>
+__device__ __forceinline__ uint32_t e4m3x2_bf16(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
+}
+__device__ __forceinline__ u32x4_t e4m3x8_bf16(uint32_t lo, uint32_t hi) {
+  u32x4_t r;
+  r.x = e4m3x2_bf16<false>(lo);
+  r.y = e4m3x2_bf16<true>(lo);
+  r.z = e4m3x2_bf16<false>(hi);
+  r.w = e4m3x2_bf16<true>(hi);
+  return r;
+}
+
 // Element offset of B[n][j] in a bf16 slot's B region. Rank columns are
 // stored in blocks of 16: block b holds columns 16 b .. 16 b + 15 of every
 // row, [d_out][16] contiguous, so one block's columns over 32 consecutive

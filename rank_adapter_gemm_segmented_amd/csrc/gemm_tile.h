@@ -53,16 +53,19 @@ __device__ __forceinline__ void vm_barrier() {
 // are 2 KB bytes (KB bf16), unpadded, and 16-byte chunk c of row r sits in slot
 // c ^ gswz(r) of the row, so the rows read together by one fragment load fall
 // in distinct LDS banks.
-template <int BR, int BT, int WR, int WT, int NB, int KB, int NX>
+// W8: the W rows are FP8 codes of KB bytes (one per column), in the same ring.
+template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, bool W8 = false>
 struct GCfg {
+  static constexpr bool kW8 = W8;
+  static constexpr int WRB = W8 ? KB : 2 * KB;             // bytes per LDS row of W
   static constexpr int kBR = BR, kBT = BT, kWR = WR, kWT = WT, kNB = NB, kKB = KB, kNX = NX;
   static constexpr int NWR = BR / WR, NWT = BT / WT;
   static constexpr int NW = NWR * NWT;
   static constexpr int NT = NW * kWave;
   static constexpr int MR = WR / 32, MT = WT / 32;        // 32x32 blocks per wave
-  static constexpr int RB = 2 * KB;                        // bytes per LDS row
-  static constexpr int WSTAGE_B = BR * RB, XSTAGE_B = BT * RB;   // ring slots
-  static constexpr int DPW_W = BR * 2 * KB / 1024 / NW;    // 1 KB loads per wave per stage: W rows
+  static constexpr int RB = 2 * KB;                        // bytes per LDS row of positions
+  static constexpr int WSTAGE_B = BR * WRB, XSTAGE_B = BT * RB;   // ring slots
+  static constexpr int DPW_W = BR * WRB / 1024 / NW;    // 1 KB loads per wave per stage: W rows
   static constexpr int DPW_X = BT * 2 * KB / 1024 / NW;    // and positions
   static constexpr int DPW = DPW_W + DPW_X;
   static constexpr int XRING = NB * WSTAGE_B;              // byte offset of the position ring
@@ -75,8 +78,13 @@ struct GCfg {
   static constexpr int YT_BYTES = NW * WT * (2 * WR + 16);
   static constexpr int LDS_BYTES0 = MAIN_BYTES > 96 * 1024 ? MAIN_BYTES : 96 * 1024;
   static constexpr int LDS_BYTES = LDS_BYTES0 > YT_BYTES ? LDS_BYTES0 : YT_BYTES;
-  static_assert(KB == 32 || KB == 64, "stage depth");
-  static_assert((BR * 2 * KB) % (1024 * NW) == 0 && (BT * 2 * KB) % (1024 * NW) == 0,
+  // epilogue stores (store_epilogue, store_f32): 32 positions by half of the
+  // wave's row blocks, fp32, per wave; LDS of a kernel with no other use for it
+  static constexpr int EPI_MC = MR >= 2 ? MR / 2 : 1;
+  static constexpr int EPI_BYTES = NW * 32 * (EPI_MC * 128 + 16);
+  static constexpr int TILE_BYTES = MAIN_BYTES > EPI_BYTES ? MAIN_BYTES : EPI_BYTES;
+  static_assert(KB == 32 || KB == 64 || (W8 && KB == 128), "stage depth");
+  static_assert((BR * WRB) % (1024 * NW) == 0 && (BT * 2 * KB) % (1024 * NW) == 0,
                 "each ring's stage splits into whole loads per wave");
   static_assert(NB >= 2 && NX >= 2 && NB >= NX && VMC <= 63, "ring depths and vmcnt range");
 };
@@ -92,7 +100,7 @@ struct GCfg {
 // (r >> 1) & 3 permutations conflicted two ways.
 template <int KB>
 __device__ __forceinline__ int gswz(int r) {
-  return KB == 64 ? (((r >> 1) ^ ((r & 1) << 2)) & 7) : ((r >> 2) & 3);
+  return KB == 128 ? r & 15 : KB == 64 ? (((r >> 1) ^ ((r & 1) << 2)) & 7) : ((r >> 2) & 3);
 }
 
 // Scheduling hint for one k-step: the R fragment reads of the next k-step
@@ -109,37 +117,42 @@ __device__ __forceinline__ void sched_reads_over_mfma() {
 // The rows a wave loads: per stage DPW_W loads of the W ring and DPW_X of the
 // position ring. Load i < DPW_W of wave w fills the W slot's 1 KB chunk
 // J = i NW + w, load DPW_W + i the position slot's chunk J; lane l writes byte
-// 1024 J + 16 l of the slot, i.e. row r, slot l % (KB / 8), and so fetches chunk
-// (slot ^ gswz(r)) of that row. wrow(r) and xrow(r) give the address of the
-// tile's r-th W row and position.
+// 1024 J + 16 l of the slot, i.e. one 16-byte slot of a row r, and so fetches
+// chunk (slot ^ swizzle of r) of that row. wrow(r) and xrow(r) give the address
+// of the tile's r-th W row and position.
 template <class C>
 struct TileSrc {
-  const uint16_t* src[C::DPW];
-  int scol[C::DPW];
+  static constexpr int kWSw = C::WRB / 2;                 // (gswz goes by the row's bytes)
+  const char* src[C::DPW];
+  int scol[C::DPW];                                       // first column of the lane's chunk
   template <class WRow, class XRow>
   __device__ __forceinline__ void set(int wave, int lane, WRow wrow, XRow xrow) {
 #pragma unroll
     for (int i = 0; i < C::DPW; ++i) {
       const bool isx = i >= C::DPW_W;
-      const int J = (isx ? i - C::DPW_W : i) * C::NW + wave;
-      const int r = J * (1024 / (2 * C::kKB)) + lane / (C::kKB / 8);
-      scol[i] = ((lane % (C::kKB / 8)) ^ gswz<C::kKB>(r)) * 8;
-      src[i] = (isx ? xrow(r) : wrow(r)) + scol[i];
+      const int at = ((isx ? i - C::DPW_W : i) * C::NW + wave) * 64 + lane;   // 16-byte slot of the ring slot
+      if (isx) {
+        const int r = at / (C::RB / 16), c = (at % (C::RB / 16)) ^ gswz<C::kKB>(r);
+        src[i] = (const char*)xrow(r) + 16 * c;
+        scol[i] = 8 * c;
+      } else {
+        const int r = at / (C::WRB / 16), c = (at % (C::WRB / 16)) ^ gswz<kWSw>(r);
+        src[i] = (const char*)wrow(r) + 16 * c;
+        scol[i] = (C::kW8 ? 16 : 8) * c;
+      }
     }
   }
   // load I of stage st (W rows for I < DPW_W, else positions) into the ring;
   // columns past d_in read `zeros`, so that every stage has the same count
-  template <int I, bool NT>
+  template <int I>
   __device__ __forceinline__ void issue(int st, uint32_t lds0, int wave, int d_in, const void* zeros) const {
     constexpr bool isx = I >= C::DPW_W;
     constexpr int j = isx ? I - C::DPW_W : I;
     const uint32_t slot = isx ? lds0 + C::XRING + (uint32_t)(st % C::kNX) * C::XSTAGE_B
                               : lds0 + (uint32_t)(st % C::kNB) * C::WSTAGE_B;
-    const uint32_t at = slot + (uint32_t)(j * C::NW + wave) * 1024;
     const int k0 = st * C::kKB;
-    const void* g = sel_addr(k0 + scol[I] < d_in, src[I] + k0, zeros);
-    if (NT && !isx) dma16_nt(g, at);
-    else dma16(g, at);
+    dma16(sel_addr(k0 + scol[I] < d_in, src[I] + k0 * (isx || !C::kW8 ? 2 : 1), zeros),
+          slot + (uint32_t)(j * C::NW + wave) * 1024);
   }
 };
 
@@ -182,11 +195,11 @@ __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, con
     }
   };
   auto load_w = [&](int st) {
-    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I, false>(st, lds0, wave, d_in, zeros), ...); }
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I>(st, lds0, wave, d_in, zeros), ...); }
     (std::make_integer_sequence<int, C::DPW_W>{});
   };
   auto load_x = [&](int st) {
-    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I, false>(st, lds0, wave, d_in, zeros), ...); }
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I>(st, lds0, wave, d_in, zeros), ...); }
     (std::make_integer_sequence<int, C::DPW_X>{});
   };
   auto mfma = [&](int set, int i) {
@@ -206,7 +219,7 @@ __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, con
   constexpr int D1 = upto(NM - H);
   auto request = [&]<int L0, int N>(int t, std::integral_constant<int, L0>, std::integral_constant<int, N>) {
     [&]<int... J>(std::integer_sequence<int, J...>) {
-      (s.template issue<L0 + J, false>(L0 + J < C::DPW_W ? t + NB : t + NX, lds0, wave, d_in, zeros), ...);
+      (s.template issue<L0 + J>(L0 + J < C::DPW_W ? t + NB : t + NX, lds0, wave, d_in, zeros), ...);
     }(std::make_integer_sequence<int, N>{});
     if constexpr (N > 0) __builtin_amdgcn_sched_barrier(0);
   };
@@ -259,21 +272,30 @@ __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, con
 
 // Main loop of the smaller tiles (two waves per SIMD): a barrier per stage, the
 // fragments of k-step kk + 1 read while k-step kk is multiplied.
-template <class C, bool NT>
+//
+// FP8 W: a lane reads 16 codes at once, two k-steps' worth, and converts 8 of
+// them per step (e4m3 is exact in bf16). Lane half h's codes are columns 32 q +
+// 16 h .. + 15 of step pair q, so the position fragments of steps 2 q and 2 q + 1
+// are columns 32 q + 16 h .. + 7 and + 8 .. + 15: which column sits in which k slot
+// of an MFMA does not matter as long as both operands agree.
+template <class C>
 __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, const void* zeros, char* lds,
                                               int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
   constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = KB / 16;
   const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  int fcol[KS];
+  int fx[KS], fw[KS];                                     // byte of the lane's chunk in its row
 #pragma unroll
-  for (int kk = 0; kk < KS; ++kk) fcol[kk] = ((kk * 2 + kh) ^ gswz<KB>(l32)) * 16;
+  for (int kk = 0; kk < KS; ++kk) {
+    fx[kk] = ((C::kW8 ? (kk >> 1) * 4 + 2 * kh + (kk & 1) : kk * 2 + kh) ^ gswz<KB>(l32)) * 16;
+    fw[kk] = ((C::kW8 ? (kk >> 1) * 2 + kh : kk * 2 + kh) ^ gswz<TileSrc<C>::kWSw>(l32)) * 16;
+  }
   auto load_w = [&](int st) {
-    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I, NT>(st, lds0, wave, d_in, zeros), ...); }
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I>(st, lds0, wave, d_in, zeros), ...); }
     (std::make_integer_sequence<int, C::DPW_W>{});
   };
   auto load_x = [&](int st) {
-    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I, NT>(st, lds0, wave, d_in, zeros), ...); }
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I>(st, lds0, wave, d_in, zeros), ...); }
     (std::make_integer_sequence<int, C::DPW_X>{});
   };
 #pragma unroll
@@ -286,28 +308,41 @@ __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, con
     vm_barrier<C::VMC>();
     load_w(st + NB - 1);
     load_x(st + NX - 1);
-    const char* Lw = lds + (st % NB) * C::WSTAGE_B + (wr * C::kWR + l32) * C::RB;
+    const char* Lw = lds + (st % NB) * C::WSTAGE_B + (wr * C::kWR + l32) * C::WRB;
     const char* Lx = lds + C::XRING + (st % NX) * C::XSTAGE_B + (wt * C::kWT + l32) * C::RB;
-    u32x4_t fa[2][C::MR], fb[2][C::MT];
+    u32x4_t fa[2][C::MR], fb[2][C::MT];                   // (FP8: fa by step pair)
     auto frag = [&](int kk) {
+      if (!C::kW8 || kk % 2 == 0) {
 #pragma unroll
-      for (int m = 0; m < C::MR; ++m) fa[kk & 1][m] = *(const u32x4_t*)(Lw + m * 32 * C::RB + fcol[kk]);
+        for (int m = 0; m < C::MR; ++m)
+          fa[C::kW8 ? (kk >> 1) & 1 : kk & 1][m] = *(const u32x4_t*)(Lw + m * 32 * C::WRB + fw[kk]);
+      }
 #pragma unroll
-      for (int n = 0; n < C::MT; ++n) fb[kk & 1][n] = *(const u32x4_t*)(Lx + n * 32 * C::RB + fcol[kk]);
+      for (int n = 0; n < C::MT; ++n) fb[kk & 1][n] = *(const u32x4_t*)(Lx + n * 32 * C::RB + fx[kk]);
     };
     frag(0);
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
       if (kk + 1 < KS) frag(kk + 1);
 #pragma unroll
-      for (int m = 0; m < C::MR; ++m)
+      for (int m = 0; m < C::MR; ++m) {
+        u32x4_t wa;
+        if constexpr (C::kW8) {
+          const u32x4_t raw = fa[(kk >> 1) & 1][m];
+          wa = (kk & 1) ? e4m3x8_bf16(raw.z, raw.w) : e4m3x8_bf16(raw.x, raw.y);
+        } else {
+          wa = fa[kk & 1][m];
+        }
 #pragma unroll
-        for (int n = 0; n < C::MT; ++n) acc[m][n] = mfma32g(fa[kk & 1][m], fb[kk & 1][n], acc[m][n]);
+        for (int n = 0; n < C::MT; ++n) acc[m][n] = mfma32g(wa, fb[kk & 1][n], acc[m][n]);
+      }
     }
-    __builtin_amdgcn_sched_group_barrier(0x100, C::MR + C::MT, 0);
+    if constexpr (!C::kW8) {
+      __builtin_amdgcn_sched_group_barrier(0x100, C::MR + C::MT, 0);
 #pragma unroll
-    for (int kk = 0; kk + 1 < KS; ++kk) sched_reads_over_mfma<C::MR + C::MT, C::MR * C::MT>();
-    __builtin_amdgcn_sched_group_barrier(0x008, C::MR * C::MT, 0);
+      for (int kk = 0; kk + 1 < KS; ++kk) sched_reads_over_mfma<C::MR + C::MT, C::MR * C::MT>();
+      __builtin_amdgcn_sched_group_barrier(0x008, C::MR * C::MT, 0);
+    }
   }
   vm_barrier<0>();
 }
@@ -322,13 +357,12 @@ __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, con
 // rounded once and stored as 16 bytes, consecutive lanes covering a row.
 template <class C, bool GATED, class RowOf>
 __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], char* lds, int wave, int lane, int v0,
-                                               int p0, int p_end, int d_out, const EpiView& epi, void* y_,
-                                               RowOf row_of) {
-  constexpr int MC = C::MR >= 2 ? C::MR / 2 : 1;        // row blocks per pass
+                                               int p0, int p_end, int d_out, const EpiView& epi, const float* w_scale,
+                                               void* y_, RowOf row_of) {
+  constexpr int MC = C::EPI_MC;                         // row blocks per pass
   constexpr int NF = MC * (GATED ? 16 : 32);            // features per pass
   constexpr int PITCH = MC * 128 + 16;                  // tile row (bytes)
   constexpr int CPR = NF / 8, PPP = kWave / CPR;        // lanes per position, positions per step
-  static_assert(C::NW * 32 * PITCH <= C::LDS_BYTES, "epilogue tile fits the LDS");
   const int l32 = lane % 32, h = lane / 32, c = lane % CPR;
   const int d_y = GATED ? d_out / 2 : d_out;
   char* tile = lds + wave * 32 * PITCH;
@@ -341,6 +375,14 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
     const int vr = v0 + m0 * 32;
     const int col = (GATED ? vr / 2 : vr) + 8 * c;
     float b[8], bu[8];
+    float sc[8], su[8];                                       // (FP8 W)
+    if constexpr (C::kW8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sc[e] = w_scale[wrow_of<GATED>(vr + lr + e, d_out)];
+        su[e] = GATED ? w_scale[wrow_of<GATED>(vr + lr + 16 + e, d_out)] : 0.f;
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       b[e] = epi.bias ? elem_f32<uint16_t>(epi.bias, wrow_of<GATED>(vr + lr + e, d_out)) : 0.f;
@@ -378,11 +420,15 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
           u1 = *(const f32x4_t*)(tr + 80);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = (e < 4 ? z0[e] : z1[e - 4]) + b[e];
+        for (int e = 0; e < 8; ++e) {
+          const float z = e < 4 ? z0[e] : z1[e - 4];
+          o[e] = C::kW8 ? fmaf(z, sc[e], b[e]) : z + b[e];
+        }
         activate_n<true>(o, epi.act);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if constexpr (GATED) o[e] *= (e < 4 ? u0[e] : u1[e - 4]) + bu[e];
+          const float u = e < 4 ? u0[e] : u1[e - 4];
+          if constexpr (GATED) o[e] *= C::kW8 ? fmaf(u, su[e], bu[e]) : u + bu[e];
           if (res) o[e] += r8[e];
         }
         if (vec) {
@@ -401,19 +447,21 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
 // p0 .. p0 + WT - 1 below p_end, position p to row p of y, bias added.
 template <class C>
 __device__ __forceinline__ void store_f32(f32x16_t (&acc)[C::MR][C::MT], char* lds, int wave, int lane, int v0, int p0,
-                                          int p_end, int d_out, const uint16_t* bias, float* y) {
-  constexpr int MC = C::MR >= 2 ? C::MR / 2 : 1;   // row blocks per pass through the LDS tile, as store_epilogue
+                                          int p_end, int d_out, const uint16_t* bias, const float* w_scale, float* y) {
+  constexpr int MC = C::EPI_MC;   // row blocks per pass through the LDS tile, as store_epilogue
   constexpr int PITCH = MC * 128 + 16, CPR = MC * 8, PPP = kWave / CPR;
-  static_assert(C::NW * 32 * PITCH <= C::LDS_BYTES, "tile fits the LDS");
   const int l32 = lane % 32, h = lane / 32, c = lane % CPR;
   char* tile = lds + wave * 32 * PITCH;
   const bool vec = d_out % 4 == 0;
 #pragma unroll
   for (int m0 = 0; m0 < C::MR; m0 += MC) {
     const int col = v0 + m0 * 32 + 4 * c;
-    float b[4];
+    float b[4], sc[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = bias ? elem_f32<uint16_t>(bias, min(col + i, d_out - 1)) : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      b[i] = bias ? elem_f32<uint16_t>(bias, min(col + i, d_out - 1)) : 0.f;
+      sc[i] = C::kW8 ? w_scale[min(col + i, d_out - 1)] : 1.f;
+    }
 #pragma unroll
     for (int n = 0; n < C::MT; ++n) {
 #pragma unroll
@@ -428,7 +476,7 @@ __device__ __forceinline__ void store_f32(f32x16_t (&acc)[C::MR][C::MT], char* l
         if (p >= p_end || col >= d_out) continue;
         f32x4_t z = *(const f32x4_t*)(tile + tl * PITCH + 16 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] += b[i];
+        for (int i = 0; i < 4; ++i) z[i] = C::kW8 ? fmaf(z[i], sc[i], b[i]) : z[i] + b[i];
         float* dst = y + (long long)p * d_out + col;
         if (vec) *(f32x4_t*)dst = z;
         else

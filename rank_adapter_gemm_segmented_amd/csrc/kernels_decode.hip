@@ -51,26 +51,6 @@ __device__ __forceinline__ long long part_off(int c, int i, int rb, int tb, int 
   return ((((long long)c * n_tiles + i) * 4 + rb) * ntb + tb) * 256;
 }
 
-
-// Eight FP8 e4m3 codes (OCP E4M3: bias 7, subnormals m/8 * 2^-6) -> eight
-// bf16 values, exact: every e4m3 value has at most 4 significant bits and an
-// exponent inside bf16's range. gfx950's scaled conversion turns two codes
-// into two bf16 per instruction (scale 1; checked against the E4M3
-// definition on all 256 codes).
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-template <bool HI>
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
-}
-__device__ __forceinline__ u32x4_t e4m3x8_to_bf16x8(uint32_t lo, uint32_t hi) {
-  u32x4_t r;
-  r.x = e4m3x2_to_bf16x2<false>(lo);
-  r.y = e4m3x2_to_bf16x2<true>(lo);
-  r.z = e4m3x2_to_bf16x2<false>(hi);
-  r.w = e4m3x2_to_bf16x2<true>(hi);
-  return r;
-}
-
 // W8: W holds FP8 e4m3 codes (one byte per element, a float32 scale per row
 // applied by k_finish). A lane's 16-byte load then covers 16 columns, which
 // serve two consecutive k-steps: lane group g = l / 16 of the step pair
@@ -265,7 +245,7 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
       const int kp = min(ks_begin + (s & ~1), kDecMaxKc / 32 - 2);   // the step pair's first step
       xc = kp * 32 + 2 * kq + 8 * (s & 1);
       const u32x4_t raw = wr[s / 2];
-      wop = (s & 1) ? e4m3x8_to_bf16x8(raw.z, raw.w) : e4m3x8_to_bf16x8(raw.x, raw.y);
+      wop = (s & 1) ? e4m3x8_bf16(raw.z, raw.w) : e4m3x8_bf16(raw.x, raw.y);
     } else {
       xc = min(ks_begin + s, kDecMaxKc / 32 - 1) * 32 + kq;
       wop = wr[s];

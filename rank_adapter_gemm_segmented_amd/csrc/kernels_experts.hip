@@ -22,17 +22,6 @@ __device__ __forceinline__ f32x4_t mfma16e(u32x4_t a, u32x4_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-// Two e4m3 codes -> two bf16 (exact), as in the decode kernel.
-template <bool HI>
-__device__ __forceinline__ uint32_t e4m3x2_bf16(uint32_t w) {
-  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-  bf16x2_t r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI);
-  return __builtin_bit_cast(uint32_t, r);
-}
-__device__ __forceinline__ u32x4_t e4m3x8_bf16(uint32_t lo, uint32_t hi) {
-  return u32x4_t{e4m3x2_bf16<false>(lo), e4m3x2_bf16<true>(lo), e4m3x2_bf16<false>(hi), e4m3x2_bf16<true>(hi)};
-}
-
 constexpr int kXBf16 = 0, kXFp8w = 1, kXF32 = 2;   // element types of the streaming kernel
 
 // ---------------------------------------------------------------------------
@@ -238,7 +227,7 @@ template <class C, int OUT, bool PIPE>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW / 4, C::NW / 4)))
 void k_experts_tile(ExpertsArgs a, int n_rt, int rg) {
   constexpr bool GATED = OUT == 1;
-  __shared__ __attribute__((aligned(1024))) char lds[C::LDS_BYTES];
+  __shared__ __attribute__((aligned(1024))) char lds[C::TILE_BYTES];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int nrx = (n_rt + 7) / 8;                        // row tiles per XCD
   const int j = blockIdx.x >> 3;
@@ -249,11 +238,12 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int rg) {
   const int e = find_expert(a.seg_start, a.E, a.n_pos, C::kBT, run, &p0, &p1);
   if (e < 0) return;   // uniform: past the last run
   const int d_in = a.d_in, d_out = a.d_out, r0 = rt * C::kBR;
-  const uint16_t* __restrict__ W = (const uint16_t*)a.W + (long long)e * d_out * d_in;
+  constexpr int WB = C::kW8 ? 1 : 2;                     // bytes per W element
+  const char* __restrict__ W = (const char*)a.W + (long long)e * d_out * d_in * WB;
   const uint16_t* __restrict__ x = (const uint16_t*)a.x;
 
   TileSrc<C> src;
-  src.set(wave, lane, [&](int r) { return W + (long long)wrow_of<GATED>(r0 + r, d_out) * d_in; },
+  src.set(wave, lane, [&](int r) { return W + (long long)wrow_of<GATED>(r0 + r, d_out) * d_in * WB; },
           [&](int r) {
             const int p = min(p0 + r, p1 - 1);           // (absent positions repeat the last)
             const int row = a.token_index ? a.token_index[p] : p;
@@ -267,16 +257,17 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int rg) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.f;
   if constexpr (PIPE) pipe_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
-  else ring_mainloop<C, false>(src, d_in, expert_zeros, lds, wave, lane, acc);
+  else ring_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
 
   const int wr = wave / C::NWT, wt = wave % C::NWT;
   const int v0 = r0 + wr * C::kWR, pw = p0 + wt * C::kWT;
   EpiView epi = a.epi;
   if (epi.bias) epi.bias = (const uint16_t*)epi.bias + (long long)e * d_out;
+  const float* ws = C::kW8 ? a.w_scale + (long long)e * d_out : nullptr;
   if constexpr (OUT == 2) {
-    store_f32<C>(acc, lds, wave, lane, v0, pw, p1, d_out, (const uint16_t*)epi.bias, (float*)a.y);
+    store_f32<C>(acc, lds, wave, lane, v0, pw, p1, d_out, (const uint16_t*)epi.bias, ws, (float*)a.y);
   } else {
-    store_epilogue<C, GATED>(acc, lds, wave, lane, v0, pw, p1, d_out, epi, a.y, [](int p) { return p; });
+    store_epilogue<C, GATED>(acc, lds, wave, lane, v0, pw, p1, d_out, epi, ws, a.y, [](int p) { return p; });
   }
 }
 
@@ -362,17 +353,41 @@ static void launch_tile(const ExpertsArgs& a, hipStream_t st) {
 }
 
 typedef GCfg<256, 256, 128, 128, 4, 32, 4> Tile256;
-typedef GCfg<128, 128, 64, 32, 3, 64, 3> Tile128;
-typedef GCfg<64, 128, 32, 32, 4, 64, 4> Tile64;
+template <bool W8> using Tile128 = GCfg<128, 128, 64, 32, 3, W8 ? 128 : 64, W8 ? 2 : 3, W8>;
+template <bool W8> using Tile64 = GCfg<128, 64, 32, 32, 4, W8 ? 128 : 64, 4, W8>;
+typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
+
+// Form by the rows per expert. Up to two (FP8: twelve), the streaming form; it
+// also takes what has too few tiles for the card, and fp32. Then tiles of 32, 64,
+// 128 and 256 positions, the smallest that holds most experts' rows: W, which
+// decides the time up to about 100 rows, is then read once, and the tile's
+// rings keep more of it requested than registers can. Two of eight experts,
+// 4096 -> 2 x 14336, bf16, us: 16 tokens 316 with 32 positions, 337 streamed; 64
+// tokens 322 with 64, 390 streamed; 128 tokens 342 with 64, 360 with 128; 256
+// tokens 378 with 128, 451 with 64; 512 tokens 532 with 256, 557 with 128. FP8
+// halves W, not the tile's work: 32 tokens 179 streamed, 204 with 64 positions;
+// 128 tokens 230 with 64, 284 streamed. (FP8 stages are 128 columns deep: 237
+// with 64.)
+template <bool W8>
+static void launch_bf16(const ExpertsArgs& a, hipStream_t st) {
+  const long long active = std::min(a.E, a.n_pos);
+  const double mean = (double)a.n_pos / active;
+  const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  const long long tiles256 = (rows + 255) / 256 * (a.n_pos / 256 + active / 2);   // of about this many
+  if (mean <= (W8 ? 12 : 2) || (rows + 127) / 128 * active < 256) return launch_stream<W8 ? kXFp8w : kXBf16>(a, st);
+  if constexpr (!W8) {
+    if (mean <= 8) return launch_tile<Tile32, false>(a, st);
+    if (mean >= 192 || (mean >= 112 && tiles256 >= 1024)) return launch_tile<Tile256, true>(a, st);
+  }
+  if (mean <= 48) launch_tile<Tile64<W8>, false>(a, st);
+  else launch_tile<Tile128<W8>, false>(a, st);
+}
 
 void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st) {
   if (a.n_pos <= 0) return;
-  const int mean = a.n_pos / std::min(a.E, a.n_pos);   // positions per expert
-  if (bf16 && !a.w_scale && mean >= 192) return launch_tile<Tile256, true>(a, st);
-  if (bf16 && !a.w_scale && mean >= 64) return launch_tile<Tile128, false>(a, st);
   if (!bf16) launch_stream<kXF32>(a, st);
-  else if (a.w_scale) launch_stream<kXFp8w>(a, st);
-  else launch_stream<kXBf16>(a, st);
+  else if (a.w_scale) launch_bf16<true>(a, st);
+  else launch_bf16<false>(a, st);
 }
 
 void launch_combine(const CombineArgs& a, bool bf16, hipStream_t st) {

@@ -1100,8 +1100,9 @@ void k_gemm2(LinearArgs a) {
   static_assert(C::NW * WT * YP <= C::LDS_BYTES, "y tile fits the LDS");
   if (a.lora_on && !a.delta) __syncthreads();          // the expand's LDS reads are done
   if constexpr (EPI != kEpiNone) {
+    static_assert(C::EPI_BYTES <= C::LDS_BYTES, "epilogue tile fits the LDS");
     auto row_of = [&](int p) { return a.sv.token_index ? min(max(a.sv.token_index[p], 0), T - 1) : p; };
-    store_epilogue<C, GATED>(acc, (char*)lds, wave, lane, r0 + wr * WR, t0 + wt * WT, T, d_out, a.epi, a.y, row_of);
+    store_epilogue<C, GATED>(acc, (char*)lds, wave, lane, r0 + wr * WR, t0 + wt * WT, T, d_out, a.epi, nullptr, a.y, row_of);
     return;
   }
   uint16_t* __restrict__ y = (uint16_t*)a.y;
