@@ -41,6 +41,12 @@ __device__ __forceinline__ void dma16_nt(const void* g, uint32_t m0) {
                : "memory", "m0");
 }
 
+// The same with a uniform base and a 32-bit byte offset per lane.
+__device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m0)
+               : "memory", "m0");
+}
+
 template <int N>
 __device__ __forceinline__ void vm_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -156,6 +162,46 @@ struct TileSrc {
   }
 };
 
+// The rows of the largest tile (below): as TileSrc, but a uniform base each for
+// W and x and a 32-bit byte offset per lane and load, so that a load in the main
+// loop costs no vector instruction but itself. (With a 64-bit address and a
+// select against `zeros` per load, 7 to 9 instructions between two MFMAs, the
+// wave fell behind its MFMAs: 1990 to 2095 us for the largest case.)
+// The caller keeps W's tile and all of x within 4 GB of their bases.
+template <class C>
+struct PipeSrc {
+  static_assert(C::kKB == 32 && C::kNB == C::kNX && !C::kW8, "one chunk column per lane, one request order");
+  const char* wb;
+  const char* xb;
+  uint32_t off[C::DPW];
+  int scol;                                               // first column of the lane's chunk, of every load
+  template <class WOff, class XOff>
+  __device__ __forceinline__ void set(int wave, int lane, const void* w, const void* x, WOff woff, XOff xoff) {
+    wb = (const char*)w;
+    xb = (const char*)x;
+    // row r = 16 J + lane / 4 of chunk J: r mod 16 and with it the swizzle go by the lane alone
+    const int c = (lane % 4) ^ gswz<32>(lane / 4);
+    scol = 8 * c;
+#pragma unroll
+    for (int i = 0; i < C::DPW; ++i) {
+      const bool isx = i >= C::DPW_W;
+      const int r = ((isx ? i - C::DPW_W : i) * C::NW + wave) * 16 + lane / 4;
+      off[i] = (isx ? xoff(r) : woff(r)) + 16 * c;
+    }
+  }
+  // load I of stage st; WHOLE: the stage lies inside d_in
+  template <int I, bool WHOLE>
+  __device__ __forceinline__ void issue(int st, uint32_t lds0, int wave, int d_in, const void* zeros) const {
+    constexpr bool isx = I >= C::DPW_W;
+    constexpr int j = isx ? I - C::DPW_W : I;
+    const uint32_t at = (isx ? lds0 + C::XRING + (uint32_t)(st % C::kNX) * C::XSTAGE_B
+                             : lds0 + (uint32_t)(st % C::kNB) * C::WSTAGE_B) + (uint32_t)(j * C::NW + wave) * 1024;
+    const char* base = (isx ? xb : wb) + (long long)st * (2 * C::kKB);
+    if constexpr (WHOLE) dma16_off(base, off[I], at);
+    else dma16(sel_addr(st * C::kKB + scol < d_in, base + off[I], zeros), at);
+  }
+};
+
 // Main loop of the largest tile: 4 waves, one per SIMD, each 128 x 128 of a 256
 // x 256 tile. A SIMD then has no second wave to cover a barrier or an LDS read
 // with, so the loop is laid out by hand: MFMA by MFMA, with the reads of the
@@ -171,9 +217,9 @@ struct TileSrc {
 // whole and this one's slots are free. The first fragments of the next stage
 // are read under the remaining MFMAs.
 template <class C>
-__device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, const void* zeros, char* lds,
+__device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, const void* zeros, char* lds,
                                               int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
-  constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = KB / 16;
+  constexpr int KB = C::kKB, NB = C::kNB, KS = KB / 16;
   constexpr int MR = C::MR, MT = C::MT, NM = MR * MT, NF = MR + MT;
   constexpr int H = NM / 4;
   static_assert(KS % 2 == 0, "fragment sets alternate within a stage");
@@ -191,58 +237,36 @@ __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, con
       const int m = f == 0 ? 0 : f - MT;
       fa[set][m] = *(const u32x4_t*)(lds + (st % NB) * C::WSTAGE_B + wbase + m * 32 * C::RB + fcol[kk]);
     } else {
-      fb[set][f - 1] = *(const u32x4_t*)(lds + (st % NX) * C::XSTAGE_B + xbase + (f - 1) * 32 * C::RB + fcol[kk]);
+      fb[set][f - 1] = *(const u32x4_t*)(lds + (st % NB) * C::XSTAGE_B + xbase + (f - 1) * 32 * C::RB + fcol[kk]);
     }
-  };
-  auto load_w = [&](int st) {
-    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I>(st, lds0, wave, d_in, zeros), ...); }
-    (std::make_integer_sequence<int, C::DPW_W>{});
-  };
-  auto load_x = [&](int st) {
-    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I>(st, lds0, wave, d_in, zeros), ...); }
-    (std::make_integer_sequence<int, C::DPW_X>{});
   };
   auto mfma = [&](int set, int i) {
     acc[i / MT][i % MT] = mfma32g(fa[set][i / MT], fb[set][i % MT], acc[i / MT][i % MT]);
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  // Iteration t of the loop requests W stage t + NB and position stage t + NX
-  // into the slots that stage t has freed, one load per few MFMAs (a burst of
-  // them holds up the wave at issue: 2135 us for the largest case, against
-  // 1992 spread over 24 of a stage's 32 MFMAs and 1995 over all of them): the
-  // first D1 under the rest of stage t's last k-step, the others under stage
-  // t + 1 before its own boundary.
+  // Iteration t of the loop requests stage t + NB into the slots that stage t
+  // has freed, one load per few MFMAs (a burst of them holds up the wave at
+  // issue: 2135 us for the largest case, against 1992 spread over 24 of a
+  // stage's 32 MFMAs and 1995 over all of them): the first D1 under the rest of
+  // stage t's last k-step, the others under stage t + 1 before its own boundary.
   constexpr int NS = KS * NM;                            // MFMAs of a stage
   constexpr int SP = NS * 3 / 4;                         // over which its requests are spread
   auto upto = [](int i) constexpr { return i >= SP ? C::DPW : i * C::DPW / SP; };
   constexpr int D1 = upto(NM - H);
-  auto request = [&]<int L0, int N>(int t, std::integral_constant<int, L0>, std::integral_constant<int, N>) {
-    [&]<int... J>(std::integer_sequence<int, J...>) {
-      (s.template issue<L0 + J>(L0 + J < C::DPW_W ? t + NB : t + NX, lds0, wave, d_in, zeros), ...);
-    }(std::make_integer_sequence<int, N>{});
+  auto request = [&]<bool WHOLE, int L0, int N>(std::bool_constant<WHOLE>, int t, std::integral_constant<int, L0>,
+                                                std::integral_constant<int, N>) {
+    [&]<int... J>(std::integer_sequence<int, J...>) { (s.template issue<L0 + J, WHOLE>(t + NB, lds0, wave, d_in, zeros), ...); }
+    (std::make_integer_sequence<int, N>{});
     if constexpr (N > 0) __builtin_amdgcn_sched_barrier(0);
   };
   // what is requested after MFMA I of a stage (counted from the boundary before it)
-  auto request_at = [&]<int I>(int t, std::integral_constant<int, I>) {
+  auto request_at = [&]<int I>(auto whole, int t, std::integral_constant<int, I>) {
     constexpr int L0 = upto(I), L1 = upto(I + 1);
-    request(t, std::integral_constant<int, L0>{}, std::integral_constant<int, L1 - L0>{});
+    request(whole, t, std::integral_constant<int, L0>{}, std::integral_constant<int, L1 - L0>{});
   };
   auto each = []<int... I>(std::integer_sequence<int, I...>, auto f) { (f(std::integral_constant<int, I>{}), ...); };
-
-  const int nst = (d_in + KB - 1) / KB;
-  // requests of the iterations before the first (of those only that exist:
-  // position stages start NB - NX iterations later), the last one's first part only
-#pragma unroll
-  for (int t = -NB; t < -1; ++t) {
-    load_w(t + NB);
-    if (t + NX >= 0) load_x(t + NX);
-  }
-  request(-1, std::integral_constant<int, 0>{}, std::integral_constant<int, D1>{});
-  vm_barrier<(NX - 2) * C::DPW + D1>();
-#pragma unroll
-  for (int f = 0; f < NF; ++f) frag(0, 0, 0, f);
-  for (int st = 0; st < nst; ++st) {
+  auto stage = [&](auto whole, int st) {
     each(std::make_integer_sequence<int, (KS - 1) * NM>{}, [&](auto ic) {
       constexpr int I = ic.value, kk = I / NM, i = I % NM;
       mfma(kk & 1, i);
@@ -250,12 +274,12 @@ __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, con
         frag(st, kk + 1, (kk + 1) & 1, i * NF / NM);
         __builtin_amdgcn_sched_barrier(0);
       }
-      request_at(st - 1, std::integral_constant<int, NM - H + I>{});
+      request_at(whole, st - 1, std::integral_constant<int, NM - H + I>{});
     });
     constexpr int LS = (KS - 1) & 1;
     each(std::make_integer_sequence<int, H>{}, [&](auto ic) {
       mfma(LS, ic.value);
-      request_at(st - 1, std::integral_constant<int, NS - H + ic.value>{});
+      request_at(whole, st - 1, std::integral_constant<int, NS - H + ic.value>{});
     });
     vm_barrier<C::VMC>();
     __builtin_amdgcn_sched_barrier(0);
@@ -264,9 +288,22 @@ __device__ __forceinline__ void pipe_mainloop(const TileSrc<C>& s, int d_in, con
       mfma(LS, H + I);
       if constexpr (I < NF) frag(st + 1, 0, 0, I);
       __builtin_amdgcn_sched_barrier(0);
-      request_at(st, ic);
+      request_at(whole, st, ic);
     });
-  }
+  };
+
+  const int nst = (d_in + KB - 1) / KB, nwhole = d_in / KB;
+  constexpr std::false_type part{};
+  // the iterations before the first, the last of them its first part only
+#pragma unroll
+  for (int t = -NB; t < -1; ++t) request(part, t, std::integral_constant<int, 0>{}, std::integral_constant<int, C::DPW>{});
+  request(part, -1, std::integral_constant<int, 0>{}, std::integral_constant<int, D1>{});
+  vm_barrier<(NB - 2) * C::DPW + D1>();
+#pragma unroll
+  for (int f = 0; f < NF; ++f) frag(0, 0, 0, f);
+  int st = 0;
+  for (; st + NB < nwhole; ++st) stage(std::true_type{}, st);   // every request is a whole stage
+  for (; st < nst; ++st) stage(part, st);
   vm_barrier<0>();   // the ring's last loads (zeros) land before the LDS is reused
 }
 

@@ -242,13 +242,11 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int rg) {
   const char* __restrict__ W = (const char*)a.W + (long long)e * d_out * d_in * WB;
   const uint16_t* __restrict__ x = (const uint16_t*)a.x;
 
-  TileSrc<C> src;
-  src.set(wave, lane, [&](int r) { return W + (long long)wrow_of<GATED>(r0 + r, d_out) * d_in * WB; },
-          [&](int r) {
-            const int p = min(p0 + r, p1 - 1);           // (absent positions repeat the last)
-            const int row = a.token_index ? a.token_index[p] : p;
-            return x + (long long)min(max(row, 0), a.n_rows - 1) * d_in;
-          });
+  auto row_of = [&](int r) {
+    const int p = min(p0 + r, p1 - 1);                   // (absent positions repeat the last)
+    const int row = a.token_index ? a.token_index[p] : p;
+    return min(max(row, 0), a.n_rows - 1);
+  };
   f32x16_t acc[C::MR][C::MT];
 #pragma unroll
   for (int m = 0; m < C::MR; ++m)
@@ -256,8 +254,21 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int rg) {
     for (int n = 0; n < C::MT; ++n)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.f;
-  if constexpr (PIPE) pipe_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
-  else ring_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
+  if constexpr (PIPE) {
+    // W offsets from the tile's first row (gated: its first gate row; the up
+    // rows lie d_out / 2 rows further)
+    const int w0 = wrow_of<GATED>(r0, d_out);
+    PipeSrc<C> src;
+    src.set(wave, lane, W + (long long)w0 * d_in * 2, x,
+            [&](int r) { return (uint32_t)(wrow_of<GATED>(r0 + r, d_out) - w0) * (uint32_t)(2 * d_in); },
+            [&](int r) { return (uint32_t)row_of(r) * (uint32_t)(2 * d_in); });
+    pipe_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
+  } else {
+    TileSrc<C> src;
+    src.set(wave, lane, [&](int r) { return W + (long long)wrow_of<GATED>(r0 + r, d_out) * d_in * WB; },
+            [&](int r) { return x + (long long)row_of(r) * d_in; });
+    ring_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
+  }
 
   const int wr = wave / C::NWT, wt = wave % C::NWT;
   const int v0 = r0 + wr * C::kWR, pw = p0 + wt * C::kWT;
@@ -357,7 +368,7 @@ template <bool W8> using Tile128 = GCfg<128, 128, 64, 32, 3, W8 ? 128 : 64, W8 ?
 template <bool W8> using Tile64 = GCfg<128, 64, 32, 32, 4, W8 ? 128 : 64, 4, W8>;
 typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
 
-// Form by the rows per expert. Up to two (FP8: twelve), the streaming form; it
+// Form by the rows per expert. Up to two (FP8: twenty), the streaming form; it
 // also takes what has too few tiles for the card, and fp32. Then tiles of 32, 64,
 // 128 and 256 positions, the smallest that holds most experts' rows: W, which
 // decides the time up to about 100 rows, is then read once, and the tile's
@@ -365,7 +376,7 @@ typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
 // 4096 -> 2 x 14336, bf16, us: 16 tokens 316 with 32 positions, 337 streamed; 64
 // tokens 322 with 64, 390 streamed; 128 tokens 342 with 64, 360 with 128; 256
 // tokens 378 with 128, 451 with 64; 512 tokens 532 with 256, 557 with 128. FP8
-// halves W, not the tile's work: 32 tokens 179 streamed, 204 with 64 positions;
+// halves W, not the tile's work: 64 tokens 201 streamed, 222 with 64 positions;
 // 128 tokens 230 with 64, 284 streamed. (FP8 stages are 128 columns deep: 237
 // with 64.)
 template <bool W8>
@@ -373,11 +384,13 @@ static void launch_bf16(const ExpertsArgs& a, hipStream_t st) {
   const long long active = std::min(a.E, a.n_pos);
   const double mean = (double)a.n_pos / active;
   const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  // the largest tile addresses x and its rows of W by 32-bit offsets
+  const bool near = 2ll * a.n_rows * a.d_in < (1ll << 32) && (a.gated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
   const long long tiles256 = (rows + 255) / 256 * (a.n_pos / 256 + active / 2);   // of about this many
-  if (mean <= (W8 ? 12 : 2) || (rows + 127) / 128 * active < 256) return launch_stream<W8 ? kXFp8w : kXBf16>(a, st);
+  if (mean <= (W8 ? 20 : 2) || (rows + 127) / 128 * active < 256) return launch_stream<W8 ? kXFp8w : kXBf16>(a, st);
   if constexpr (!W8) {
     if (mean <= 8) return launch_tile<Tile32, false>(a, st);
-    if (mean >= 192 || (mean >= 112 && tiles256 >= 1024)) return launch_tile<Tile256, true>(a, st);
+    if (near && (mean >= 192 || (mean >= 112 && tiles256 >= 1024))) return launch_tile<Tile256, true>(a, st);
   }
   if (mean <= 48) launch_tile<Tile64<W8>, false>(a, st);
   else launch_tile<Tile128<W8>, false>(a, st);
