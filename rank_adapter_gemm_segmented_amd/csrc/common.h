@@ -25,6 +25,13 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) {
   return __uint_as_float(((uint32_t)b) << 16);
 }
 
+// Two floats -> two bf16 in one word (RNE, one instruction on gfx950).
+__device__ __forceinline__ uint32_t cvt_pk_bf16(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
 // Pack 8 floats into a bf16x8 operand (RNE).
 __device__ __forceinline__ bf16x8_t pack_bf16x8(const float* v) {
   u32x4_t r;

@@ -79,4 +79,18 @@ __device__ __forceinline__ int find_expert(const int32_t* __restrict__ seg_start
   return -1;
 }
 
+// Runs of at most BT positions in all.
+__device__ __forceinline__ int count_runs(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT) {
+  const int lane = threadIdx.x % kWave;
+  int n = 0;
+  for (int e0 = 0; e0 < E; e0 += kWave) {
+    const int e = min(e0 + lane, E - 1);
+    const int s0 = min(max(seg_start[e], 0), n_pos), s1 = min(max(seg_start[e + 1], 0), n_pos);
+    n += e0 + lane < E ? (max(s1 - s0, 0) + BT - 1) / BT : 0;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
 }  // namespace mlora

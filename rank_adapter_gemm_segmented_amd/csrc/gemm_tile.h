@@ -469,7 +469,7 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
           if (res) o[e] += r8[e];
         }
         if (vec) {
-          *(u32x4_t*)(y + at) = __builtin_bit_cast(u32x4_t, pack_bf16x8(o));
+          *(u32x4_t*)(y + at) = u32x4_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]), cvt_pk_bf16(o[6], o[7])};
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)

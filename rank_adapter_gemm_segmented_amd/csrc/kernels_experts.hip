@@ -210,38 +210,48 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiled form (bf16, more rows per expert): a workgroup takes BR (virtual) rows
-// of one expert by a run of up to BT of its positions over the whole of d_in.
+// Tiled form (more rows per expert): a workgroup takes BR (virtual) rows of one
+// expert by a run of up to BT of its positions over the whole of d_in.
 //
-// Block order: block b runs on XCD b % 8, which takes row tiles xcd, xcd + 8, ...
-// and for each of them a group of rg runs one after another, then the next
-// group: the runs of an expert that are in flight on an XCD share its L2's copy
-// of W, which is read from memory once per group, and the row tiles in flight
-// share the rows of x. Groups of 16 runs hold whole experts of a prefill batch
-// (8 experts of about 1024 rows: 1934 us against 1957 with 8 and 1992 with 4);
-// where an expert has one or two runs they share no W, and short groups leave
-// more row tiles to share x.
+// Order of the tiles: block b runs on XCD b % 8, which takes row tiles xcd, xcd +
+// 8, ... : groups of rg runs, in a group row tile by row tile, its runs side by
+// side. The runs of an expert that are in flight on an XCD share its L2's copy
+// of W, which is read from memory once per group, the row tiles in flight share
+// the rows of x, and the XCDs read neighbouring rows of W at the same time (an
+// eighth of the row tiles in a row for each XCD: 1167 us against 1072, way back of
+// a prefill batch). Groups of 16 runs hold whole experts of such a batch (8
+// experts of about 1024 rows: 1934 us against 1957 with 8 and 1992 with 4); where
+// an expert has one or two runs they share no W, and short groups leave more
+// row tiles to share x. The last n_rt % 8 row tiles go round the XCDs run by run.
 // ---------------------------------------------------------------------------
+
+// Tiles of XCD x among `runs` runs by n_rt row tiles, and the j-th of them.
+__host__ __device__ __forceinline__ int xcd_tiles(int x, int runs, int n_rt) {
+  return n_rt / 8 * runs + (n_rt % 8 * runs - x + 7) / 8;
+}
+__device__ __forceinline__ void xcd_tile(int j, int x, int runs, int n_rt, int rg, int* rt, int* run) {
+  const int n8 = n_rt / 8;
+  if (j < n8 * runs) {
+    const int group = j / (n8 * rg), k = j - group * n8 * rg, gs = max(min(rg, runs - group * rg), 1);
+    *rt = k / gs * 8 + x;
+    *run = group * rg + k % gs;
+  } else {
+    const int k = (j - n8 * runs) * 8 + x;
+    *rt = n8 * 8 + k / runs;
+    *run = k % runs;
+  }
+}
+
+// One tile: rows r0 .. r0 + BR - 1 by positions p0 .. min(p0 + BT, p1) - 1.
 // OUT: 0 bf16 rows, 1 bf16 rows of a gated product, 2 fp32 rows (no activation)
 template <class C, int OUT, bool PIPE>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW / 4, C::NW / 4)))
-void k_experts_tile(ExpertsArgs a, int n_rt, int rg) {
+__device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0, int p1, int r0, char* lds) {
   constexpr bool GATED = OUT == 1;
-  __shared__ __attribute__((aligned(1024))) char lds[C::TILE_BYTES];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
-  const int nrx = (n_rt + 7) / 8;                        // row tiles per XCD
-  const int j = blockIdx.x >> 3;
-  const int rt = (j / rg % nrx) * 8 + (blockIdx.x & 7);
-  const int run = j / (rg * nrx) * rg + j % rg;
-  if (rt >= n_rt) return;
-  int p0, p1;
-  const int e = find_expert(a.seg_start, a.E, a.n_pos, C::kBT, run, &p0, &p1);
-  if (e < 0) return;   // uniform: past the last run
-  const int d_in = a.d_in, d_out = a.d_out, r0 = rt * C::kBR;
   constexpr int WB = C::kW8 ? 1 : 2;                     // bytes per W element
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int d_in = a.d_in, d_out = a.d_out;
   const char* __restrict__ W = (const char*)a.W + (long long)e * d_out * d_in * WB;
   const uint16_t* __restrict__ x = (const uint16_t*)a.x;
-
   auto row_of = [&](int r) {
     const int p = min(p0 + r, p1 - 1);                   // (absent positions repeat the last)
     const int row = a.token_index ? a.token_index[p] : p;
@@ -280,6 +290,55 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int rg) {
   } else {
     store_epilogue<C, GATED>(acc, lds, wave, lane, v0, pw, p1, d_out, epi, ws, a.y, [](int p) { return p; });
   }
+}
+
+template <class C, int OUT>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW / 4, C::NW / 4)))
+void k_experts_tile(ExpertsArgs a, int n_rt, int rg, int max_runs) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::TILE_BYTES];
+  const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
+  if (j >= xcd_tiles(x, max_runs, n_rt)) return;   // uniform
+  int rt, run, p0, p1;
+  xcd_tile(j, x, max_runs, n_rt, rg, &rt, &run);   // (of the most runs there can be: the rest find no expert)
+  const int e = find_expert(a.seg_start, a.E, a.n_pos, C::kBT, run, &p0, &p1);
+  if (e < 0) return;   // uniform
+  expert_tile<C, OUT, false>(a, e, p0, p1, rt * C::kBR, lds);
+}
+
+// The largest tile, 256 x 256, and what it leaves. An XCD's 32 CUs take its
+// tiles in rounds of 32; those of a last round that would keep a quarter or a
+// half of them busy are cut into four (128 x 128) or two (256 x 128) for all of
+// them (the way back of a prefill batch, 72 tiles per XCD: 1067 -> us). A run
+// of at most 128 positions takes the 256 x 128 form too.
+typedef GCfg<256, 256, 128, 128, 4, 32, 4> Tile256;
+typedef GCfg<256, 128, 128, 64, 5, 32, 5> Tile256Half;
+typedef GCfg<128, 128, 64, 64, 8, 32, 8> Tile256Quarter;
+constexpr int kXcdCus = 32;
+
+template <int OUT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void k_experts_tile256(ExpertsArgs a, int n_rt, int rg, int max_runs) {
+  __shared__ __attribute__((aligned(1024))) char lds[Tile256::TILE_BYTES];
+  static_assert(Tile256Half::TILE_BYTES <= Tile256::TILE_BYTES && Tile256Quarter::TILE_BYTES <= Tile256::TILE_BYTES, "one LDS block");
+  const int runs = min(count_runs(a.seg_start, a.E, a.n_pos, 256), max_runs);   // (more: overlapping segments)
+  const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
+  const int mine = xcd_tiles(x, runs, n_rt);
+  const int whole = mine / kXcdCus * kXcdCus, rem = mine - whole;
+  const int cut = rem <= kXcdCus / 4 ? 4 : rem <= kXcdCus / 2 ? 2 : 1;
+  if (j >= whole + rem * cut) return;   // uniform: past the XCD's last tile
+  const int i = j < whole ? j : whole + (j - whole) / cut, piece = j < whole ? 0 : (j - whole) % cut;
+  const int parts = j < whole ? 1 : cut;
+  int rt, run, p0, p1;
+  xcd_tile(i, x, runs, n_rt, rg, &rt, &run);
+  const int e = find_expert(a.seg_start, a.E, a.n_pos, 256, run, &p0, &p1);
+  if (e < 0) return;
+  // (parts 4: piece & 1 the row half, piece >> 1 the position half; parts 2: the position half)
+  const int ph = parts == 4 ? piece >> 1 : piece;
+  const int q0 = p0 + 128 * ph;
+  if (q0 >= p1) return;
+  if (parts == 4) expert_tile<Tile256Quarter, OUT, true>(a, e, q0, min(p1, q0 + 128), rt * 256 + 128 * (piece & 1), lds);
+  else if (parts == 2 || p1 - p0 <= 128) expert_tile<Tile256Half, OUT, true>(a, e, q0, min(p1, q0 + 128), rt * 256, lds);
+  else expert_tile<Tile256, OUT, true>(a, e, p0, p1, rt * 256, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -351,19 +410,33 @@ static void launch_stream(const ExpertsArgs& a, hipStream_t st) {
   else launch_stream_n<TYPE, 4, 4, 4>(a, st);
 }
 
-template <class C, bool PIPE>
-static void launch_tile(const ExpertsArgs& a, hipStream_t st) {
-  const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
-  const int n_rt = (rows + C::kBR - 1) / C::kBR;
-  const int rg = a.n_pos / std::min(a.E, a.n_pos) >= 2 * C::kBT ? 16 : 4;   // runs per group, by the rows per expert
-  const long long groups = (run_bound(a, C::kBT) + rg - 1) / rg;
-  const dim3 grid((unsigned)(8 * ((n_rt + 7) / 8) * rg * groups)), block(C::NT);
-  if (a.f32_out) hipLaunchKernelGGL((k_experts_tile<C, 2, PIPE>), grid, block, 0, st, a, n_rt, rg);
-  else if (a.gated) hipLaunchKernelGGL((k_experts_tile<C, 1, PIPE>), grid, block, 0, st, a, n_rt, rg);
-  else hipLaunchKernelGGL((k_experts_tile<C, 0, PIPE>), grid, block, 0, st, a, n_rt, rg);
+static int runs_per_group(const ExpertsArgs& a, int BT) {   // by the rows per expert
+  return a.n_pos / std::min(a.E, a.n_pos) >= 2 * BT ? 16 : 4;
 }
 
-typedef GCfg<256, 256, 128, 128, 4, 32, 4> Tile256;
+template <class C>
+static void launch_tile(const ExpertsArgs& a, hipStream_t st) {
+  const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  const int n_rt = (rows + C::kBR - 1) / C::kBR, rg = runs_per_group(a, C::kBT);
+  const int max_runs = (int)run_bound(a, C::kBT);
+  const dim3 grid(8 * xcd_tiles(0, max_runs, n_rt)), block(C::NT);
+  if (a.f32_out) hipLaunchKernelGGL((k_experts_tile<C, 2>), grid, block, 0, st, a, n_rt, rg, max_runs);
+  else if (a.gated) hipLaunchKernelGGL((k_experts_tile<C, 1>), grid, block, 0, st, a, n_rt, rg, max_runs);
+  else hipLaunchKernelGGL((k_experts_tile<C, 0>), grid, block, 0, st, a, n_rt, rg, max_runs);
+}
+
+static void launch_tile256(const ExpertsArgs& a, hipStream_t st) {
+  const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  const int n_rt = (rows + 255) / 256, rg = runs_per_group(a, 256);
+  // per XCD at most its share of the tiles and, where the last ones are cut,
+  // 24 pieces more
+  const int max_runs = (int)run_bound(a, 256);
+  const dim3 grid(8 * (xcd_tiles(0, max_runs, n_rt) + 24)), block(256);
+  if (a.f32_out) hipLaunchKernelGGL(k_experts_tile256<2>, grid, block, 0, st, a, n_rt, rg, max_runs);
+  else if (a.gated) hipLaunchKernelGGL(k_experts_tile256<1>, grid, block, 0, st, a, n_rt, rg, max_runs);
+  else hipLaunchKernelGGL(k_experts_tile256<0>, grid, block, 0, st, a, n_rt, rg, max_runs);
+}
+
 template <bool W8> using Tile128 = GCfg<128, 128, 64, 32, 3, W8 ? 128 : 64, W8 ? 2 : 3, W8>;
 template <bool W8> using Tile64 = GCfg<128, 64, 32, 32, 4, W8 ? 128 : 64, 4, W8>;
 typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
@@ -389,11 +462,11 @@ static void launch_bf16(const ExpertsArgs& a, hipStream_t st) {
   const long long tiles256 = (rows + 255) / 256 * (a.n_pos / 256 + active / 2);   // of about this many
   if (mean <= (W8 ? 20 : 2) || (rows + 127) / 128 * active < 256) return launch_stream<W8 ? kXFp8w : kXBf16>(a, st);
   if constexpr (!W8) {
-    if (mean <= 8) return launch_tile<Tile32, false>(a, st);
-    if (near && (mean >= 192 || (mean >= 112 && tiles256 >= 1024))) return launch_tile<Tile256, true>(a, st);
+    if (mean <= 8) return launch_tile<Tile32>(a, st);
+    if (near && (mean >= 192 || (mean >= 112 && tiles256 >= 1024))) return launch_tile256(a, st);
   }
-  if (mean <= 48) launch_tile<Tile64<W8>, false>(a, st);
-  else launch_tile<Tile128<W8>, false>(a, st);
+  if (mean <= 48) launch_tile<Tile64<W8>>(a, st);
+  else launch_tile<Tile128<W8>>(a, st);
 }
 
 void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st) {
