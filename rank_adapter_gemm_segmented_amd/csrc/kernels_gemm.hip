@@ -679,6 +679,7 @@ __global__ __launch_bounds__((BR / WR) * (BT / WT) * kWave)
 __attribute__((amdgpu_waves_per_eu((BR / WR) * (BT / WT) / 4, (BR / WR) * (BT / WT) / 4)))
 void k_gemm2(LinearArgs a) {
   constexpr bool GATED = EPI == kEpiGated;
+  constexpr bool PIPE = BR == 256 && (BR / WR) * (BT / WT) == 4;   // (one wave per SIMD)
   using C = GCfg<BR, BT, WR, WT, NB, KB, NX>;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[C::LDS_BYTES / 2];
   __shared__ int4 pinfo[BT];
@@ -718,6 +719,27 @@ void k_gemm2(LinearArgs a) {
   const uint16_t* __restrict__ W = (const uint16_t*)a.W;
   const uint16_t* zeros = (const uint16_t*)a.pv.zeros;
 
+  f32x16_t acc[C::MR][C::MT];
+#pragma unroll
+  for (int m = 0; m < C::MR; ++m)
+#pragma unroll
+    for (int n = 0; n < C::MT; ++n)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.f;
+
+  // Main loop. PIPE: that of the largest tile (gemm_tile.h).
+  if constexpr (PIPE) {
+    const int w0 = wrow_of<GATED>(r0, d_out);
+    PipeSrc<C> src;
+    src.set(wave, lane, W + (long long)w0 * d_in, x,
+            [&](int r) { return (uint32_t)(wrow_of<GATED>(r0 + r, d_out) - w0) * (uint32_t)(2 * d_in); },
+            [&](int r) {
+              const int p = min(t0 + r, T - 1);
+              const int row = a.sv.token_index ? a.sv.token_index[p] : p;
+              return (uint32_t)min(max(row, 0), T - 1) * (uint32_t)(2 * d_in);
+            });
+    pipe_mainloop<C>(src, d_in, zeros, (char*)lds, wave, lane, acc);
+  } else {
   // loader: load i < DPW_W of wave w fills the W slot's 1 KB chunk
   // J = i NW + w, load DPW_W + i the position slot's chunk J; lane l writes
   // its byte J 1024 + 16 l of the slot, i.e. row r, slot l % (KB/8), and so
@@ -770,14 +792,6 @@ void k_gemm2(LinearArgs a) {
   auto issue_x = [&](int st) {
     issue_part(st, C::DPW_W, C::DPW_X, lds0 + C::XRING + (uint32_t)(st % NX) * C::XSTAGE_B + (uint32_t)wave * 1024);
   };
-
-  f32x16_t acc[C::MR][C::MT];
-#pragma unroll
-  for (int m = 0; m < C::MR; ++m)
-#pragma unroll
-    for (int n = 0; n < C::MT; ++n)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.f;
 
   // fragment reads: row R (a multiple of 32 plus l32), chunk kk 2 + kh / 8
   int fcol[KB / 16];
@@ -833,6 +847,7 @@ void k_gemm2(LinearArgs a) {
     issue_x(st + NX - 1);
     compute(L + (st % NB) * C::WSTAGE_B, L + C::XRING + (st % NX) * C::XSTAGE_B);
   }
+  }
   // the dense adapter term of k_expand_delta (zero where a position has no
   // adapter): lane (l32, h) takes rows 8 q + 4 h .. + 3 of each 32-row block
   // at its position. Small tiles request it here, so it lands while the
@@ -844,7 +859,8 @@ void k_gemm2(LinearArgs a) {
   // (With an epilogue every tile adds it here.)
   constexpr bool kDeltaTile = EPI == kEpiNone && C::NW * WT * (4 * WR + 16) <= C::LDS_BYTES;
   constexpr bool kDeltaEarly = !kDeltaTile && C::MR * C::MT <= 4;
-  const bool use_delta = a.lora_on && a.delta != nullptr;
+  // (no dense term with as many tiles as the 4-wave form has: kDxMaxBytes is 64 of them)
+  const bool use_delta = !PIPE && a.lora_on && a.delta != nullptr;
   auto delta_ptr = [&](int n, int m, int q) {
     const int p = min(t0 + wt * WT + n * 32 + l32, T - 1);
     const int v = r0 + wr * WR + m * 32 + 8 * q + 4 * (lane / 32);
@@ -893,7 +909,7 @@ void k_gemm2(LinearArgs a) {
   // the pool straight into MFMA operand registers, a ring of kEpiRing units
   // ahead of the unit being multiplied. (With the dense term of
   // k_expand_delta, added above, none of this runs.)
-  if (a.lora_on && !a.delta) {
+  if (a.lora_on && (PIPE || !a.delta)) {
     const int RC = a.r_ws < 64 ? a.r_ws : 64;        // rank columns per chunk (16, 32 or 64)
     const int VP = RC + 8;                           // hi/lo row pitch (bf16)
     uint16_t* vsh = lds;
@@ -1233,12 +1249,18 @@ static void launch_g(const LinearArgs& a, hipStream_t st, bool grouped_order) {
   if (BR == 256 && n_rt % 4 == 0 && n_tt % 2 == 0 && (long long)n_rt * n_tt <= 256) g.gorder = 2;
   g.wnt = n_tt <= 2;
   const dim3 grid(n_rt * n_tt), block(GCfg<BR, BT, WR, WT, NB, KB, NX>::NT);
-  if (a.epi_kind == kEpiGated)
-    hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiGated>), grid, block, 0, st, g);
-  else if (a.epi_kind == kEpiPlain)
-    hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiPlain>), grid, block, 0, st, g);
-  else
-    hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiNone>), grid, block, 0, st, g);
+  // (of the 256 x 256 tiles, the 8-wave one runs without an epilogue, the 4-wave one with)
+  constexpr bool kWithEpi = BR < 256 || WT == 128, kWithout = BR < 256 || WT < 128;
+  if constexpr (kWithEpi) {
+    if (a.epi_kind == kEpiGated)
+      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiGated>), grid, block, 0, st, g);
+    else if (a.epi_kind == kEpiPlain)
+      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiPlain>), grid, block, 0, st, g);
+  }
+  if constexpr (kWithout) {
+    if (a.epi_kind == kEpiNone)
+      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiNone>), grid, block, 0, st, g);
+  }
 }
 
 // MLORA_FORCE_SHRINK=mfma keeps the MFMA shrink on short segments too.
@@ -1314,7 +1336,14 @@ void launch_linear_bf16(const LinearArgs& a, hipStream_t st) {
     return (long long)((a.d_out + br - 1) / br) * ((a.T + bt - 1) / bt);
   };
   constexpr long long kFill = 192;   // tiles that keep most of the 256 CUs busy
-  if (a.T > 128 && tiles(256, 256) >= kFill) launch_g<256, 256, 128, 64, 2, 64, 2>(a, st, false);
+  // With an epilogue the largest tile runs 4 waves of 128 x 128 on the main
+  // loop of gemm_tile.h, which addresses x and its rows of W by 32-bit offsets
+  // (past them: 128x128 tiles).
+  const bool large = a.T > 128 && tiles(256, 256) >= kFill, epi = a.epi_kind != kEpiNone;
+  const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
+                    (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
+  if (large && epi && near) launch_g<256, 256, 128, 128, 4, 32, 4>(a, st, true);
+  else if (large && !epi) launch_g<256, 256, 128, 64, 2, 64, 2>(a, st, false);
   else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 64, 3>(a, st, true);
   else if (a.T > 128 && tiles(64, 256) >= kFill) launch_g<64, 256, 64, 64, 3, 64, 3>(a, st, true);
   else launch_g<64, 128, 32, 32, 4, 64, 4>(a, st, true);
