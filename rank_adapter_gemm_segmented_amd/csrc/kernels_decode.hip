@@ -24,6 +24,7 @@
 // 4*(l/16)+v, column l%16.
 #include "common.h"
 #include "launch.h"
+#include "stream_tile.h"
 
 namespace mlora {
 
@@ -56,8 +57,12 @@ __device__ __forceinline__ long long part_off(int c, int i, int rb, int tb, int 
 // serve two consecutive k-steps: lane group g = l / 16 of the step pair
 // (2q, 2q + 1) starting at column C takes columns C + 16 g .. + 7 in step 2q
 // and C + 16 g + 8 .. + 15 in step 2q + 1, and reads x at the same columns.
-// GATED: the items' rows are virtual rows (epilogue.h).
-template <int TT, bool W8, bool GATED>
+// GATED: the items' rows are virtual rows (epilogue.h). NT: W loads marked
+// nontemporal. With an epilogue they are not, but for 64 tokens on a long d_in:
+// a row's 128-byte line comes by two loads, and the mark loses it in between
+// (64 tokens, 4096 -> 4096: 18.2 us marked, 17.0 not; one token, gate|up in FP8:
+// 40.6 and 38.6; 64 tokens, 14336 -> 4096: 51.1 and 53.5).
+template <int TT, bool W8, bool GATED, bool NT>
 __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
   constexpr int NTB = TT / 16;
   constexpr int XP = kDecXPitch;
@@ -147,15 +152,16 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
   const uint16_t* wrow = W + (long long)wrow_of<GATED>(nrow, d_out) * d_in + k0;
   const uint8_t* wrow8 = (const uint8_t*)a.W + (long long)wrow_of<GATED>(nrow, d_out) * d_in + k0;
   u32x4_t wr[kDecWSteps];
+  auto ld_w = [](const void* p) { return NT ? ld_nt16(p) : ld16(p); };
   auto load_w = [&](int s) {
     // steps of the other k-half read the pool's zero block (address select)
     if constexpr (W8) {   // slot s holds step pair (2s, 2s + 1)
       const int k = (ks_begin + 2 * s) * 32 + 2 * kq;
-      wr[s] = ld_nt16(ks_begin + 2 * s < ks_end ? (const void*)(wrow8 + min(k, kc - 16))
+      wr[s] = ld_w(ks_begin + 2 * s < ks_end ? (const void*)(wrow8 + min(k, kc - 16))
                                                 : (const void*)((const uint16_t*)a.pv.zeros + kq));
     } else {
       const int k = (ks_begin + s) * 32 + kq;
-      wr[s] = ld_nt16(ks_begin + s < ks_end ? wrow + min(k, kc - 8) : (const uint16_t*)a.pv.zeros + kq);
+      wr[s] = ld_w(ks_begin + s < ks_end ? wrow + min(k, kc - 8) : (const uint16_t*)a.pv.zeros + kq);
     }
   };
   // FP8: the 16 steps are 8 loads; half of them are requested ahead of the
@@ -332,6 +338,80 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
     shrink_unit(ar[0]);
     if (bi >= kWave) break;
     shrink_unit(ar[1]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// stream, whole d_in: for a few tokens on wide layers (with an epilogue). A
+// workgroup takes 32 (virtual) rows of W over the whole of d_in, its 8 waves a
+// part of d_in each (stream_tile.h), and adds their sums in wave order: no split
+// of d_in over workgroups, one partial tile per row tile for k_finish.
+// The first blocks are the shrink units, 16 rank rows of one segment each, which
+// leave one partial of v per wave and the position table, as k_stream does.
+// ---------------------------------------------------------------------------
+constexpr int kWideWaves = 8;
+
+template <bool W8, bool GATED>
+__global__ __launch_bounds__(kWideWaves * kWave) void k_stream_wide(DecodeArgs a, int n_units) {
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
+  const int l16 = lane % 16, g = lane / 16;
+  const int T = a.T, d_in = a.d_in, d_out = a.d_out;
+  // the lane's token (absent ones repeat the last)
+  int row = min(l16, T - 1);
+  if (a.sv.token_index) row = min(max(a.sv.token_index[row], 0), T - 1);   // uniform
+  const char* xrow = (const char*)a.x + (long long)row * d_in * 2;
+  const int b = blockIdx.x;
+  if (b < n_units) {   // uniform: a shrink unit
+    const SegView& sv = a.sv;
+    const int nq = (a.pv.max_rank + 15) / 16, s = b / nq, j0 = b % nq * 16;
+    if (s >= seg_count(sv)) return;
+    const int ps = max(sv.seg_start[s], 0), pe = min(sv.seg_start[s + 1], T);
+    const int ad0 = sv.seg_adapter[s], rk = sv.seg_rank[s];
+    const bool live = pe > ps && ad0 >= 0 && ad0 < a.pv.capacity && rk > 0;
+    const int rr = live ? min(rk, a.pv.max_rank) : 0;
+    if (j0 == 0) {   // the rank the expand applies: capped by the registered one
+      const int r = live ? min(rr, a.pv.rank[ad0]) : 0;
+      const int ad = r > 0 ? ad0 : -1;
+      for (int t = ps + tid; t < pe; t += kWideWaves * kWave)
+        a.pos[t] = make_int4(ad, ad >= 0 ? r : 0, __float_as_int(ad >= 0 ? sv.seg_scale[s] : 0.f), 0);
+    }
+    const int rows = min(rr - j0, 16);
+    if (rows <= 0) return;
+    const char* A = (const char*)a.pv.base + ((long long)ad0 * a.pv.slot_elems + (long long)j0 * d_in) * 2;
+    const uint32_t ao[1] = {(uint32_t)min(l16, rows - 1) * (uint32_t)(d_in * 2) + 16 * g};
+    const char* xp[1] = {xrow + 16 * g};
+    f32x4_t v[1][1];
+    stream_product<kXBf16, 1, 1, kWideWaves, false>(A, 0, ao, xp, d_in, wave, g, v);
+    float* vp = a.v_part + ((long long)wave * T + l16) * a.r_ws + j0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * g + i;
+      if (j < rows && l16 >= ps && l16 < pe) vp[j] = v[0][0][i];
+    }
+    return;
+  }
+  __shared__ f32x4_t red[kWideWaves][2][kWave];
+  constexpr int EB = W8 ? 1 : 2;
+  const int v0 = 32 * (b - n_units);
+  const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out;
+  const char* wbase = (const char*)a.W + (long long)min(f0, nf - 1) * d_in * EB;
+  uint32_t wo[GATED ? 1 : 2];
+#pragma unroll
+  for (int r = 0; r < (GATED ? 1 : 2); ++r)
+    wo[r] = (uint32_t)max(min(16 * r + l16, nf - 1 - f0), 0) * (uint32_t)(d_in * EB) + 16 * g;
+  const char* xp[1] = {xrow + (W8 ? 32 : 16) * g};
+  f32x4_t acc[2][1];
+  stream_product<W8 ? kXFp8w : kXBf16, 2, 1, kWideWaves, GATED>(wbase, (long long)nf * d_in * EB, wo, xp, d_in, wave, g, acc);
+  red[wave][0][lane] = acc[0][0];
+  red[wave][1][lane] = acc[1][0];
+  __syncthreads();
+  if (tid < 2 * kWave) {
+    f32x4_t sum = red[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kWideWaves; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += red[w][wave][lane][i];
+    *(f32x4_t*)(a.ypart + part_off(0, v0 / 64, v0 / 32 % 2 * 2 + wave, 0, a.n_tiles, 1) + lane * 4) = sum;
   }
 }
 
@@ -643,9 +723,37 @@ void decode_plan(int d_in, int d_out, int* n_tiles, int* kc, int* n_chunks) {
   *n_chunks = (d_in + k - 1) / k;
 }
 
+// Whole-d_in streaming with an epilogue: up to 8 tokens on layers of at least
+// this many tiles of 64 rows. Both kernels, 4096 -> 2 x 14336 gated: one token
+// 53.0 us against 59.5 with d_in split over workgroups (FP8 33.0 against 38.6),
+// 4 tokens 54.5 against 62.8, 16 tokens 63.5 against 59.7; 4096 -> 8192: one token
+// 22.0 against 19.0.
+constexpr int kWideTiles = 256, kWideTokens = 8;
+
 template <int TT, bool W8, int EPI>
-static void launch_decode_epi(const DecodeArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_stream_bf16<TT, W8, EPI == kEpiGated>), dim3(a.n_tiles * a.n_chunks), dim3(kDecThreads), 0, st, a);
+static void launch_decode_epi(DecodeArgs a, hipStream_t st) {
+  constexpr bool GATED = EPI == kEpiGated;
+  const dim3 items(a.n_tiles * a.n_chunks);
+  if constexpr (EPI == kEpiNone) {
+    hipLaunchKernelGGL((k_stream_bf16<TT, W8, false, true>), items, dim3(kDecThreads), 0, st, a);
+  } else {
+    bool done = false;
+    if constexpr (TT == 16) {
+      if (a.T <= kWideTokens && a.n_tiles >= kWideTiles) {
+        a.n_chunks = 1;   // what k_finish adds up
+        const int units = a.lora_on ? a.sv.n_seg * ((a.pv.max_rank + 15) / 16) : 0;
+        hipLaunchKernelGGL((k_stream_wide<W8, GATED>), dim3(units + 2 * a.n_tiles), dim3(kWideWaves * kWave), 0, st, a, units);
+        done = true;
+      }
+    }
+    if constexpr (TT == 64) {
+      if (a.d_in > 8192) {
+        hipLaunchKernelGGL((k_stream_bf16<TT, W8, GATED, true>), items, dim3(kDecThreads), 0, st, a);
+        done = true;
+      }
+    }
+    if (!done) hipLaunchKernelGGL((k_stream_bf16<TT, W8, GATED, false>), items, dim3(kDecThreads), 0, st, a);
+  }
   if (a.lora_on && a.pv.n_slices > 0)
     hipLaunchKernelGGL((k_finish_bf16<TT, W8, true, EPI>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
   else

@@ -13,16 +13,11 @@
 #include "../../include/mlora.h"
 #include "experts.h"
 #include "gemm_tile.h"
+#include "stream_tile.h"
 
 namespace mlora {
 
 __device__ __attribute__((aligned(16))) uint32_t expert_zeros[64];   // read past d_in
-
-__device__ __forceinline__ f32x4_t mfma16e(u32x4_t a, u32x4_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
-}
-
-constexpr int kXBf16 = 0, kXFp8w = 1, kXF32 = 2;   // element types of the streaming kernel
 
 // ---------------------------------------------------------------------------
 // Streaming form, every type: an item is 16 NR (virtual) rows of one expert by
@@ -31,19 +26,9 @@ constexpr int kXBf16 = 0, kXFp8w = 1, kXF32 = 2;   // element types of the strea
 // straight into MFMA operand registers, and their sums are added in wave order
 // through LDS. W is read once where an expert has at most 16 NTB rows.
 //
-// A unit is two 16-byte loads per row block: lane group g = l / 16 takes bytes
-// 16 g and 64 + 16 g, so a row's 128-byte line is whole within the unit. bf16:
-// a load is one 32-column MFMA operand; FP8: 16 columns, two operands (columns
-// 16 g and 16 g + 8 of the 64); fp32: 4 columns, four 16x16x4 products.
-//
-// Bound by W's bytes. One unit per wave is in flight, refilled as it is
-// consumed: the waves resident on a CU (28 of 67 registers) keep 224 KB
-// requested, and a second unit per wave cost as much occupancy as it gave
-// (121 against 113 us, 64 tokens over 64 FP8 experts of 4096 -> 2 x 1024). W is
-// loaded without the nontemporal mark: a line's two halves come by two loads,
-// and the mark lost the first half's line (128 against 113 us). Neighbouring
-// workgroups take neighbouring row tiles, so the card streams W in order
-// (an order that put an expert's runs side by side on an XCD: 119 us).
+// Bound by W's bytes (stream_tile.h). Neighbouring workgroups take neighbouring
+// row tiles, so the card streams W in order (an order that put an expert's runs
+// side by side on an XCD: 119 us against 113).
 // ---------------------------------------------------------------------------
 constexpr int kGridY = 32768;   // runs per grid row (y is limited; z takes the rest)
 
@@ -64,10 +49,7 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
   const int v0 = rt * 16 * NR;                                     // first (virtual) row
   auto wrow = [&](int v) { return (long long)e * d_out + wrow_of<GATED>(v, d_out); };
 
-  // W: a uniform base (gated: one for gate rows and one for up rows) and a
-  // 32-bit offset per lane and row block; rows past the last are clamped to it.
-  // Registers are occupancy here, and occupancy is bytes in flight: with a
-  // 64-bit address per row block the kernel took 108 registers and 127 us.
+  // W: a uniform base and 32-bit offsets; rows past the last are clamped to it
   constexpr int NO = GATED ? NR / 2 : NR;                          // distinct row blocks
   const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out;
   const char* wbase = (const char*)a.W + ((long long)e * d_out + f0) * d_in * EB;
@@ -84,71 +66,7 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
   }
 
   f32x4_t acc[NR][NTB];
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int t = 0; t < NTB; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  u32x4_t w[2][NR], x[2][XL][NTB];
-  auto load = [&](int u) {                                         // unit u, whole
-    const char* wu = wbase + (long long)u * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int r = 0; r < NR; ++r) w[h][r] = ld16((GATED && (r & 1) ? wu + up : wu) + wo[GATED ? r / 2 : r] + 64 * h);
-#pragma unroll
-      for (int i = 0; i < XL; ++i)
-#pragma unroll
-        for (int t = 0; t < NTB; ++t) x[h][i][t] = ld16(xp[t] + (long long)u * (UC * XB) + h * (UC / 2 * XB) + 16 * i);
-    }
-  };
-  auto multiply = [&]() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int t = 0; t < NTB; ++t) {
-          if constexpr (TYPE == kXBf16) {
-            acc[r][t] = mfma16e(w[h][r], x[h][0][t], acc[r][t]);
-          } else if constexpr (TYPE == kXFp8w) {
-            acc[r][t] = mfma16e(e4m3x8_bf16(w[h][r].x, w[h][r].y), x[h][0][t], acc[r][t]);
-            acc[r][t] = mfma16e(e4m3x8_bf16(w[h][r].z, w[h][r].w), x[h][XL - 1][t], acc[r][t]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[h][r][i]), __uint_as_float(x[h][0][t][i]),
-                                                               acc[r][t], 0, 0, 0);
-          }
-        }
-  };
-  const int nu = d_in / UC;                                        // whole units
-  const int ub = nu * wave / NW, ue = nu * (wave + 1) / NW;        // this wave's
-  if (ub < ue) {   // uniform
-    load(ub);
-    for (int u = ub; u + 1 < ue; ++u) {
-      multiply();
-      load(u + 1);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    multiply();
-  }
-  if (nu * UC < d_in && wave == NW - 1) {   // uniform: the columns behind the last whole unit
-    const char* wu = wbase + (long long)nu * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = nu * UC + h * UC / 2 + 16 / EB * g < d_in;   // (d_in is a multiple of 16 bytes of W)
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-        w[h][r] = in ? ld16((GATED && (r & 1) ? wu + up : wu) + wo[GATED ? r / 2 : r] + 64 * h) : zero_u32x4();
-#pragma unroll
-      for (int i = 0; i < XL; ++i)
-#pragma unroll
-        for (int t = 0; t < NTB; ++t)
-          x[h][i][t] = in ? ld16(xp[t] + (long long)nu * (UC * XB) + h * (UC / 2 * XB) + 16 * i) : zero_u32x4();
-    }
-    multiply();
-  }
+  stream_product<TYPE, NR, NTB, NW, GATED>(wbase, up, wo, xp, d_in, wave, g, acc);
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll

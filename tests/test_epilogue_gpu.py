@@ -108,6 +108,17 @@ def test_decode(i, gated):
     layer.check(ACTS[(i + 2) % 5], lora_on=0)
 
 
+# a few tokens on layers of many rows: W streamed over the whole of d_in
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,d_in,d_out,fp8", [(1, 264, 16640, False), (5, 1040, 16390, False), (8, 72, 16400, False),
+                                              (8, 528, 17000, True), (3, 16, 16386, True), (9, 272, 16640, True)])
+def test_wide_decode(T, d_in, d_out, fp8, gated):
+    log(f"[epilogue] wide decode T={T} {d_in}->{d_out} fp8={fp8} gated={gated}")
+    layer = Layer(torch.bfloat16, T, d_in, d_out, gated, seed=T, shuffled=T > 3, fp8=fp8, max_run=2)
+    layer.check("silu")
+    layer.check("gelu", lora_on=0)
+
+
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("i", range(len(TILED)))
 def test_tiled(i, gated):
