@@ -342,38 +342,58 @@ def merge_adapter(W, pool: Pool, adapter_id: int, scale: float, out=None):
 
 
 # ---- the layer with what follows it -------------------------------------------
+# These calls are short at small sizes: each tensor is looked at once, for its
+# device, layout and pointer together.
+
+_i32t, _f32t, _u8t, _bf16t = torch.int32, torch.float32, torch.uint8, torch.bfloat16
+_device = torch._C._cuda_getDevice
+
+
+def _refuse(t, dev, what):
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: tensors must be on the current device")
+    raise ValueError(f"{what}: tensors must be contiguous")
+
+
+def _at(t, dev: int, what: str):
+    """Pointer of a contiguous tensor of the current device (the call runs on
+    that device's current stream), None for None."""
+    if t is None:
+        return None
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dev, what)
+    return t.data_ptr()
+
+
+def _at_i32(t, dev: int, what: str):
+    if t is None:
+        return None
+    if t.dtype is not _i32t:
+        raise TypeError(f"{what}: segment metadata must be int32")
+    return _at(t, dev, what)
+
 
 def _act_code(act: str, gated: bool) -> int:
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    return ACTS[act] | (_GATED if gated else 0)
-
-
-def _here(what: str, *tensors):
-    """Every tensor given is contiguous and on the current device: the call
-    runs on that device's current stream."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or t.get_device() != dev:
-            raise ValueError(f"{what}: tensors must be on the current device")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: tensors must be contiguous")
+    return code | _GATED if gated else code
 
 
 def _epilogue_out(x, rows: int, d_out: int, gated: bool, bias, bias_shape, residual, out):
     """Checks an epilogue's tensors and returns y."""
-    if gated and d_out % 2:
-        raise ValueError("a gated product needs an even number of weight rows")
-    shape = (rows, d_out // 2 if gated else d_out)
-    if bias is not None and (bias.dtype != x.dtype or tuple(bias.shape) != bias_shape):
+    if gated:
+        if d_out % 2:
+            raise ValueError("a gated product needs an even number of weight rows")
+        d_out //= 2
+    shape, dt = (rows, d_out), x.dtype
+    if bias is not None and (bias.dtype is not dt or bias.shape != bias_shape):
         raise ValueError(f"bias must be {list(bias_shape)} of x's dtype")
-    if residual is not None and (residual.dtype != x.dtype or tuple(residual.shape) != shape):
+    if residual is not None and (residual.dtype is not dt or residual.shape != shape):
         raise ValueError(f"residual must be {list(shape)} of x's dtype")
     if out is None:
-        return torch.empty(shape, dtype=x.dtype, device=x.device)
-    if out.dtype != x.dtype or tuple(out.shape) != shape:
+        return x.new_empty(shape)
+    if out.dtype is not dt or out.shape != shape:
         raise ValueError(f"out must be {list(shape)} of x's dtype")
     return out
 
@@ -385,55 +405,54 @@ def linear_epilogue(x, W, pool: Pool, seg_start=None, seg_adapter=None, seg_rank
     ``gated``, W stacks gate over up rows and the result is act(gate) * up +
     residual. With ``w_scale``, W holds e4m3 codes (``mlora_linear_fp8w_epilogue``).
     ``residual`` may be ``out`` itself."""
-    if w_scale is None:
-        _check_xw(x, W, pool)
-    else:
-        if x.dtype != torch.bfloat16 or pool.dtype != torch.bfloat16:
-            raise TypeError("x and the pool must be bf16")
-        if W.dtype != torch.uint8 or tuple(W.shape) != (pool.d_out, pool.d_in):
-            raise ValueError("W must be uint8 [d_out, d_in]")
-        if w_scale.dtype != torch.float32 or tuple(w_scale.shape) != (pool.d_out,):
+    what, dev, d_out, d_in = "linear_epilogue", _device(), pool.d_out, pool.d_in
+    if x.dtype is not pool.dtype or (w_scale is None and W.dtype is not pool.dtype):
+        raise TypeError("x and W must have the pool's dtype")
+    if x.dim() != 2 or x.shape[1] != d_in or W.shape != (d_out, d_in):
+        raise ValueError("x must be [T, d_in] and W [d_out, d_in]")
+    if w_scale is not None:
+        if x.dtype is not _bf16t or W.dtype is not _u8t:
+            raise TypeError("with w_scale, x and the pool must be bf16 and W uint8")
+        if w_scale.dtype is not _f32t or w_scale.shape != (d_out,):
             raise ValueError("w_scale must be float32 [d_out]")
-        if x.dim() != 2 or x.shape[1] != pool.d_in:
-            raise ValueError("x must be [T, d_in]")
-    if seg_scale is not None and seg_scale.dtype != torch.float32:
+    if seg_scale is not None and seg_scale.dtype is not _f32t:
         raise TypeError("seg_scale must be float32")
     T = x.shape[0]
     code = _act_code(act, gated)
-    y = _epilogue_out(x, T, pool.d_out, gated, bias, (pool.d_out,), residual, out)
-    _here("linear_epilogue", x, W, w_scale, seg_scale, bias, residual, y, workspace)
+    y = _epilogue_out(x, T, d_out, gated, bias, (d_out,), residual, out)
     ws = workspace if workspace is not None else pool.workspace(T)
-    n_seg = seg_adapter.numel() if seg_adapter is not None else 0
-    epi = _Epilogue(_ptr(bias), _ptr(residual), code)
-    meta = (_ptr(_i32(seg_start, "seg_start")), _ptr(_i32(seg_adapter, "seg_adapter")), _ptr(_i32(seg_rank, "seg_rank")),
-            _ptr(seg_scale), _ptr(_i32(token_index, "token_index")), T, n_seg, int(lora_on), ctypes.byref(epi),
-            y.data_ptr(), ws.data_ptr(), ws.numel(), _stream())
+    epi = _Epilogue(_at(bias, dev, what), _at(residual, dev, what), code)
+    rest = (pool.handle, _at_i32(seg_start, dev, what), _at_i32(seg_adapter, dev, what), _at_i32(seg_rank, dev, what),
+            _at(seg_scale, dev, what), _at_i32(token_index, dev, what), T,
+            seg_adapter.numel() if seg_adapter is not None else 0, lora_on, ctypes.byref(epi), _at(y, dev, what),
+            _at(ws, dev, what), ws.numel(), _raw_stream(dev))
     if w_scale is None:
-        _check(_lib.mlora_linear_epilogue(x.data_ptr(), W.data_ptr(), pool.handle, *meta), "mlora_linear_epilogue")
+        code = _lib.mlora_linear_epilogue(_at(x, dev, what), _at(W, dev, what), *rest)
     else:
-        _check(_lib.mlora_linear_fp8w_epilogue(x.data_ptr(), W.data_ptr(), w_scale.data_ptr(), pool.handle, *meta),
-               "mlora_linear_fp8w_epilogue")
+        code = _lib.mlora_linear_fp8w_epilogue(_at(x, dev, what), _at(W, dev, what), _at(w_scale, dev, what), *rest)
+    if code:
+        raise MloraError(code, "mlora_linear_epilogue" if w_scale is None else "mlora_linear_fp8w_epilogue")
     return y
 
 
 def linear_tokens_epilogue(x, W, pool: Pool, token_adapter, adapter_scale, lora_on: int = 1, bias=None,
                            act: str = "none", gated: bool = False, residual=None, out=None, workspace=None):
     """``mlora_linear_tokens_epilogue``: ``linear_epilogue`` on an unsorted batch."""
+    what, dev, d_out = "linear_tokens_epilogue", _device(), pool.d_out
     _check_xw(x, W, pool)
     T = x.shape[0]
     code = _act_code(act, gated)
-    y = _epilogue_out(x, T, pool.d_out, gated, bias, (pool.d_out,), residual, out)
-    if adapter_scale is not None and (adapter_scale.dtype != torch.float32 or adapter_scale.numel() != pool.capacity):
+    y = _epilogue_out(x, T, d_out, gated, bias, (d_out,), residual, out)
+    if adapter_scale is not None and (adapter_scale.dtype is not _f32t or adapter_scale.numel() != pool.capacity):
         raise TypeError("adapter_scale must be float32 [capacity]")
     if token_adapter is not None and token_adapter.numel() != T:
         raise ValueError("token_adapter must be [T]")
-    _here("linear_tokens_epilogue", x, W, adapter_scale, bias, residual, y, workspace)
     ws = workspace if workspace is not None else pool.workspace(T)
-    epi = _Epilogue(_ptr(bias), _ptr(residual), code)
-    _check(_lib.mlora_linear_tokens_epilogue(x.data_ptr(), W.data_ptr(), pool.handle,
-                                             _ptr(_i32(token_adapter, "token_adapter")), _ptr(adapter_scale), T,
-                                             int(lora_on), ctypes.byref(epi), y.data_ptr(), ws.data_ptr(), ws.numel(),
-                                             _stream()), "mlora_linear_tokens_epilogue")
+    epi = _Epilogue(_at(bias, dev, what), _at(residual, dev, what), code)
+    _check(_lib.mlora_linear_tokens_epilogue(_at(x, dev, what), _at(W, dev, what), pool.handle,
+                                             _at_i32(token_adapter, dev, what), _at(adapter_scale, dev, what), T,
+                                             int(lora_on), ctypes.byref(epi), _at(y, dev, what), _at(ws, dev, what),
+                                             ws.numel(), _raw_stream(dev)), "mlora_linear_tokens_epilogue")
     return y
 
 
@@ -451,48 +470,52 @@ def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None
     """``mlora_route``: top-k expert choice of logits [T, E] and its segments.
     Returns (expert [T, k], weight [T, k], token_index [T k], seg_start [E + 1],
     position [T, k]); ``out`` is such a tuple to write into."""
+    what, dev = "route", _device()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     code = _dtype_code(logits.dtype)
     T, E = logits.shape
-    dev = logits.device
     if not 1 <= top_k <= E:
         raise MloraError(STATUS_CODE["MLORA_ERR_SHAPE"], "mlora_route")
+    at_logits, P = _at(logits, dev, what), T * top_k
+    ws = workspace if workspace is not None else route_workspace(T, E, top_k, logits.device)
     if out is None:
-        out = (torch.empty((T, top_k), dtype=torch.int32, device=dev),
-               torch.empty((T, top_k), dtype=torch.float32, device=dev),
-               torch.empty(T * top_k, dtype=torch.int32, device=dev),
-               torch.empty(E + 1, dtype=torch.int32, device=dev),
-               torch.empty((T, top_k), dtype=torch.int32, device=dev))
+        # one allocation, an output every `at` elements (16-byte aligned)
+        at, slot, st = (P + 3) & ~3, (T, top_k), (top_k, 1)
+        buf = logits.new_empty(4 * at + E + 1, dtype=_i32t)
+        out = (buf.as_strided(slot, st, 0), buf.view(_f32t).as_strided(slot, st, at),
+               buf.as_strided((P,), (1,), 2 * at), buf.as_strided((E + 1,), (1,), 4 * at),
+               buf.as_strided(slot, st, 3 * at))
+        p0 = buf.data_ptr()
+        ptrs = (p0, p0 + 4 * at, p0 + 8 * at, p0 + 16 * at, p0 + 12 * at)
     else:
-        for t, n, dt in zip(out, (T * top_k, T * top_k, T * top_k, E + 1, T * top_k),
-                            (torch.int32, torch.float32, torch.int32, torch.int32, torch.int32)):
-            if t.dtype != dt or t.numel() != n:
+        for t, n, dt in zip(out, (P, P, P, E + 1, P), (_i32t, _f32t, _i32t, _i32t, _i32t)):
+            if t.dtype is not dt or t.numel() != n:
                 raise ValueError("out must be (expert, weight, token_index, seg_start, position) of this batch")
-    expert, weight, token_index, seg_start, position = out
-    _here("route", logits, *out, workspace)
-    ws = workspace if workspace is not None else route_workspace(T, E, top_k, dev)
-    _check(_lib.mlora_route(logits.data_ptr(), code, T, E, top_k, int(bool(renormalize)), expert.data_ptr(),
-                            weight.data_ptr(), token_index.data_ptr(), seg_start.data_ptr(), position.data_ptr(),
-                            ws.data_ptr(), ws.numel(), _stream()), "mlora_route")
+        ptrs = [_at(t, dev, what) for t in out]
+    code = _lib.mlora_route(at_logits, code, T, E, top_k, 1 if renormalize else 0, *ptrs, _at(ws, dev, what), ws.numel(),
+                            _raw_stream(dev))
+    if code:
+        raise MloraError(code, "mlora_route")
     return out
 
 
 def _check_experts(x, W, seg_start, w_scale):
     """Checks the operands of an expert product; returns (dtype code, E, d_out, d_in)."""
-    code = _dtype_code(x.dtype)
+    dt = x.dtype
+    code = _dtype_code(dt)
     if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
         raise ValueError("x must be [rows, d_in] and W [E, d_out, d_in]")
     E, d_out, d_in = W.shape
     if w_scale is None:
-        if W.dtype != x.dtype:
+        if W.dtype is not dt:
             raise TypeError("x and W must have one dtype")
     else:
-        if W.dtype != torch.uint8 or x.dtype != torch.bfloat16:
+        if W.dtype is not _u8t or dt is not _bf16t:
             raise TypeError("with w_scale, W must be uint8 and x bf16")
-        if w_scale.dtype != torch.float32 or tuple(w_scale.shape) != (E, d_out):
+        if w_scale.dtype is not _f32t or w_scale.shape != (E, d_out):
             raise ValueError("w_scale must be float32 [E, d_out]")
-    if seg_start.dtype != torch.int32 or seg_start.numel() != E + 1:
+    if seg_start.dtype is not _i32t or seg_start.numel() != E + 1:
         raise ValueError("seg_start must be int32 [E + 1]")
     return code, E, d_out, d_in
 
@@ -502,14 +525,17 @@ def experts_linear(x, W, seg_start, token_index=None, bias=None, act: str = "non
     """``mlora_experts_linear``: act(W_e x[token_index[p]] + bias_e) for the sorted
     positions p of every expert e (``route``'s seg_start and token_index), gated as
     ``linear_epilogue``. Rows of the result behind seg_start[-1] are not written."""
+    what, dev = "experts_linear", _device()
     code, E, d_out, d_in = _check_experts(x, W, seg_start, w_scale)
-    n_pos = token_index.numel() if token_index is not None else x.shape[0]
+    n_rows = x.shape[0]
+    n_pos = token_index.numel() if token_index is not None else n_rows
+    epi = _Epilogue(_at(bias, dev, what), None, _act_code(act, gated))
     y = _epilogue_out(x, n_pos, d_out, gated, bias, (E, d_out), None, out)
-    _here("experts_linear", x, W, seg_start, w_scale, bias, y)
-    epi = _Epilogue(_ptr(bias), None, _act_code(act, gated))
-    _check(_lib.mlora_experts_linear(x.data_ptr(), W.data_ptr(), _ptr(w_scale), code, x.shape[0], E, d_in, d_out,
-                                     seg_start.data_ptr(), _ptr(_i32(token_index, "token_index")), n_pos,
-                                     ctypes.byref(epi), y.data_ptr(), _stream()), "mlora_experts_linear")
+    code = _lib.mlora_experts_linear(_at(x, dev, what), _at(W, dev, what), _at(w_scale, dev, what), code, n_rows, E, d_in,
+                                     d_out, _at(seg_start, dev, what), _at_i32(token_index, dev, what), n_pos,
+                                     ctypes.byref(epi), _at(y, dev, what), _raw_stream(dev))
+    if code:
+        raise MloraError(code, "mlora_experts_linear")
     return y
 
 
@@ -526,19 +552,21 @@ def experts_combine(h, W, seg_start, position, weight, bias=None, residual=None,
                     workspace=None):
     """``mlora_experts_combine``: residual[t] + sum_j weight[t, j] (W_e h[position[t, j]] + bias_e),
     with ``route``'s seg_start, position and weight. ``residual`` may be ``out`` itself."""
+    what, dev = "experts_combine", _device()
     code, E, d_out, d_in = _check_experts(h, W, seg_start, w_scale)
-    if position.dim() != 2 or position.dtype != torch.int32:
+    if position.dim() != 2 or position.dtype is not _i32t:
         raise ValueError("position must be int32 [T, k]")
     T, k = position.shape
-    if weight.dtype != torch.float32 or weight.shape != position.shape:
+    if weight.dtype is not _f32t or weight.shape != position.shape:
         raise ValueError("weight must be float32 [T, k]")
     if h.shape[0] != T * k:
         raise ValueError("h must hold a row per slot: [T k, d_in]")
     y = _epilogue_out(h, T, d_out, False, bias, (E, d_out), residual, out)
-    _here("experts_combine", h, W, seg_start, position, weight, w_scale, bias, residual, y, workspace)
     ws = workspace if workspace is not None else experts_workspace(T, k, E, d_out, h.dtype, h.device)
-    _check(_lib.mlora_experts_combine(h.data_ptr(), W.data_ptr(), _ptr(w_scale), code, T, k, E, d_in, d_out,
-                                      seg_start.data_ptr(), position.data_ptr(), weight.data_ptr(), _ptr(bias),
-                                      _ptr(residual), y.data_ptr(), ws.data_ptr(), ws.numel(), _stream()),
-           "mlora_experts_combine")
+    code = _lib.mlora_experts_combine(_at(h, dev, what), _at(W, dev, what), _at(w_scale, dev, what), code, T, k, E, d_in,
+                                      d_out, _at(seg_start, dev, what), _at(position, dev, what), _at(weight, dev, what),
+                                      _at(bias, dev, what), _at(residual, dev, what), _at(y, dev, what),
+                                      _at(ws, dev, what), ws.numel(), _raw_stream(dev))
+    if code:
+        raise MloraError(code, "mlora_experts_combine")
     return y

@@ -79,10 +79,15 @@ __global__ __launch_bounds__(256) void k_shrink_f32(LinearArgs a) {
 // small layer loads everything in one round trip.
 constexpr int kF32KB = 256;
 constexpr int kF32Feat = 16;
+constexpr int kF32FusedRank = 16;   // largest rank of the fused shrink (two groups of 8)
 
 // EPI: what follows the layer. Gated: the 16 rows are 8 features' gate rows,
 // then their up rows, so thread tx + 8 holds the up value of thread tx.
-template <int EPI>
+// FUSED: the shrink runs here too (no k_shrink_f32, no table): the 16 threads of
+// a position split each chunk's columns among them and keep partial dot
+// products with the position's rank rows, 4 loads of 16 bytes a row. Every
+// feature tile repeats it, which a small layer hides under its latency.
+template <int EPI, bool FUSED>
 __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
   constexpr bool GATED = EPI == kEpiGated;
   __shared__ float Ws[kF32Feat][kF32KB + 1];
@@ -117,7 +122,7 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
   // this position's adapter entry, requested with the first chunk (the
   // epilogue's B and v loads then need no further round trip)
   const int p = p0 + ty;
-  const int4 pe4 = a.lora_on ? a.pos_info[min(p, T - 1)] : make_int4(0, -1, 0, 0);
+  const int4 pe4 = !FUSED && a.lora_on ? a.pos_info[min(p, T - 1)] : make_int4(0, -1, 0, 0);
   f32x4_t wreg[N4], xreg[N4];
   auto load = [&](int kb) {
 #pragma unroll
@@ -128,7 +133,68 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
       xreg[i] = xok ? *(const f32x4_t*)(xsrc[i] + kb) : f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
   };
+  // FUSED: the position's segment, adapter and rank rows. The rows to read are
+  // the segment's own, clamped into the slot; the registered rank only masks v.
+  // Loads are unconditional, at clamped places, and the first one leads W and x.
+  constexpr int RG = 8;                                   // rank rows loaded together
+  const SegView& sg = a.sv;
+  const int f_S = FUSED ? seg_count(sg) : 0, pc = min(p, T - 1);
+  int f_st = 0;
+  if constexpr (FUSED) f_st = sg.seg_start[min(tx, f_S)];
   load(0);
+  int f_ad = -1, f_r = 0, f_rows = 0;
+  float f_sc = 0.f, vacc[FUSED ? kF32FusedRank : 1];
+  const float* f_A = (const float*)a.pv.zeros;
+  if constexpr (FUSED) {
+    int s = 0;
+    if (f_S <= 16) {   // uniform: the starts are in the position's 16 threads
+      const unsigned long long m = __ballot(tx < f_S && f_st <= pc) >> (16 * (ty % 4));
+      s = max(__popcll(m & 0xffffull) - 1, 0);
+    } else {
+      s = find_segment(sg.seg_start, f_S, pc);
+    }
+    const int sc = min(s, max(f_S - 1, 0));
+    int beg = sg.seg_start[sc], end = sg.seg_start[sc + 1], ad = sg.seg_adapter[sc], rk = sg.seg_rank[sc];
+    f_sc = sg.seg_scale[sc];
+    asm volatile("" : "+v"(beg), "+v"(end), "+v"(ad), "+v"(rk), "+v"(f_sc));   // (all in flight together)
+    if (f_S > 0 && beg <= pc && pc < end && ad >= 0 && ad < a.pv.capacity && rk > 0) {
+      f_ad = ad;
+      f_rows = min(rk, a.pv.max_rank);
+      f_A = (const float*)a.pv.base + (long long)ad * a.pv.slot_elems;
+    }
+    f_r = a.pv.rank[max(f_ad, 0)];                        // (used behind the products)
+#pragma unroll
+    for (int j = 0; j < kF32FusedRank; ++j) vacc[j] = 0.f;
+  }
+  // rank rows j0 .. j0 + RG - 1 at the thread's columns of chunk kb (absent rows
+  // repeat the last, without an adapter they are zeros)
+  auto load_a = [&](int kb, int j0, f32x4_t (&av)[RG][kF32KB / 64]) {
+#pragma unroll
+    for (int j = 0; j < RG; ++j)
+#pragma unroll
+      for (int i = 0; i < kF32KB / 64; ++i)
+        av[j][i] = *(const f32x4_t*)(f_A + (f_rows > 0 ? (long long)min(j0 + j, f_rows - 1) * d_in + min(kb + 64 * i + 4 * tx, d_in - 4) : 0));
+  };
+  // the row of B, in groups of 4 columns below the rank rounded up to 8 (the
+  // rows' pitch; columns past the rank are zero)
+  f32x4_t bq[kF32FusedRank / 4];
+  auto load_b = [&]() {
+    f_r = f_ad >= 0 ? max(min(f_rows, f_r), 0) : 0;
+    const int nb = GATED ? wrow(tx) : min(n0 + tx, d_out - 1);
+    const float* bn = f_A + (f_r > 0 ? a.pv.b_offset + (long long)nb * round_up8(f_r) : 0);
+#pragma unroll
+    for (int g = 0; g < kF32FusedRank / 4; ++g) bq[g] = *(const f32x4_t*)(4 * g < f_r ? bn + 4 * g : (const float*)a.pv.zeros);
+  };
+  auto dot_a = [&](int j0, const f32x4_t (&av)[RG][kF32KB / 64]) {
+#pragma unroll
+    for (int i = 0; i < kF32KB / 64; ++i)                 // (columns past d_in: x is zero in LDS)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float xv = Xs[ty][64 * i + 4 * tx + e];
+#pragma unroll
+        for (int j = 0; j < RG; ++j) vacc[j0 + j] = fmaf(av[j][i][e], xv, vacc[j0 + j]);
+      }
+  };
   for (int kb = 0; kb < d_in; kb += kF32KB) {
 #pragma unroll
     for (int i = 0; i < N4; ++i)
@@ -139,22 +205,46 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
       }
     __syncthreads();
     if (kb + kF32KB < d_in) load(kb + kF32KB);   // uniform
+    f32x4_t av[RG][kF32KB / 64];
+    if constexpr (FUSED) {
+      load_a(kb, 0, av);                                  // in flight during the base product
+      if (kb == 0) load_b();
+    }
 #pragma unroll 16
     for (int kk = 0; kk < kF32KB; ++kk) acc = fmaf(Ws[tx][kk], Xs[ty][kk], acc);
+    if constexpr (FUSED) {
+      dot_a(0, av);
+      if (a.pv.max_rank > RG) {                           // uniform
+        load_a(kb, RG, av);
+        dot_a(RG, av);
+      }
+    }
     __syncthreads();
+  }
+  if constexpr (FUSED) {
+#pragma unroll
+    for (int j = 0; j < kF32FusedRank; ++j)
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) vacc[j] += __shfl_xor(vacc[j], off, 16);
   }
   const int n = GATED ? wrow(tx) : n0 + tx;
   if (!GATED && (n >= d_out || p >= T)) return;
   const SegView& sv = a.sv;
   float val = acc;
-  const int ad = pe4.y, r = min(pe4.z, a.pv.max_rank);
+  const int ad = FUSED ? f_ad : pe4.y, r = min(FUSED ? f_r : pe4.z, a.pv.max_rank);
   if (a.lora_on && ad >= 0 && ad < a.pv.capacity && r > 0) {
     const float* Bb = (const float*)a.pv.base + (long long)ad * a.pv.slot_elems + a.pv.b_offset;
     const float* bn = Bb + (long long)n * round_up8(r);
     const float* vp = a.v_part + (long long)(GATED ? min(p, T - 1) : p) * a.r_ws;
     float lora = 0.f;
-    for (int j = 0; j < r; ++j) lora = fmaf(bn[j], vp[j], lora);
-    val = fmaf(__int_as_float(pe4.w), lora, val);
+    if constexpr (FUSED) {
+#pragma unroll
+      for (int j = 0; j < kF32FusedRank; ++j) lora = fmaf(bq[j / 4][j % 4], j < r ? vacc[j] : 0.f, lora);
+      val = fmaf(f_sc, lora, val);
+    } else {
+      for (int j = 0; j < r; ++j) lora = fmaf(bn[j], vp[j], lora);
+      val = fmaf(__int_as_float(pe4.w), lora, val);
+    }
   }
   int f = n, d_y = d_out;                 // y's column and width
   if constexpr (EPI != kEpiNone) {
@@ -178,14 +268,23 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
   ((float*)a.y)[at] = val;
 }
 
+// With an epilogue, a layer of low rank and at most 512 columns and rows runs
+// in one launch (16 tokens, 256 -> 256, rank 8: 13.8 us in two).
 void launch_linear_f32(const LinearArgs& a, hipStream_t st) {
-  if (a.lora_on && a.seg_grid > 0)
-    hipLaunchKernelGGL(k_shrink_f32, dim3(a.seg_grid), dim3(256), 0, st, a);
+  const bool lora = a.lora_on && a.seg_grid > 0;
+  const bool fused = lora && a.epi_kind != kEpiNone && a.pv.max_rank <= kF32FusedRank && a.d_in <= 512 && a.d_out <= 512;
+  if (lora && !fused) hipLaunchKernelGGL(k_shrink_f32, dim3(a.seg_grid), dim3(256), 0, st, a);
   const int rows = a.epi_kind == kEpiGated ? gated_rows(a.d_out) : a.d_out;
   dim3 grid((rows + kF32Feat - 1) / kF32Feat, (a.T + 15) / 16);
-  if (a.epi_kind == kEpiGated) hipLaunchKernelGGL(k_gemm_f32<kEpiGated>, grid, dim3(256), 0, st, a);
-  else if (a.epi_kind == kEpiPlain) hipLaunchKernelGGL(k_gemm_f32<kEpiPlain>, grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(k_gemm_f32<kEpiNone>, grid, dim3(256), 0, st, a);
+  if (a.epi_kind == kEpiGated) {
+    if (fused) hipLaunchKernelGGL((k_gemm_f32<kEpiGated, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_gemm_f32<kEpiGated, false>), grid, dim3(256), 0, st, a);
+  } else if (a.epi_kind == kEpiPlain) {
+    if (fused) hipLaunchKernelGGL((k_gemm_f32<kEpiPlain, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_gemm_f32<kEpiPlain, false>), grid, dim3(256), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((k_gemm_f32<kEpiNone, false>), grid, dim3(256), 0, st, a);
+  }
 }
 
 }  // namespace mlora
