@@ -46,15 +46,16 @@ struct CombineArgs {
 };
 void launch_combine(const CombineArgs& a, bool bf16, hipStream_t st);
 
-// Item `item` of a batch cut into runs of at most BT positions per expert:
-// its expert and positions [*p0, *p1), or -1 past the last item. Every wave
-// finds it by itself (64 experts per step: one load pair, a wave scan of the
-// run counts, a ballot), so no barrier precedes the weight loads. Starts are
-// clamped into [0, n_pos]: a lying seg_start drops or repeats positions but
-// never leaves the arrays.
-__device__ __forceinline__ int find_expert(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT, int item,
-                                           int* p0, int* p1) {
+// Run `item` of a batch cut into runs of at most BT positions per expert: the
+// expert, its positions [*s0, *s1), its number of runs and the runs before it,
+// or -1 past the last run. Every wave finds it by itself (64 experts per step:
+// one load pair, a wave scan of the run counts, a ballot), so no barrier
+// precedes the weight loads. Starts are clamped into [0, n_pos]: a lying
+// seg_start drops or repeats positions but never leaves the arrays.
+__device__ __forceinline__ int find_run(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT, int item,
+                                        int* s0_, int* s1_, int* runs, int* before) {
   const int lane = threadIdx.x % kWave;
+  int done = 0;
   for (int e0 = 0; e0 < E; e0 += kWave) {
     const int e = min(e0 + lane, E - 1);
     const int s0 = min(max(seg_start[e], 0), n_pos), s1 = min(max(seg_start[e + 1], 0), n_pos);
@@ -65,18 +66,29 @@ __device__ __forceinline__ int find_expert(const int32_t* __restrict__ seg_start
       const int up = __shfl_up(inc, off, kWave);
       if (lane >= off) inc += up;
     }
-    const unsigned long long m = __ballot(inc > item);
+    const unsigned long long m = __ballot(inc > item - done);
     if (m) {   // uniform
       const int l = (int)__builtin_ctzll(m);
-      const int b = __builtin_amdgcn_readlane(s0, l) +
-                    BT * (item - (__builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(n, l)));
-      *p0 = b;
-      *p1 = min(b + BT, __builtin_amdgcn_readlane(s1, l));
+      *s0_ = __builtin_amdgcn_readlane(s0, l);
+      *s1_ = __builtin_amdgcn_readlane(s1, l);
+      *runs = __builtin_amdgcn_readlane(n, l);
+      *before = done + __builtin_amdgcn_readlane(inc, l) - *runs;
       return e0 + l;
     }
-    item -= __builtin_amdgcn_readlane(inc, kWave - 1);
+    done += __builtin_amdgcn_readlane(inc, kWave - 1);
   }
   return -1;
+}
+
+// The same, with the run's positions [*p0, *p1).
+__device__ __forceinline__ int find_expert(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT, int item,
+                                           int* p0, int* p1) {
+  int s0, s1, runs, before;
+  const int e = find_run(seg_start, E, n_pos, BT, item, &s0, &s1, &runs, &before);
+  if (e < 0) return -1;
+  *p0 = s0 + BT * (item - before);
+  *p1 = min(*p0 + BT, s1);
+  return e;
 }
 
 // Runs of at most BT positions in all.

@@ -132,32 +132,49 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
 // expert by a run of up to BT of its positions over the whole of d_in.
 //
 // Order of the tiles: block b runs on XCD b % 8, which takes row tiles xcd, xcd +
-// 8, ... : groups of rg runs, in a group row tile by row tile, its runs side by
-// side. The runs of an expert that are in flight on an XCD share its L2's copy
-// of W, which is read from memory once per group, the row tiles in flight share
-// the rows of x, and the XCDs read neighbouring rows of W at the same time (an
-// eighth of the row tiles in a row for each XCD: 1167 us against 1072, way back of
-// a prefill batch). Groups of 16 runs hold whole experts of such a batch (8
-// experts of about 1024 rows: 1934 us against 1957 with 8 and 1992 with 4); where
-// an expert has one or two runs they share no W, and short groups leave more
-// row tiles to share x. The last n_rt % 8 row tiles go round the XCDs run by run.
+// 8, ... : group of runs by group, in a group row tile by row tile, its runs side
+// by side, so the XCDs read neighbouring rows of W at the same time (an eighth of
+// the row tiles in a row for each XCD: 1167 us against 1072, way back of a prefill
+// batch). The last n_rt % 8 row tiles go round the XCDs run by run.
+//
+// Where experts have several runs, a group is of one expert's, at most 8: the
+// runs in flight on an XCD share its L2's copy of the expert's rows of W, which is
+// read from memory once per group, and the row tiles in flight share the rows of
+// x (prefill batch, 8 experts of about 1024 rows: 1828 us, 1856 with groups of 4,
+// 1893 with groups of 16 runs whatever their expert; 512 tokens: 521 against 553).
+// Where hardly an expert has two, W's bytes decide, and groups of 4 runs of
+// several experts read W from several places at a time (64 tokens, two of eight
+// experts: 326 us against 351 expert by expert; 256 tokens: 379 against 392).
 // ---------------------------------------------------------------------------
+constexpr int kExpertGroup = 8, kRunGroup = 4;
 
-// Tiles of XCD x among `runs` runs by n_rt row tiles, and the j-th of them.
+// Tiles of XCD x among `runs` runs by n_rt row tiles, and the j-th of them: its
+// expert (or -1), positions [*p0, *p1) and row tile.
 __host__ __device__ __forceinline__ int xcd_tiles(int x, int runs, int n_rt) {
   return n_rt / 8 * runs + (n_rt % 8 * runs - x + 7) / 8;
 }
-__device__ __forceinline__ void xcd_tile(int j, int x, int runs, int n_rt, int rg, int* rt, int* run) {
+__device__ __forceinline__ int xcd_tile(const ExpertsArgs& a, int BT, bool by_expert, int j, int x, int runs, int n_rt,
+                                        int* rt, int* p0, int* p1) {
   const int n8 = n_rt / 8;
-  if (j < n8 * runs) {
-    const int group = j / (n8 * rg), k = j - group * n8 * rg, gs = max(min(rg, runs - group * rg), 1);
-    *rt = k / gs * 8 + x;
-    *run = group * rg + k % gs;
-  } else {
+  int run;
+  if (j >= n8 * runs) {
     const int k = (j - n8 * runs) * 8 + x;
     *rt = n8 * 8 + k / runs;
-    *run = k % runs;
+    run = k % runs;
+  } else if (by_expert) {   // uniform
+    int s0, s1, mine, before;
+    if (find_run(a.seg_start, a.E, a.n_pos, BT, j / n8, &s0, &s1, &mine, &before) < 0) return -1;
+    const int k = j - n8 * before, c = k / (n8 * kExpertGroup), kc = k - c * n8 * kExpertGroup;
+    const int gs = max(min(kExpertGroup, mine - c * kExpertGroup), 1);
+    *rt = min(kc / gs, n8 - 1) * 8 + x;
+    run = before + c * kExpertGroup + kc % gs;
+  } else {
+    const int group = j / (n8 * kRunGroup), k = j - group * n8 * kRunGroup, gs = min(kRunGroup, runs - group * kRunGroup);
+    *rt = k / gs * 8 + x;
+    run = group * kRunGroup + k % gs;
   }
+  const int e = find_expert(a.seg_start, a.E, a.n_pos, BT, run, p0, p1);
+  return e >= 0 && *p0 < *p1 ? e : -1;
 }
 
 // One tile: rows r0 .. r0 + BR - 1 by positions p0 .. min(p0 + BT, p1) - 1.
@@ -212,13 +229,13 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0,
 
 template <class C, int OUT>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW / 4, C::NW / 4)))
-void k_experts_tile(ExpertsArgs a, int n_rt, int rg, int max_runs) {
+void k_experts_tile(ExpertsArgs a, int n_rt, int max_runs, bool by_expert) {
   __shared__ __attribute__((aligned(1024))) char lds[C::TILE_BYTES];
   const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
   if (j >= xcd_tiles(x, max_runs, n_rt)) return;   // uniform
-  int rt, run, p0, p1;
-  xcd_tile(j, x, max_runs, n_rt, rg, &rt, &run);   // (of the most runs there can be: the rest find no expert)
-  const int e = find_expert(a.seg_start, a.E, a.n_pos, C::kBT, run, &p0, &p1);
+  int rt, p0, p1;
+  // (of the most runs there can be: the rest find no expert)
+  const int e = xcd_tile(a, C::kBT, by_expert, j, x, max_runs, n_rt, &rt, &p0, &p1);
   if (e < 0) return;   // uniform
   expert_tile<C, OUT, false>(a, e, p0, p1, rt * C::kBR, lds);
 }
@@ -235,7 +252,7 @@ constexpr int kXcdCus = 32;
 
 template <int OUT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void k_experts_tile256(ExpertsArgs a, int n_rt, int rg, int max_runs) {
+void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
   __shared__ __attribute__((aligned(1024))) char lds[Tile256::TILE_BYTES];
   static_assert(Tile256Half::TILE_BYTES <= Tile256::TILE_BYTES && Tile256Quarter::TILE_BYTES <= Tile256::TILE_BYTES, "one LDS block");
   const int runs = min(count_runs(a.seg_start, a.E, a.n_pos, 256), max_runs);   // (more: overlapping segments)
@@ -246,9 +263,8 @@ void k_experts_tile256(ExpertsArgs a, int n_rt, int rg, int max_runs) {
   if (j >= whole + rem * cut) return;   // uniform: past the XCD's last tile
   const int i = j < whole ? j : whole + (j - whole) / cut, piece = j < whole ? 0 : (j - whole) % cut;
   const int parts = j < whole ? 1 : cut;
-  int rt, run, p0, p1;
-  xcd_tile(i, x, runs, n_rt, rg, &rt, &run);
-  const int e = find_expert(a.seg_start, a.E, a.n_pos, 256, run, &p0, &p1);
+  int rt, p0, p1;
+  const int e = xcd_tile(a, 256, true, i, x, runs, n_rt, &rt, &p0, &p1);
   if (e < 0) return;
   // (parts 4: piece & 1 the row half, piece >> 1 the position half; parts 2: the position half)
   const int ph = parts == 4 ? piece >> 1 : piece;
@@ -328,31 +344,28 @@ static void launch_stream(const ExpertsArgs& a, hipStream_t st) {
   else launch_stream_n<TYPE, 4, 4, 4>(a, st);
 }
 
-static int runs_per_group(const ExpertsArgs& a, int BT) {   // by the rows per expert
-  return a.n_pos / std::min(a.E, a.n_pos) >= 2 * BT ? 16 : 4;
-}
-
 template <class C>
 static void launch_tile(const ExpertsArgs& a, hipStream_t st) {
   const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
-  const int n_rt = (rows + C::kBR - 1) / C::kBR, rg = runs_per_group(a, C::kBT);
+  const int n_rt = (rows + C::kBR - 1) / C::kBR;
   const int max_runs = (int)run_bound(a, C::kBT);
+  const bool by_expert = 4ll * a.n_pos >= 3ll * C::kBT * std::min(a.E, a.n_pos);   // a mean of three quarters of a run
   const dim3 grid(8 * xcd_tiles(0, max_runs, n_rt)), block(C::NT);
-  if (a.f32_out) hipLaunchKernelGGL((k_experts_tile<C, 2>), grid, block, 0, st, a, n_rt, rg, max_runs);
-  else if (a.gated) hipLaunchKernelGGL((k_experts_tile<C, 1>), grid, block, 0, st, a, n_rt, rg, max_runs);
-  else hipLaunchKernelGGL((k_experts_tile<C, 0>), grid, block, 0, st, a, n_rt, rg, max_runs);
+  if (a.f32_out) hipLaunchKernelGGL((k_experts_tile<C, 2>), grid, block, 0, st, a, n_rt, max_runs, by_expert);
+  else if (a.gated) hipLaunchKernelGGL((k_experts_tile<C, 1>), grid, block, 0, st, a, n_rt, max_runs, by_expert);
+  else hipLaunchKernelGGL((k_experts_tile<C, 0>), grid, block, 0, st, a, n_rt, max_runs, by_expert);
 }
 
 static void launch_tile256(const ExpertsArgs& a, hipStream_t st) {
   const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
-  const int n_rt = (rows + 255) / 256, rg = runs_per_group(a, 256);
+  const int n_rt = (rows + 255) / 256;
   // per XCD at most its share of the tiles and, where the last ones are cut,
   // 24 pieces more
   const int max_runs = (int)run_bound(a, 256);
   const dim3 grid(8 * (xcd_tiles(0, max_runs, n_rt) + 24)), block(256);
-  if (a.f32_out) hipLaunchKernelGGL(k_experts_tile256<2>, grid, block, 0, st, a, n_rt, rg, max_runs);
-  else if (a.gated) hipLaunchKernelGGL(k_experts_tile256<1>, grid, block, 0, st, a, n_rt, rg, max_runs);
-  else hipLaunchKernelGGL(k_experts_tile256<0>, grid, block, 0, st, a, n_rt, rg, max_runs);
+  if (a.f32_out) hipLaunchKernelGGL(k_experts_tile256<2>, grid, block, 0, st, a, n_rt, max_runs);
+  else if (a.gated) hipLaunchKernelGGL(k_experts_tile256<1>, grid, block, 0, st, a, n_rt, max_runs);
+  else hipLaunchKernelGGL(k_experts_tile256<0>, grid, block, 0, st, a, n_rt, max_runs);
 }
 
 template <bool W8> using Tile128 = GCfg<128, 128, 64, 32, 3, W8 ? 128 : 64, W8 ? 2 : 3, W8>;
