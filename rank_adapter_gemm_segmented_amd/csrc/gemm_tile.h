@@ -170,7 +170,8 @@ struct TileSrc {
 // The caller keeps W's tile and all of x within 4 GB of their bases.
 template <class C>
 struct PipeSrc {
-  static_assert(C::kKB == 32 && C::kNB == C::kNX && !C::kW8, "one chunk column per lane, one request order");
+  static_assert(C::NW == 4 && C::kNB == C::kNX && !C::kW8, "one chunk column per lane, one request order");
+  static constexpr int RPC = 1024 / C::RB, CPR = C::RB / 16;   // rows of a 1 KB chunk, 16-byte chunks of a row
   const char* wb;
   const char* xb;
   uint32_t off[C::DPW];
@@ -179,13 +180,14 @@ struct PipeSrc {
   __device__ __forceinline__ void set(int wave, int lane, const void* w, const void* x, WOff woff, XOff xoff) {
     wb = (const char*)w;
     xb = (const char*)x;
-    // row r = 16 J + lane / 4 of chunk J: r mod 16 and with it the swizzle go by the lane alone
-    const int c = (lane % 4) ^ gswz<32>(lane / 4);
+    // row r = RPC J + lane / CPR of chunk J = 4 j + wave: r mod 16 and with it the
+    // swizzle do not go by j
+    const int c = (lane % CPR) ^ gswz<C::kKB>(wave * RPC + lane / CPR);
     scol = 8 * c;
 #pragma unroll
     for (int i = 0; i < C::DPW; ++i) {
       const bool isx = i >= C::DPW_W;
-      const int r = ((isx ? i - C::DPW_W : i) * C::NW + wave) * 16 + lane / 4;
+      const int r = ((isx ? i - C::DPW_W : i) * C::NW + wave) * RPC + lane / CPR;
       off[i] = (isx ? xoff(r) : woff(r)) + 16 * c;
     }
   }
@@ -246,12 +248,14 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
   };
 
   // Iteration t of the loop requests stage t + NB into the slots that stage t
-  // has freed, one load per few MFMAs (a burst of them holds up the wave at
-  // issue: 2135 us for the largest case, against 1992 spread over 24 of a
-  // stage's 32 MFMAs and 1995 over all of them): the first D1 under the rest of
-  // stage t's last k-step, the others under stage t + 1 before its own boundary.
+  // has freed, one load per few MFMAs of half a stage: a burst of them holds up
+  // the wave at issue, later ones land too late (prefill batch of 8 experts:
+  // 1885 us over a quarter of the stage, 1804 over half, 1828 over three
+  // quarters; 1869 with stages of 32 columns, whose rows are half lines, in rings
+  // of 4). The first D1 go under the rest of stage t's last k-step, the others
+  // under stage t + 1 before its own boundary.
   constexpr int NS = KS * NM;                            // MFMAs of a stage
-  constexpr int SP = NS * 3 / 4;                         // over which its requests are spread
+  constexpr int SP = NS / 2;                             // over which its requests are spread
   auto upto = [](int i) constexpr { return i >= SP ? C::DPW : i * C::DPW / SP; };
   constexpr int D1 = upto(NM - H);
   auto request = [&]<bool WHOLE, int L0, int N>(std::bool_constant<WHOLE>, int t, std::integral_constant<int, L0>,

@@ -1342,7 +1342,7 @@ void launch_linear_bf16(const LinearArgs& a, hipStream_t st) {
   const bool large = a.T > 128 && tiles(256, 256) >= kFill, epi = a.epi_kind != kEpiNone;
   const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
                     (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
-  if (large && epi && near) launch_g<256, 256, 128, 128, 4, 32, 4>(a, st, true);
+  if (large && epi && near) launch_g<256, 256, 128, 128, 2, 64, 2>(a, st, true);
   else if (large && !epi) launch_g<256, 256, 128, 64, 2, 64, 2>(a, st, false);
   else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 64, 3>(a, st, true);
   else if (a.T > 128 && tiles(64, 256) >= kFill) launch_g<64, 256, 64, 64, 3, 64, 3>(a, st, true);
