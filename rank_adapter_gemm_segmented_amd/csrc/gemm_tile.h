@@ -438,48 +438,57 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
           *(f32x4_t*)(tile + l32 * PITCH + (m * 32 + 8 * q + 4 * h) * 4) =
               f32x4_t{acc[m0 + m][n][4 * q], acc[m0 + m][n][4 * q + 1], acc[m0 + m][n][4 * q + 2], acc[m0 + m][n][4 * q + 3]};
       // (wave-private tile: the wave's own LDS writes are ordered before its reads)
-#pragma unroll 1
-      for (int tb = 0; tb < 32; tb += PPP) {
-        const int tl = tb + lane / CPR;
-        const int p = p0 + n * 32 + tl;
-        if (p >= p_end || col >= d_y) continue;
-        const long long at = (long long)row_of(p) * d_y + col;
-        float r8[8], o[8];
-        if (res && vec) {   // uniform (col + 8 <= d_y then)
-          const u32x4_t r = *(const u32x4_t*)(res + at);
+      auto finish = [&](auto plain) {   // plain: whole 16-byte pieces, no residual
+        constexpr bool PLAIN = decltype(plain)::value;
+#pragma unroll 2
+        for (int tb = 0; tb < 32; tb += PPP) {
+          const int tl = tb + lane / CPR;
+          const int p = p0 + n * 32 + tl;
+          if (p >= p_end || col >= d_y) continue;
+          const long long at = (long long)row_of(p) * d_y + col;
+          float r8[8], o[8];
+          if constexpr (!PLAIN) {
+            if (res && vec) {   // uniform (col + 8 <= d_y then)
+              const u32x4_t r = *(const u32x4_t*)(res + at);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r8[e] = __uint_as_float((e & 1) ? (r[e / 2] & 0xffff0000u) : (r[e / 2] << 16));
-        } else {
+              for (int e = 0; e < 8; ++e) r8[e] = __uint_as_float((e & 1) ? (r[e / 2] & 0xffff0000u) : (r[e / 2] << 16));
+            } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r8[e] = res && col + e < d_y ? bf16_bits_to_f32(res[at + e]) : 0.f;
-        }
-        const char* tr = tile + tl * PITCH + lr * 4;
-        const f32x4_t z0 = *(const f32x4_t*)tr, z1 = *(const f32x4_t*)(tr + 16);
-        f32x4_t u0 = z0, u1 = z1;
-        if constexpr (GATED) {
-          u0 = *(const f32x4_t*)(tr + 64);
-          u1 = *(const f32x4_t*)(tr + 80);
-        }
+              for (int e = 0; e < 8; ++e) r8[e] = res && col + e < d_y ? bf16_bits_to_f32(res[at + e]) : 0.f;
+            }
+          }
+          const char* tr = tile + tl * PITCH + lr * 4;
+          const f32x4_t z0 = *(const f32x4_t*)tr, z1 = *(const f32x4_t*)(tr + 16);
+          f32x4_t u0 = z0, u1 = z1;
+          if constexpr (GATED) {
+            u0 = *(const f32x4_t*)(tr + 64);
+            u1 = *(const f32x4_t*)(tr + 80);
+          }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float z = e < 4 ? z0[e] : z1[e - 4];
-          o[e] = C::kW8 ? fmaf(z, sc[e], b[e]) : z + b[e];
-        }
-        activate_n<true>(o, epi.act);
+          for (int e = 0; e < 8; ++e) {
+            const float z = e < 4 ? z0[e] : z1[e - 4];
+            o[e] = C::kW8 ? fmaf(z, sc[e], b[e]) : z + b[e];
+          }
+          activate_n<true>(o, epi.act);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float u = e < 4 ? u0[e] : u1[e - 4];
-          if constexpr (GATED) o[e] *= C::kW8 ? fmaf(u, su[e], bu[e]) : u + bu[e];
-          if (res) o[e] += r8[e];
-        }
-        if (vec) {
-          *(u32x4_t*)(y + at) = u32x4_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]), cvt_pk_bf16(o[6], o[7])};
-        } else {
+          for (int e = 0; e < 8; ++e) {
+            const float u = e < 4 ? u0[e] : u1[e - 4];
+            if constexpr (GATED) o[e] *= C::kW8 ? fmaf(u, su[e], bu[e]) : u + bu[e];
+            if constexpr (!PLAIN) {
+              if (res) o[e] += r8[e];
+            }
+          }
+          if (PLAIN || vec) {
+            *(u32x4_t*)(y + at) = u32x4_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]), cvt_pk_bf16(o[6], o[7])};
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (col + e < d_y) y[at + e] = f32_to_bf16_bits(o[e]);
+            for (int e = 0; e < 8; ++e)
+              if (col + e < d_y) y[at + e] = f32_to_bf16_bits(o[e]);
+          }
         }
-      }
+      };
+      if (vec && !res) finish(std::true_type{});   // uniform
+      else finish(std::false_type{});
     }
   }
 }
