@@ -170,7 +170,7 @@ struct TileSrc {
 // The caller keeps W's tile and all of x within 4 GB of their bases.
 template <class C>
 struct PipeSrc {
-  static_assert(C::NW == 4 && C::kNB == C::kNX && !C::kW8, "one chunk column per lane, one request order");
+  static_assert(C::NW == 4 && C::kNB >= C::kNX && !C::kW8, "one chunk column per lane");
   static constexpr int RPC = 1024 / C::RB, CPR = C::RB / 16;   // rows of a 1 KB chunk, 16-byte chunks of a row
   const char* wb;
   const char* xb;
@@ -186,16 +186,19 @@ struct PipeSrc {
     scol = 8 * c;
 #pragma unroll
     for (int i = 0; i < C::DPW; ++i) {
-      const bool isx = i >= C::DPW_W;
-      const int r = ((isx ? i - C::DPW_W : i) * C::NW + wave) * RPC + lane / CPR;
+      const bool isx = i < C::DPW_X;
+      const int r = ((isx ? i : i - C::DPW_X) * C::NW + wave) * RPC + lane / CPR;
       off[i] = (isx ? xoff(r) : woff(r)) + 16 * c;
     }
   }
-  // load I of stage st; WHOLE: the stage lies inside d_in
+  // load I of iteration t, positions (stage t + NX) before W rows (stage t + NB);
+  // WHOLE: the stages lie inside d_in
   template <int I, bool WHOLE>
-  __device__ __forceinline__ void issue(int st, uint32_t lds0, int wave, int d_in, const void* zeros) const {
-    constexpr bool isx = I >= C::DPW_W;
-    constexpr int j = isx ? I - C::DPW_W : I;
+  __device__ __forceinline__ void issue(int t, uint32_t lds0, int wave, int d_in, const void* zeros) const {
+    constexpr bool isx = I < C::DPW_X;
+    constexpr int j = isx ? I : I - C::DPW_X;
+    const int st = t + (isx ? C::kNX : C::kNB);
+    if (isx && C::kNB > C::kNX && st < 0) return;          // (before the first position stage)
     const uint32_t at = (isx ? lds0 + C::XRING + (uint32_t)(st % C::kNX) * C::XSTAGE_B
                              : lds0 + (uint32_t)(st % C::kNB) * C::WSTAGE_B) + (uint32_t)(j * C::NW + wave) * 1024;
     const char* base = (isx ? xb : wb) + (long long)st * (2 * C::kKB);
@@ -221,9 +224,13 @@ struct PipeSrc {
 template <class C>
 __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, const void* zeros, char* lds,
                                               int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
-  constexpr int KB = C::kKB, NB = C::kNB, KS = KB / 16;
+  constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = KB / 16;
   constexpr int MR = C::MR, MT = C::MT, NM = MR * MT, NF = MR + MT;
   constexpr int H = NM / 4;
+  // loads that may still be in flight at the boundary before stage s: those
+  // requested after its positions' (with a deeper W ring also the W rows behind
+  // them, whose stage comes later; its own W rows were requested before)
+  constexpr int LATER = NB > NX ? C::DPW_W : 0, VMC = (NX - 2) * C::DPW + LATER;
   static_assert(KS % 2 == 0, "fragment sets alternate within a stage");
   const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
@@ -239,7 +246,7 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
       const int m = f == 0 ? 0 : f - MT;
       fa[set][m] = *(const u32x4_t*)(lds + (st % NB) * C::WSTAGE_B + wbase + m * 32 * C::RB + fcol[kk]);
     } else {
-      fb[set][f - 1] = *(const u32x4_t*)(lds + (st % NB) * C::XSTAGE_B + xbase + (f - 1) * 32 * C::RB + fcol[kk]);
+      fb[set][f - 1] = *(const u32x4_t*)(lds + (st % NX) * C::XSTAGE_B + xbase + (f - 1) * 32 * C::RB + fcol[kk]);
     }
   };
   auto mfma = [&](int set, int i) {
@@ -247,20 +254,21 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  // Iteration t of the loop requests stage t + NB into the slots that stage t
-  // has freed, one load per few MFMAs of half a stage: a burst of them holds up
-  // the wave at issue, later ones land too late (prefill batch of 8 experts:
-  // 1885 us over a quarter of the stage, 1804 over half, 1828 over three
-  // quarters; 1869 with stages of 32 columns, whose rows are half lines, in rings
-  // of 4). The first D1 go under the rest of stage t's last k-step, the others
-  // under stage t + 1 before its own boundary.
+  // Iteration t of the loop requests position stage t + NX and W stage t + NB
+  // into the slots that stage t has freed, one load per few MFMAs over three
+  // quarters of a stage: a burst of them holds up the wave at issue, later ones
+  // land too late. The first D1 go under the rest of stage t's last k-step, the
+  // others under stage t + 1 before its own boundary. Prefill batch of 8 experts,
+  // W ring of 3 and x ring of 2 stages: 1707 us, 1732 over half a stage, 1718 over
+  // all of it; 2 + 2 stages: 1804 over half, 1885 over a quarter; stages of 32
+  // columns (rows of half lines) in rings of 4: 1869.
   constexpr int NS = KS * NM;                            // MFMAs of a stage
-  constexpr int SP = NS / 2;                             // over which its requests are spread
+  constexpr int SP = NS * 3 / 4;                         // over which its requests are spread
   auto upto = [](int i) constexpr { return i >= SP ? C::DPW : i * C::DPW / SP; };
   constexpr int D1 = upto(NM - H);
   auto request = [&]<bool WHOLE, int L0, int N>(std::bool_constant<WHOLE>, int t, std::integral_constant<int, L0>,
                                                 std::integral_constant<int, N>) {
-    [&]<int... J>(std::integer_sequence<int, J...>) { (s.template issue<L0 + J, WHOLE>(t + NB, lds0, wave, d_in, zeros), ...); }
+    [&]<int... J>(std::integer_sequence<int, J...>) { (s.template issue<L0 + J, WHOLE>(t, lds0, wave, d_in, zeros), ...); }
     (std::make_integer_sequence<int, N>{});
     if constexpr (N > 0) __builtin_amdgcn_sched_barrier(0);
   };
@@ -285,7 +293,7 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
       mfma(LS, ic.value);
       request_at(whole, st - 1, std::integral_constant<int, NS - H + ic.value>{});
     });
-    vm_barrier<C::VMC>();
+    vm_barrier<VMC>();
     __builtin_amdgcn_sched_barrier(0);
     each(std::make_integer_sequence<int, NM - H>{}, [&](auto ic) {
       constexpr int I = ic.value;
@@ -302,7 +310,7 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
 #pragma unroll
   for (int t = -NB; t < -1; ++t) request(part, t, std::integral_constant<int, 0>{}, std::integral_constant<int, C::DPW>{});
   request(part, -1, std::integral_constant<int, 0>{}, std::integral_constant<int, D1>{});
-  vm_barrier<(NB - 2) * C::DPW + D1>();
+  vm_barrier<VMC + D1>();
 #pragma unroll
   for (int f = 0; f < NF; ++f) frag(0, 0, 0, f);
   int st = 0;

@@ -245,7 +245,7 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int max_runs, bool by_expert) {
 // half of them busy are cut into four (128 x 128) or two (256 x 128) for all of
 // them (the way back of a prefill batch, 72 tiles per XCD: 1072 -> 1007 us). A run
 // of at most 128 positions takes the 256 x 128 form too.
-typedef GCfg<256, 256, 128, 128, 2, 64, 2> Tile256;
+typedef GCfg<256, 256, 128, 128, 3, 64, 2> Tile256;
 typedef GCfg<256, 128, 128, 64, 3, 64, 3> Tile256Half;
 typedef GCfg<128, 128, 64, 64, 4, 64, 4> Tile256Quarter;
 constexpr int kXcdCus = 32;
@@ -253,8 +253,8 @@ constexpr int kXcdCus = 32;
 template <int OUT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
-  __shared__ __attribute__((aligned(1024))) char lds[Tile256Half::TILE_BYTES];
-  static_assert(Tile256::TILE_BYTES <= Tile256Half::TILE_BYTES && Tile256Quarter::TILE_BYTES <= Tile256Half::TILE_BYTES, "one LDS block");
+  __shared__ __attribute__((aligned(1024))) char lds[160 * 1024];
+  static_assert(Tile256::TILE_BYTES <= sizeof(lds) && Tile256Half::TILE_BYTES <= sizeof(lds) && Tile256Quarter::TILE_BYTES <= sizeof(lds), "one LDS block");
   const int runs = min(count_runs(a.seg_start, a.E, a.n_pos, 256), max_runs);   // (more: overlapping segments)
   const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
   const int mine = xcd_tiles(x, runs, n_rt);

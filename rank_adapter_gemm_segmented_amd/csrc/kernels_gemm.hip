@@ -681,8 +681,16 @@ void k_gemm2(LinearArgs a) {
   constexpr bool GATED = EPI == kEpiGated;
   constexpr bool PIPE = BR == 256 && (BR / WR) * (BT / WT) == 4;   // (one wave per SIMD)
   using C = GCfg<BR, BT, WR, WT, NB, KB, NX>;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[C::LDS_BYTES / 2];
-  __shared__ int4 pinfo[BT];
+  // the rings, then what the expand lists: the tile's position entries, each
+  // wave's work units of a rank chunk and run starts. PIPE: the rings take all of
+  // the LDS, and the lists lie in it behind the staged v.
+  constexpr int WRUNS = WT + 1;
+  constexpr int UDESC_AT = BT * 16, WSTART_AT = UDESC_AT + C::NW * kEpiMaxUnits * 16;
+  constexpr int LIST_BYTES = WSTART_AT + (C::NW * WRUNS * 4 + 15) / 16 * 16;
+  constexpr int LIST_AT = PIPE ? 96 * 1024 : C::LDS_BYTES;
+  static_assert(!PIPE || (LIST_AT + LIST_BYTES <= C::LDS_BYTES && BT * (64 + 8) * 4 <= LIST_AT), "v and the lists fit the LDS");
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[(C::LDS_BYTES + (PIPE ? 0 : LIST_BYTES)) / 2];
+  int4* pinfo = (int4*)((char*)lds + LIST_AT);
 
   // wave index made scalar: every per-wave quantity below is then uniform
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
@@ -914,9 +922,8 @@ void k_gemm2(LinearArgs a) {
     const int VP = RC + 8;                           // hi/lo row pitch (bf16)
     uint16_t* vsh = lds;
     uint16_t* vsl = lds + BT * VP;
-    constexpr int WRUNS = WT + 1;
-    __shared__ int wstart[C::NW][WRUNS];             // per-wave run starts (tile positions)
-    __shared__ int4 udesc[C::NW][kEpiMaxUnits];      // per-wave work units of a rank chunk
+    int (*wstart)[WRUNS] = (int (*)[WRUNS])((char*)pinfo + WSTART_AT);                      // per-wave run starts (tile positions)
+    int4 (*udesc)[kEpiMaxUnits] = (int4 (*)[kEpiMaxUnits])((char*)pinfo + UDESC_AT);       // per-wave work units of a rank chunk
 
     const int teff = min(BT, T - t0);
     for (int t = tid; t < BT; t += C::NT) {
@@ -1342,7 +1349,7 @@ void launch_linear_bf16(const LinearArgs& a, hipStream_t st) {
   const bool large = a.T > 128 && tiles(256, 256) >= kFill, epi = a.epi_kind != kEpiNone;
   const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
                     (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
-  if (large && epi && near) launch_g<256, 256, 128, 128, 2, 64, 2>(a, st, true);
+  if (large && epi && near) launch_g<256, 256, 128, 128, 3, 64, 2>(a, st, true);
   else if (large && !epi) launch_g<256, 256, 128, 64, 2, 64, 2>(a, st, false);
   else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 64, 3>(a, st, true);
   else if (a.T > 128 && tiles(64, 256) >= kFill) launch_g<64, 256, 64, 64, 3, 64, 3>(a, st, true);
