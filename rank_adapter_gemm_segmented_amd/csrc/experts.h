@@ -46,63 +46,68 @@ struct CombineArgs {
 };
 void launch_combine(const CombineArgs& a, bool bf16, hipStream_t st);
 
-// Run `item` of a batch cut into runs of at most BT positions per expert: the
-// expert, its positions [*s0, *s1), its number of runs and the runs before it,
-// or -1 past the last run. Every wave finds it by itself (64 experts per step:
-// one load pair, a wave scan of the run counts, a ballot), so no barrier
-// precedes the weight loads. Starts are clamped into [0, n_pos]: a lying
-// seg_start drops or repeats positions but never leaves the arrays.
-__device__ __forceinline__ int find_run(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT, int item,
-                                        int* s0_, int* s1_, int* runs, int* before) {
-  const int lane = threadIdx.x % kWave;
+// A batch cut into runs of at most BT positions per expert. Every wave finds a
+// run by itself, 64 experts per step (one load pair, a wave scan of the run
+// counts, a ballot), so no barrier precedes the weight loads. Starts are clamped
+// into [0, n_pos]: a lying seg_start drops or repeats positions but never leaves
+// the arrays.
+struct RunScan {   // of 64 experts, one per lane
+  int s0, s1;      // positions
+  int n, inc;      // runs, and their inclusive sum over the lanes
+};
+__device__ __forceinline__ RunScan scan_runs(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT, int e0) {
+  const int lane = threadIdx.x % kWave, e = min(e0 + lane, E - 1);
+  RunScan r;
+  r.s0 = min(max(seg_start[e], 0), n_pos);
+  r.s1 = min(max(seg_start[e + 1], 0), n_pos);
+  r.n = e0 + lane < E ? (max(r.s1 - r.s0, 0) + BT - 1) / BT : 0;
+  r.inc = r.n;
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int up = __shfl_up(r.inc, off, kWave);
+    if (lane >= off) r.inc += up;
+  }
+  return r;
+}
+
+// Runs in all; `first` is the scan from expert 0.
+__device__ __forceinline__ int count_runs(const RunScan& first, const int32_t* __restrict__ seg_start, int E, int n_pos, int BT) {
+  int n = __builtin_amdgcn_readlane(first.inc, kWave - 1);
+  for (int e0 = kWave; e0 < E; e0 += kWave)
+    n += __builtin_amdgcn_readlane(scan_runs(seg_start, E, n_pos, BT, e0).inc, kWave - 1);
+  return n;
+}
+
+// Run `item`: its expert (or -1 past the last run), the expert's positions
+// [*s0, *s1), its number of runs and the runs before it.
+__device__ __forceinline__ int find_run(const RunScan& first, const int32_t* __restrict__ seg_start, int E, int n_pos, int BT,
+                                        int item, int* s0, int* s1, int* runs, int* before) {
   int done = 0;
   for (int e0 = 0; e0 < E; e0 += kWave) {
-    const int e = min(e0 + lane, E - 1);
-    const int s0 = min(max(seg_start[e], 0), n_pos), s1 = min(max(seg_start[e + 1], 0), n_pos);
-    const int n = e0 + lane < E ? (max(s1 - s0, 0) + BT - 1) / BT : 0;
-    int inc = n;
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-      const int up = __shfl_up(inc, off, kWave);
-      if (lane >= off) inc += up;
-    }
-    const unsigned long long m = __ballot(inc > item - done);
+    const RunScan r = e0 == 0 ? first : scan_runs(seg_start, E, n_pos, BT, e0);
+    const unsigned long long m = __ballot(r.inc > item - done);
     if (m) {   // uniform
       const int l = (int)__builtin_ctzll(m);
-      *s0_ = __builtin_amdgcn_readlane(s0, l);
-      *s1_ = __builtin_amdgcn_readlane(s1, l);
-      *runs = __builtin_amdgcn_readlane(n, l);
-      *before = done + __builtin_amdgcn_readlane(inc, l) - *runs;
+      *s0 = __builtin_amdgcn_readlane(r.s0, l);
+      *s1 = __builtin_amdgcn_readlane(r.s1, l);
+      *runs = __builtin_amdgcn_readlane(r.n, l);
+      *before = done + __builtin_amdgcn_readlane(r.inc, l) - *runs;
       return e0 + l;
     }
-    done += __builtin_amdgcn_readlane(inc, kWave - 1);
+    done += __builtin_amdgcn_readlane(r.inc, kWave - 1);
   }
   return -1;
 }
 
 // The same, with the run's positions [*p0, *p1).
-__device__ __forceinline__ int find_expert(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT, int item,
-                                           int* p0, int* p1) {
+__device__ __forceinline__ int find_expert(const RunScan& first, const int32_t* __restrict__ seg_start, int E, int n_pos, int BT,
+                                           int item, int* p0, int* p1) {
   int s0, s1, runs, before;
-  const int e = find_run(seg_start, E, n_pos, BT, item, &s0, &s1, &runs, &before);
+  const int e = find_run(first, seg_start, E, n_pos, BT, item, &s0, &s1, &runs, &before);
   if (e < 0) return -1;
   *p0 = s0 + BT * (item - before);
   *p1 = min(*p0 + BT, s1);
   return e;
-}
-
-// Runs of at most BT positions in all.
-__device__ __forceinline__ int count_runs(const int32_t* __restrict__ seg_start, int E, int n_pos, int BT) {
-  const int lane = threadIdx.x % kWave;
-  int n = 0;
-  for (int e0 = 0; e0 < E; e0 += kWave) {
-    const int e = min(e0 + lane, E - 1);
-    const int s0 = min(max(seg_start[e], 0), n_pos), s1 = min(max(seg_start[e + 1], 0), n_pos);
-    n += e0 + lane < E ? (max(s1 - s0, 0) + BT - 1) / BT : 0;
-  }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
-  return __builtin_amdgcn_readfirstlane(n);
 }
 
 }  // namespace mlora

@@ -43,7 +43,8 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
   const int l16 = lane % 16, g = lane / 16;
   const int rt = blockIdx.x;
   int p0, p1;
-  const int e = find_expert(a.seg_start, a.E, a.n_pos, 16 * NTB, (int)(blockIdx.y + blockIdx.z * kGridY), &p0, &p1);
+  const int e = find_expert(scan_runs(a.seg_start, a.E, a.n_pos, 16 * NTB, 0), a.seg_start, a.E, a.n_pos, 16 * NTB,
+                            (int)(blockIdx.y + blockIdx.z * kGridY), &p0, &p1);
   if (e < 0) return;   // uniform: past the last item
   const int d_in = a.d_in, d_out = a.d_out;
   const int v0 = rt * 16 * NR;                                     // first (virtual) row
@@ -153,8 +154,8 @@ constexpr int kExpertGroup = 8, kRunGroup = 4;
 __host__ __device__ __forceinline__ int xcd_tiles(int x, int runs, int n_rt) {
   return n_rt / 8 * runs + (n_rt % 8 * runs - x + 7) / 8;
 }
-__device__ __forceinline__ int xcd_tile(const ExpertsArgs& a, int BT, bool by_expert, int j, int x, int runs, int n_rt,
-                                        int* rt, int* p0, int* p1) {
+__device__ __forceinline__ int xcd_tile(const ExpertsArgs& a, const RunScan& first, int BT, bool by_expert, int j, int x,
+                                        int runs, int n_rt, int* rt, int* p0, int* p1) {
   const int n8 = n_rt / 8;
   int run;
   if (j >= n8 * runs) {
@@ -163,7 +164,7 @@ __device__ __forceinline__ int xcd_tile(const ExpertsArgs& a, int BT, bool by_ex
     run = k % runs;
   } else if (by_expert) {   // uniform
     int s0, s1, mine, before;
-    if (find_run(a.seg_start, a.E, a.n_pos, BT, j / n8, &s0, &s1, &mine, &before) < 0) return -1;
+    if (find_run(first, a.seg_start, a.E, a.n_pos, BT, j / n8, &s0, &s1, &mine, &before) < 0) return -1;
     const int k = j - n8 * before, c = k / (n8 * kExpertGroup), kc = k - c * n8 * kExpertGroup;
     const int gs = max(min(kExpertGroup, mine - c * kExpertGroup), 1);
     *rt = min(kc / gs, n8 - 1) * 8 + x;
@@ -173,7 +174,7 @@ __device__ __forceinline__ int xcd_tile(const ExpertsArgs& a, int BT, bool by_ex
     *rt = k / gs * 8 + x;
     run = group * kRunGroup + k % gs;
   }
-  const int e = find_expert(a.seg_start, a.E, a.n_pos, BT, run, p0, p1);
+  const int e = find_expert(first, a.seg_start, a.E, a.n_pos, BT, run, p0, p1);
   return e >= 0 && *p0 < *p1 ? e : -1;
 }
 
@@ -235,7 +236,8 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int max_runs, bool by_expert) {
   if (j >= xcd_tiles(x, max_runs, n_rt)) return;   // uniform
   int rt, p0, p1;
   // (of the most runs there can be: the rest find no expert)
-  const int e = xcd_tile(a, C::kBT, by_expert, j, x, max_runs, n_rt, &rt, &p0, &p1);
+  const RunScan first = scan_runs(a.seg_start, a.E, a.n_pos, C::kBT, 0);
+  const int e = xcd_tile(a, first, C::kBT, by_expert, j, x, max_runs, n_rt, &rt, &p0, &p1);
   if (e < 0) return;   // uniform
   expert_tile<C, OUT, false>(a, e, p0, p1, rt * C::kBR, lds);
 }
@@ -255,7 +257,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
   __shared__ __attribute__((aligned(1024))) char lds[160 * 1024];
   static_assert(Tile256::TILE_BYTES <= sizeof(lds) && Tile256Half::TILE_BYTES <= sizeof(lds) && Tile256Quarter::TILE_BYTES <= sizeof(lds), "one LDS block");
-  const int runs = min(count_runs(a.seg_start, a.E, a.n_pos, 256), max_runs);   // (more: overlapping segments)
+  const RunScan first = scan_runs(a.seg_start, a.E, a.n_pos, 256, 0);
+  const int runs = min(count_runs(first, a.seg_start, a.E, a.n_pos, 256), max_runs);   // (more: overlapping segments)
   const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
   const int mine = xcd_tiles(x, runs, n_rt);
   const int whole = mine / kXcdCus * kXcdCus, rem = mine - whole;
@@ -264,7 +267,7 @@ void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
   const int i = j < whole ? j : whole + (j - whole) / cut, piece = j < whole ? 0 : (j - whole) % cut;
   const int parts = j < whole ? 1 : cut;
   int rt, p0, p1;
-  const int e = xcd_tile(a, 256, true, i, x, runs, n_rt, &rt, &p0, &p1);
+  const int e = xcd_tile(a, first, 256, true, i, x, runs, n_rt, &rt, &p0, &p1);
   if (e < 0) return;
   // (parts 4: piece & 1 the row half, piece >> 1 the position half; parts 2: the position half)
   const int ph = parts == 4 ? piece >> 1 : piece;
