@@ -281,6 +281,11 @@ void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
 // ---------------------------------------------------------------------------
 // Way back: a token's rows weighted, summed in slot order and added to the
 // residual, in fp32, one rounding. A thread takes 4 columns of one token.
+//
+// The products stay in fp32 between the two kernels: with bf16 rows a token's sum
+// would carry top_k more roundings. A prefill batch (8192 rows of 4096) moves 200
+// MB here, 47 us at 4.3 TB/s, of 886 in all; a decode batch 7 us, mostly the
+// launch.
 // ---------------------------------------------------------------------------
 template <typename E_>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs a) {

@@ -93,6 +93,16 @@ def test_no_work_and_sizes():
     assert lib.mlora_experts_workspace_bytes(64, 8, 4, 4096, 1) == 0 and lib.mlora_experts_workspace_bytes(64, 8, 64, 0, 1) == 0
 
 
+@pytest.mark.parametrize("n_experts", [1, 8, 127, 1024])
+def test_a_workspace_for_a_batch_holds_every_smaller_one(n_experts):
+    lib, _ = _lib()
+    T = sorted({1 << i for i in range(21)} | {(1 << i) + 1 for i in range(20)} | set(range(8000, 8400, 7)) | set(range(127, 131)))
+    sizes = [lib.mlora_route_workspace_bytes(t, n_experts, 1) for t in T]
+    assert sizes == sorted(sizes)
+    sizes = [lib.mlora_experts_workspace_bytes(t, 1, n_experts, 48, 0) for t in T]
+    assert sizes == sorted(sizes)
+
+
 def test_epilogue_of_no_pool():
     lib, E = _lib()
     none = ctypes.c_void_p(None)
