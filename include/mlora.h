@@ -338,14 +338,16 @@ int mlora_validate(mlora_pool_t pool, const int32_t* seg_start, const int32_t* s
  * [n_experts + 1] with segment e the positions of expert e, and token_index.
  *
  * n_experts in 1 .. MLORA_MAX_EXPERTS, top_k in 1 .. MLORA_MAX_TOP_K and at
- * most n_experts, at most MLORA_MAX_POSITIONS slots.
+ * most n_experts, n_tokens at most MLORA_MAX_TOKENS, at most
+ * MLORA_MAX_POSITIONS slots, and slots times d_out at most MLORA_MAX_PRODUCT.
  * ---------------------------------------------------------------------- */
 #define MLORA_MAX_EXPERTS 1024
 #define MLORA_MAX_TOP_K 64
 #define MLORA_MAX_POSITIONS (1 << 23)
+#define MLORA_MAX_PRODUCT (1ll << 36)
 
-/* Bytes of workspace mlora_route needs (0 if a size is out of range). The
- * workspace needs no initialization and holds nothing between calls. */
+/* Bytes of workspace mlora_route needs for up to n_tokens tokens (0 if a size
+ * is out of range). It needs no initialization and holds nothing between calls. */
 size_t mlora_route_workspace_bytes(int n_tokens, int n_experts, int top_k);
 
 /* Choose top_k experts per token and group the batch by expert.
@@ -385,8 +387,9 @@ int mlora_experts_linear(const void* x, const void* W, const float* w_scale, int
                          const int32_t* token_index, int n_pos, const mlora_epilogue_t* epilogue, void* y,
                          hipStream_t stream);
 
-/* Bytes of workspace mlora_experts_combine needs (0 if a size is out of
- * range). It needs no initialization and holds nothing between calls. */
+/* Bytes of workspace mlora_experts_combine needs for up to n_tokens tokens (0 if
+ * a size is out of range). It needs no initialization and holds nothing between
+ * calls. */
 size_t mlora_experts_workspace_bytes(int n_tokens, int top_k, int n_experts, int d_out, int dtype);
 
 /* out[t] = residual[t] + sum over j of weight[t, j] (W_e h[p] + bias_e), with

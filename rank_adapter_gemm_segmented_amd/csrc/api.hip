@@ -101,17 +101,9 @@ WsLayout ws_layout(const mlora_pool_s* p, int T) {
   L.seg_scale = take(t1 * 4);
   L.n_seg = take(16);
   L.counts = take(t1 * 4);
-  // decode plan: of the d_out rows or, with an even d_out, of a gated call's
-  // virtual rows (up to 30 more), whichever needs more
+  // (a gated call's virtual rows, whole blocks of 32, make as many tiles of 64)
   int n_tiles = 0, kc = 0, n_chunks = 0;
   decode_plan(p->d_in, p->d_out, &n_tiles, &kc, &n_chunks);
-  size_t part_tiles = (size_t)n_chunks * n_tiles;
-  if (p->d_out % 2 == 0) {
-    int gt = 0, gk = 0, gc = 0;
-    decode_plan(p->d_in, gated_rows(p->d_out), &gt, &gk, &gc);
-    part_tiles = std::max(part_tiles, (size_t)gc * gt);
-    n_chunks = std::max(n_chunks, gc);
-  }
   // shrink partial slices: split-K of the large-T path (at most
   // kMaxShrinkSplit), and at T <= 64 also 8 waves per d_in chunk of the
   // decode stream
@@ -120,7 +112,7 @@ WsLayout ws_layout(const mlora_pool_s* p, int T) {
   L.v_part = take((size_t)splits * T * r_ws_of(p->max_rank) * 4);
   // decode partial tiles, only for token counts the decode path takes
   const size_t tt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-  L.ypart = take(p->dtype == MLORA_BF16 && T <= 64 ? part_tiles * 64 * tt * 4 : 0);
+  L.ypart = take(p->dtype == MLORA_BF16 && T <= 64 ? (size_t)n_chunks * n_tiles * 64 * tt * 4 : 0);
   L.pos_info = take((size_t)T * 16);
   L.v_fin = take((size_t)T * r_ws_of(p->max_rank) * 4);
   L.delta = take(delta_bytes(p, T));
@@ -282,7 +274,7 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
       d.r_ws = a.r_ws;
       d.epi_kind = a.epi_kind;
       d.epi = a.epi;
-      decode_plan(pool->d_in, a.epi_kind == kEpiGated ? gated_rows(pool->d_out) : pool->d_out, &d.n_tiles, &d.kc, &d.n_chunks);
+      decode_plan(pool->d_in, pool->d_out, &d.n_tiles, &d.kc, &d.n_chunks);
       d.unit_rows = decode_unit_rows(lora_on ? sv.n_seg : 0, pool->max_rank, d.n_tiles);
       d.w_scale = w_scale;
       if (log_calls())

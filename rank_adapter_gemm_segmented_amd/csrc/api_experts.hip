@@ -19,14 +19,16 @@ bool batch_ok(int n_tokens, int n_experts, int top_k) {
          (long long)n_tokens * top_k <= MLORA_MAX_POSITIONS;
 }
 
-// Checks shared by the two expert products. Returns a status.
+// Checks shared by the two expert products. Returns a status. (The limit on
+// n_pos d_out keeps a launch of the tiled forms, 512 threads per 128 x 128 tile
+// and less than one part tile per expert and run, under 2^32 threads.)
 int check_product(int dtype, const float* w_scale, int n_experts, int d_in, int d_out, long long n_pos) {
   if (dtype != MLORA_F32 && dtype != MLORA_BF16) return MLORA_ERR_DTYPE;
   if (w_scale && dtype != MLORA_BF16) return MLORA_ERR_DTYPE;
   if (n_experts < 1 || n_experts > MLORA_MAX_EXPERTS) return MLORA_ERR_SHAPE;
   if (d_in < 1 || d_in > MLORA_MAX_DIM || d_out < 1 || d_out > MLORA_MAX_DIM) return MLORA_ERR_SHAPE;
   if (d_in % (w_scale ? 16 : dtype == MLORA_F32 ? 4 : 8) != 0) return MLORA_ERR_SHAPE;
-  if (n_pos < 0 || n_pos > MLORA_MAX_POSITIONS) return MLORA_ERR_SHAPE;
+  if (n_pos < 0 || n_pos > MLORA_MAX_POSITIONS || n_pos * d_out > MLORA_MAX_PRODUCT) return MLORA_ERR_SHAPE;
   return MLORA_OK;
 }
 
@@ -107,6 +109,7 @@ int mlora_experts_linear(const void* x, const void* W, const float* w_scale, int
 size_t mlora_experts_workspace_bytes(int n_tokens, int top_k, int n_experts, int d_out, int dtype) {
   if (!batch_ok(n_tokens, n_experts, top_k) || d_out < 1 || d_out > MLORA_MAX_DIM) return 0;
   if (dtype != MLORA_F32 && dtype != MLORA_BF16) return 0;
+  if ((long long)n_tokens * top_k * d_out > MLORA_MAX_PRODUCT) return 0;
   const size_t b = ((size_t)n_tokens * top_k * d_out * 4 + 255) / 256 * 256;
   return b < 256 ? 256 : b;
 }

@@ -28,8 +28,6 @@ __device__ __forceinline__ void dma16(const void* g, uint32_t m0) {
                : "memory", "m0");
 }
 
-// Wait until at most N of this wave's vector memory operations are in flight,
-// then a workgroup barrier (LDS and scalar counters drained too; nothing else).
 // The same load marked nontemporal, for W rows that the launch reads once
 // (at most two position tiles, which run in the same round): measured on the
 // verify and heterogeneous batches, their LoRA-off passes took 1-2 us less

@@ -103,6 +103,14 @@ def test_a_workspace_for_a_batch_holds_every_smaller_one(n_experts):
     assert sizes == sorted(sizes)
 
 
+def test_products_past_the_largest_are_refused():
+    lib, E = _lib()
+    assert lib.mlora_experts_workspace_bytes(1 << 20, 8, 8, 1 << 13, 1) == 1 << 38      # 2^36 elements in fp32
+    assert lib.mlora_experts_workspace_bytes(1 << 20, 8, 8, (1 << 13) + 8, 1) == 0
+    assert lib.mlora_experts_linear(FAKE, FAKE, None, 1, 1 << 20, 8, 64, (1 << 13) + 8, FAKE, FAKE, 1 << 23, None, FAKE, None) == E["MLORA_ERR_SHAPE"]
+    assert _combine(T=1 << 20, k=8, E=8, d_out=(1 << 13) + 8) == E["MLORA_ERR_SHAPE"]
+
+
 def test_epilogue_of_no_pool():
     lib, E = _lib()
     none = ctypes.c_void_p(None)
