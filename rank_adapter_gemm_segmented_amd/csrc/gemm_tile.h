@@ -230,6 +230,7 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
   // them, whose stage comes later; its own W rows were requested before)
   constexpr int LATER = NB > NX ? C::DPW_W : 0, VMC = (NX - 2) * C::DPW + LATER;
   static_assert(KS % 2 == 0, "fragment sets alternate within a stage");
+  static_assert(NF <= NM, "a read per MFMA at most");
   const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   int fcol[KS];
@@ -296,7 +297,11 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
     each(std::make_integer_sequence<int, NM - H>{}, [&](auto ic) {
       constexpr int I = ic.value;
       mfma(LS, H + I);
-      if constexpr (I < NF) frag(st + 1, 0, 0, I);
+      // a read per MFMA, or more where the fragments outnumber them (64 x 64 per wave)
+      constexpr int F0 = NF <= NM - H ? (I < NF ? I : NF) : I * NF / (NM - H);
+      constexpr int F1 = NF <= NM - H ? (I + 1 < NF ? I + 1 : NF) : (I + 1) * NF / (NM - H);
+#pragma unroll
+      for (int f = F0; f < F1; ++f) frag(st + 1, 0, 0, f);
       __builtin_amdgcn_sched_barrier(0);
       request_at(whole, st, ic);
     });

@@ -93,6 +93,35 @@ def test_long_segments(counts, gated):
     _product("bf16", counts, 136, 520, "gelu", gated, bias=False, seed=4)
 
 
+# Sixteen experts on layers wide enough for the tiled forms: means of 5, 30, 100 (tiles of 32, 64, 128 positions) and
+# 200 rows (256). The last by how an XCD's tiles fill rounds of 32: 2 over (quarters), 11 over (halves), none, and runs
+# of at most 128 positions.
+TILED = {
+    "mean 5": [5, 1, 0, 9, 12, 3, 4, 8, 2, 5, 7, 6, 0, 33, 1, 4],
+    "mean 30": [30, 65, 0, 1, 64, 63, 12, 40, 31, 33, 32, 2, 70, 20, 0, 35],
+    "mean 100": [128, 129, 1, 0, 127, 257, 100, 90, 64, 110, 96, 140, 33, 200, 95, 60],
+    "200 each": [200] * 16,
+    "short runs": [2000, 1100, 90, 10] + [0] * 12,
+    "one expert": [0] * 7 + [3301] + [0] * 8,
+    "20 runs": [257, 513, 129, 1, 256, 255, 128, 0, 385, 300, 290, 130, 140, 260, 127, 100],
+}
+
+
+@pytest.mark.parametrize("counts", TILED.values(), ids=TILED.keys())
+@pytest.mark.parametrize("d_in,d_out", [(72, 2056), (520, 4104), (264, 4344)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_tiled(counts, d_in, d_out, gated):
+    log(f"[experts] tiled, {len(counts)} experts, {sum(counts)} rows, {d_in}->{d_out} gated={gated}")
+    _product("bf16", counts, d_in, d_out, "silu" if gated else "gelu_tanh", gated, bias=True, seed=d_in)
+
+
+@pytest.mark.parametrize("name", ["mean 30", "mean 100", "200 each"])
+@pytest.mark.parametrize("gated", [True, False])
+def test_tiled_fp8(name, gated):
+    log(f"[experts] tiled FP8, {name} gated={gated}")
+    _product("fp8w", TILED[name], 272, 2056, "silu", gated, bias=True, seed=8)
+
+
 def test_many_experts():
     log("[experts] 200 experts, most of them empty")
     counts = [0] * 200
@@ -187,6 +216,14 @@ def test_layer(kind, T, E, k, d, f, pad):
 def test_layer_large():
     log("[experts] layer bf16, 1500 tokens")
     _layer("bf16", 1500, 4, 2, 512, 768, bias=True, pad=100, seed=5)
+
+
+@pytest.mark.parametrize("kind,T,E,k,d,f,pad", [("bf16", 1600, 16, 2, 4104, 136, 0), ("bf16", 1024, 8, 2, 4104, 520, 9),
+                                                ("bf16", 2048, 8, 2, 4096, 264, 0), ("bf16", 350, 16, 4, 2056, 1040, 0),
+                                                ("bf16", 40, 16, 2, 2056, 1032, 3), ("fp8w", 400, 16, 2, 2064, 1040, 0)])
+def test_layer_tiled(kind, T, E, k, d, f, pad):
+    log(f"[experts] layer {kind}, tiled, T={T} E={E} k={k} {d}->{f}")
+    _layer(kind, T, E, k, d, f, bias=True, pad=pad, seed=T)
 
 
 def test_layer_repeats_in_place_and_captured():
