@@ -129,6 +129,19 @@ def test_tiled(i, gated):
     layer.check(ACTS[(i + 2) % 5], lora_on=0)
 
 
+# the 64x256 tile, and the largest one over many stages, with many short segments, high ranks and fused pools
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,d_in,d_out,kw", [
+    (257, 264, 6402, {}), (769, 1040, 16402, {"max_run": 100}), (2050, 520, 6146, {"max_run": 3}),
+    (1100, 264, 12320, {"max_run": 2, "ranks": (64, 16, 33, 128)}), (1030, 136, 12288, {"max_run": 60, "ranks": (200, 8)}),
+    (1100, 264, 12320, {"max_run": 30, "ranks": (16, 24), "fused": True})])
+def test_tiled_segments(T, d_in, d_out, kw, gated):
+    log(f"[epilogue] tiled T={T} {d_in}->{d_out} {kw} gated={gated}")
+    layer = Layer(torch.bfloat16, T, d_in, d_out, gated, seed=T, shuffled=True, **kw)
+    layer.check("silu")
+    layer.check("relu", lora_on=0)
+
+
 @pytest.mark.parametrize("gated", [False, True])
 def test_tiled_mfma_and_dense_expand(gated, monkeypatch):
     log(f"[epilogue] both expand forms gated={gated}")
