@@ -381,7 +381,11 @@ template <bool W8> using Tile64 = GCfg<128, 64, 32, 32, 4, W8 ? 128 : 64, 4, W8>
 typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
 
 // Form by the rows per expert. Up to two (FP8: twenty), the streaming form; it
-// also takes what has too few tiles for the card, and fp32. Then tiles of 32, 64,
+// also takes fp32 and what has too few tiles for the card: fewer than 256 of 32
+// positions (24 tokens, two of eight experts, 4096 -> 2048, 128 tiles: 27.6 us
+// streamed, 33.8 tiled), fewer than 64 of more (100 tokens, 4096 -> 1024, 64 tiles:
+// 30.1 streamed, 24.0 tiled; FP8, 100 tokens over 4 experts, 32 tiles: 16.1 and
+// 20.5). Then tiles of 32, 64,
 // 128 and 256 positions, the smallest that holds most experts' rows: W, which
 // decides the time up to about 100 rows, is then read once, and the tile's
 // rings keep more of it requested than registers can. Two of eight experts,
@@ -399,7 +403,9 @@ static void launch_bf16(const ExpertsArgs& a, hipStream_t st) {
   // the largest tile addresses x and its rows of W by 32-bit offsets
   const bool near = 2ll * a.n_rows * a.d_in < (1ll << 32) && (a.gated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
   const long long tiles256 = (rows + 255) / 256 * (a.n_pos / 256 + active / 2);   // of about this many
-  if (mean <= (W8 ? 20 : 2) || (rows + 127) / 128 * active < 256) return launch_stream<W8 ? kXFp8w : kXBf16>(a, st);
+  const int bt = mean <= 8 ? 32 : mean <= 48 ? 64 : 128;
+  const long long tiles = (rows + 127) / 128 * std::max(active, a.n_pos / bt + active / 2);
+  if (mean <= (W8 ? 20 : 2) || tiles < (mean <= 8 ? 256 : 64)) return launch_stream<W8 ? kXFp8w : kXBf16>(a, st);
   if constexpr (!W8) {
     if (mean <= 8) return launch_tile<Tile32>(a, st);
     if (near && (mean >= 192 || (mean >= 112 && tiles256 >= 1024))) return launch_tile256(a, st);
