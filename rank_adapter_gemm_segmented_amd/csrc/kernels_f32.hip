@@ -9,15 +9,45 @@
 
 namespace mlora {
 
+// v of sorted position p for rank rows j0 .. j0 + kF32Rows - 1 below r, by one wave:
+// the 64 lanes split d_in (16-byte loads, lane l at k = 4l + 256 i), every load of
+// the group in flight; each row's partial sums are added across the wave with
+// xor shuffles (a fixed order).
+constexpr int kF32Rows = 8;
+__device__ __forceinline__ void shrink_rows(const LinearArgs& a, int p, const float* __restrict__ Aa, int j0, int r) {
+  const int lane = threadIdx.x % kWave, d_in = a.d_in;   // d_in: a multiple of 4
+  int row = a.sv.token_index ? a.sv.token_index[p] : p;
+  row = min(max(row, 0), a.T - 1);
+  const float* xr = (const float*)a.x + (long long)row * d_in;
+  float acc[kF32Rows];
+#pragma unroll
+  for (int i = 0; i < kF32Rows; ++i) acc[i] = 0.f;
+  for (int k = 4 * lane; k < d_in; k += 4 * kWave) {
+    const f32x4_t xv = *(const f32x4_t*)(xr + k);
+    f32x4_t av[kF32Rows];
+#pragma unroll
+    for (int i = 0; i < kF32Rows; ++i) av[i] = *(const f32x4_t*)(Aa + (long long)min(j0 + i, r - 1) * d_in + k);
+#pragma unroll
+    for (int i = 0; i < kF32Rows; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i] = fmaf(av[i][c], xv[c], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kF32Rows; ++i) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) acc[i] += __shfl_xor(acc[i], off, kWave);
+  }
+  if (lane < kF32Rows && j0 + lane < r) {
+    float v = acc[0];
+#pragma unroll
+    for (int i = 1; i < kF32Rows; ++i) v = lane == i ? acc[i] : v;
+    a.v_part[(long long)p * a.r_ws + j0 + lane] = v;
+  }
+}
+
 // v_part[0][p][j] = sum_k A_a[j,k] x[row(p),k]; one workgroup per segment,
 // which also writes its positions' entries of the position table.
-// Wave w takes positions ps + w, ps + w + 4, ...; for a position, groups of
-// kF32Rows rank rows are read together (every load of the group in flight),
-// the 64 lanes splitting d_in (16-byte loads, lane l at k = 4l + 256 i); each
-// row's partial sums are added across the wave with xor shuffles (a fixed
-// order).
-constexpr int kF32Rows = 8;
-
+// Wave w takes positions ps + w, ps + w + 4, ...
 __global__ __launch_bounds__(256) void k_shrink_f32(LinearArgs a) {
   const int s = blockIdx.x;
   const SegView& sv = a.sv;
@@ -32,41 +62,27 @@ __global__ __launch_bounds__(256) void k_shrink_f32(LinearArgs a) {
   for (int p = ps + (int)threadIdx.x; p < pe; p += 256)
     a.pos_info[p] = make_int4(s, ad, ad >= 0 ? r : 0, __float_as_int(ad >= 0 ? sv.seg_scale[s] : 0.f));
   if (ad < 0) return;
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const float* __restrict__ x = (const float*)a.x;
+  const int wave = threadIdx.x / kWave;
   const float* __restrict__ Aa = (const float*)a.pv.base + (long long)ad * a.pv.slot_elems;
-  const int d_in = a.d_in;   // a multiple of 4
-  for (int p = ps + wave; p < pe; p += 4) {
-    int row = sv.token_index ? sv.token_index[p] : p;
-    row = min(max(row, 0), a.T - 1);
-    const float* xr = x + (long long)row * d_in;
-    for (int j0 = 0; j0 < r; j0 += kF32Rows) {
-      float acc[kF32Rows];
-#pragma unroll
-      for (int i = 0; i < kF32Rows; ++i) acc[i] = 0.f;
-      for (int k = 4 * lane; k < d_in; k += 4 * kWave) {
-        const f32x4_t xv = *(const f32x4_t*)(xr + k);
-        f32x4_t av[kF32Rows];
-#pragma unroll
-        for (int i = 0; i < kF32Rows; ++i) av[i] = *(const f32x4_t*)(Aa + (long long)min(j0 + i, r - 1) * d_in + k);
-#pragma unroll
-        for (int i = 0; i < kF32Rows; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i] = fmaf(av[i][c], xv[c], acc[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kF32Rows; ++i) {
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) acc[i] += __shfl_xor(acc[i], off, kWave);
-      }
-      if (lane < kF32Rows && j0 + lane < r) {
-        float v = acc[0];
-#pragma unroll
-        for (int i = 1; i < kF32Rows; ++i) v = lane == i ? acc[i] : v;
-        a.v_part[(long long)p * a.r_ws + j0 + lane] = v;
-      }
-    }
-  }
+  for (int p = ps + wave; p < pe; p += 4)
+    for (int j0 = 0; j0 < r; j0 += kF32Rows) shrink_rows(a, p, Aa, j0, r);
+}
+
+// The same by position, for calls with an epilogue: a wave per position and group
+// of rank rows, which finds its segment itself, so that a long segment spreads
+// over the card. v has the bits of k_shrink_f32.
+__global__ __launch_bounds__(256) void k_shrink_f32_wide(LinearArgs a) {
+  const SegView& sv = a.sv;
+  const int p = blockIdx.x * 4 + threadIdx.x / kWave, j0 = blockIdx.y * kF32Rows;
+  if (p >= a.T) return;   // (no barrier)
+  const int S = seg_count(sv);
+  const int s = S > 0 ? min(max(find_segment(sv.seg_start, S, p), 0), S - 1) : 0;
+  int r = 0, ad = -1;
+  if (S > 0 && sv.seg_start[s] <= p && p < sv.seg_start[s + 1]) ad = seg_adapter_checked(sv, a.pv, s, &r);
+  if (j0 == 0 && threadIdx.x % kWave == 0)
+    a.pos_info[p] = make_int4(s, ad, ad >= 0 ? r : 0, __float_as_int(ad >= 0 ? sv.seg_scale[s] : 0.f));
+  if (ad < 0 || j0 >= r) return;
+  shrink_rows(a, p, (const float*)a.pv.base + (long long)ad * a.pv.slot_elems, j0, r);
 }
 
 // Tile: 16 output features x 16 sorted positions, one output per thread
@@ -86,7 +102,7 @@ constexpr int kF32FusedRank = 16;   // largest rank of the fused shrink (two gro
 // FUSED: the shrink runs here too (no k_shrink_f32, no table): the 16 threads of
 // a position split each chunk's columns among them and keep partial dot
 // products with the position's rank rows, 4 loads of 16 bytes a row. Every
-// feature tile repeats it, which a small layer hides under its latency.
+// feature tile repeats it.
 template <int EPI, bool FUSED>
 __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
   constexpr bool GATED = EPI == kEpiGated;
@@ -268,16 +284,21 @@ __global__ __launch_bounds__(256) void k_gemm_f32(LinearArgs a) {
   ((float*)a.y)[at] = val;
 }
 
-// With an epilogue, a layer of low rank and at most 512 columns and rows runs
-// in one launch. us a call, two launches first: 16 tokens, 256 -> 256, rank 8: 12.3
-// and 10.0; 512 -> 512, rank 16: 16 tokens 19.9 and 19.0, 64 tokens 25.7 and 19.0,
-// 1024 tokens 228 and 147; rank 8, 4096 tokens: 514 and 502.
+// With an epilogue the shrink is the wide one (512 -> 512, rank 16, 1024 tokens of
+// 16 segments: 228 us with a workgroup per segment, 47 with it; 408 -> 101, rank
+// 64, 100 tokens of 4 segments: 188 and 20), or fused where one chunk holds d_in,
+// ranks are low and the tiles are at most one per CU, since each repeats it (256
+// -> 256, rank 8: 16 tokens 10.0 us fused, 11.3 in two launches; 1024 tokens 38 and
+// 19; 512 -> 512, 16 tokens: 19.0 and 14.2).
 void launch_linear_f32(const LinearArgs& a, hipStream_t st) {
   const bool lora = a.lora_on && a.seg_grid > 0;
-  const bool fused = lora && a.epi_kind != kEpiNone && a.pv.max_rank <= kF32FusedRank && a.d_in <= 512 && a.d_out <= 512;
-  if (lora && !fused) hipLaunchKernelGGL(k_shrink_f32, dim3(a.seg_grid), dim3(256), 0, st, a);
   const int rows = a.epi_kind == kEpiGated ? gated_rows(a.d_out) : a.d_out;
-  dim3 grid((rows + kF32Feat - 1) / kF32Feat, (a.T + 15) / 16);
+  const dim3 grid((rows + kF32Feat - 1) / kF32Feat, (a.T + 15) / 16);
+  const bool fused = lora && a.epi_kind != kEpiNone && a.pv.max_rank <= kF32FusedRank && a.d_in <= kF32KB && grid.x * grid.y <= 256;
+  if (lora && !fused) {
+    if (a.epi_kind == kEpiNone) hipLaunchKernelGGL(k_shrink_f32, dim3(a.seg_grid), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(k_shrink_f32_wide, dim3((a.T + 3) / 4, (a.pv.max_rank + kF32Rows - 1) / kF32Rows), dim3(256), 0, st, a);
+  }
   if (a.epi_kind == kEpiGated) {
     if (fused) hipLaunchKernelGGL((k_gemm_f32<kEpiGated, true>), grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_gemm_f32<kEpiGated, false>), grid, dim3(256), 0, st, a);

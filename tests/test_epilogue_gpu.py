@@ -170,6 +170,16 @@ def test_f32(T, d_in, d_out, gated):
     layer.check("gelu", lora_on=0)
 
 
+@pytest.mark.parametrize("T,d_in,d_out,kw", [(300, 256, 256, {}), (600, 516, 130, {"ranks": (64, 40, 17), "max_run": 90}),
+                                             (3, 1024, 64, {"ranks": (200, 9), "max_run": 1}), (77, 260, 514, {"ranks": (16,), "max_run": 2})])
+@pytest.mark.parametrize("gated", [False, True])
+def test_f32_by_position(T, d_in, d_out, kw, gated):
+    log(f"[epilogue] f32 T={T} {d_in}->{d_out} {kw} gated={gated}")
+    layer = Layer(torch.float32, T, d_in, d_out, gated, seed=T, shuffled=T > 20, **kw)
+    layer.check("silu")
+    layer.check("none", lora_on=0)
+
+
 @pytest.mark.parametrize("T,d_in,d_out", [(1, 1040, 450), (20, 272, 64), (64, 2064, 520)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_fp8_weight(T, d_in, d_out, gated):
