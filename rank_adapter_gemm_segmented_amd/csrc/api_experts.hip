@@ -110,7 +110,7 @@ size_t mlora_experts_workspace_bytes(int n_tokens, int top_k, int n_experts, int
   if (!batch_ok(n_tokens, n_experts, top_k) || d_out < 1 || d_out > MLORA_MAX_DIM) return 0;
   if (dtype != MLORA_F32 && dtype != MLORA_BF16) return 0;
   if ((long long)n_tokens * top_k * d_out > MLORA_MAX_PRODUCT) return 0;
-  const size_t b = ((size_t)n_tokens * top_k * d_out * 4 + 255) / 256 * 256;
+  const size_t b = ((size_t)n_tokens * top_k * f32_pitch(d_out) * 4 + 255) / 256 * 256;
   return b < 256 ? 256 : b;
 }
 

@@ -84,6 +84,14 @@ __device__ __forceinline__ void activate_n(float (&z)[N], int act) {
   }
 }
 
+// Vectors of bf16 or fp32 elements at any element's address: rows of y need not
+// start on a 16-byte boundary (a width that is no multiple of 8), and global
+// memory takes wide accesses at any address (2087 tokens, 1072 -> 13740 with a
+// residual: 158 us, 214 by single elements).
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef u32x2_t u32x2_any __attribute__((aligned(2)));
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+
 // One element of bias or residual.
 template <typename E>
 __device__ __forceinline__ float elem_f32(const void* p, long long i);

@@ -27,7 +27,7 @@ struct ExpertsArgs {
   const void* x;                // [n_rows, d_in]
   const void* W;                // [E, d_out, d_in]
   const float* w_scale;         // [E, d_out]: W holds e4m3 codes; null: W in x's type
-  void* y;                      // [n_pos, d_y]; fp32 [n_pos, d_out] where f32_out
+  void* y;                      // [n_pos, d_y]; where f32_out fp32 [n_pos, f32_pitch(d_out)]
   const int32_t* seg_start;     // [E + 1]
   const int32_t* token_index;   // [n_pos] or null
   int n_rows, E, d_in, d_out, n_pos;
@@ -36,8 +36,12 @@ struct ExpertsArgs {
 };
 void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st);
 
+// Row pitch of the products on the way back: whole vectors of 4, also for odd d_out
+// (columns past it hold anything).
+__host__ __device__ __forceinline__ int f32_pitch(int d_out) { return (d_out + 3) & ~3; }
+
 struct CombineArgs {
-  const float* part;            // [n_pos, d_out]
+  const float* part;            // [n_pos, f32_pitch(d_out)]
   const int32_t* position;      // [T, k]
   const float* weight;          // [T, k]
   const void* residual;         // [T, d_out] or null

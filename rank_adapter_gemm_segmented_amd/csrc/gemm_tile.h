@@ -458,9 +458,10 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
           if (p >= p_end || col >= d_y) continue;
           const long long at = (long long)row_of(p) * d_y + col;
           float r8[8], o[8];
+          const bool whole = PLAIN || col + 8 <= d_y;
           if constexpr (!PLAIN) {
-            if (res && vec) {   // uniform (col + 8 <= d_y then)
-              const u32x4_t r = *(const u32x4_t*)(res + at);
+            if (res && whole) {
+              const u32x4_t r = *(const u32x4_any*)(res + at);
 #pragma unroll
               for (int e = 0; e < 8; ++e) r8[e] = __uint_as_float((e & 1) ? (r[e / 2] & 0xffff0000u) : (r[e / 2] << 16));
             } else {
@@ -489,8 +490,8 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
               if (res) o[e] += r8[e];
             }
           }
-          if (PLAIN || vec) {
-            *(u32x4_t*)(y + at) = u32x4_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]), cvt_pk_bf16(o[6], o[7])};
+          if (whole) {
+            *(u32x4_any*)(y + at) = u32x4_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]), cvt_pk_bf16(o[6], o[7])};
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -505,15 +506,15 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
 }
 
 // Store of a wave's accumulators in fp32, rows v0 .. v0 + WR - 1 by positions
-// p0 .. p0 + WT - 1 below p_end, position p to row p of y, bias added.
+// p0 .. p0 + WT - 1 below p_end, position p to row p of y (pitch: d_out rounded up
+// to a multiple of 4, so that every store is whole), bias added.
 template <class C>
 __device__ __forceinline__ void store_f32(f32x16_t (&acc)[C::MR][C::MT], char* lds, int wave, int lane, int v0, int p0,
-                                          int p_end, int d_out, const uint16_t* bias, const float* w_scale, float* y) {
+                                          int p_end, int d_out, const uint16_t* bias, const float* w_scale, float* y, int pitch) {
   constexpr int MC = C::EPI_MC;   // row blocks per pass through the LDS tile, as store_epilogue
   constexpr int PITCH = MC * 128 + 16, CPR = MC * 8, PPP = kWave / CPR;
   const int l32 = lane % 32, h = lane / 32, c = lane % CPR;
   char* tile = lds + wave * 32 * PITCH;
-  const bool vec = d_out % 4 == 0;
 #pragma unroll
   for (int m0 = 0; m0 < C::MR; m0 += MC) {
     const int col = v0 + m0 * 32 + 4 * c;
@@ -538,12 +539,7 @@ __device__ __forceinline__ void store_f32(f32x16_t (&acc)[C::MR][C::MT], char* l
         f32x4_t z = *(const f32x4_t*)(tile + tl * PITCH + 16 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = C::kW8 ? fmaf(z[i], sc[i], b[i]) : z[i] + b[i];
-        float* dst = y + (long long)p * d_out + col;
-        if (vec) *(f32x4_t*)dst = z;
-        else
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (col + i < d_out) dst[i] = z[i];
+        *(f32x4_t*)(y + (long long)p * pitch + col) = z;
       }
     }
   }

@@ -649,11 +649,11 @@ __global__ __launch_bounds__(256) void k_finish_bf16(DecodeArgs a) {
     const long long at = (long long)row * d_y + f;
     uint16_t* y = (uint16_t*)a.y;
     const uint16_t* res = (const uint16_t*)a.epi.residual;
-    const bool vec = f + 3 < d_y && (d_y & 3) == 0;
+    const bool vec = f + 4 <= d_y;
     float r4[4] = {0.f, 0.f, 0.f, 0.f};
     if (res) {
       if (vec) {
-        const u32x2_t r = *(const u32x2_t*)(res + at);
+        const u32x2_t r = *(const u32x2_any*)(res + at);
 #pragma unroll
         for (int v = 0; v < 4; ++v) r4[v] = __uint_as_float((v & 1) ? (r[v / 2] & 0xffff0000u) : (r[v / 2] << 16));
       } else {
@@ -667,7 +667,7 @@ __global__ __launch_bounds__(256) void k_finish_bf16(DecodeArgs a) {
       if (res) o[v] += r4[v];
     }
     if (vec) {
-      *(u32x2_t*)(y + at) = u32x2_t{(uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16),
+      *(u32x2_any*)(y + at) = u32x2_t{(uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16),
                                     (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16)};
     } else {
 #pragma unroll

@@ -106,20 +106,19 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) o[v] *= u[v];
     }
-    const long long at = (long long)p * d_y + f;
-    const bool vec = d_y % 4 == 0;
+    const bool whole = f + 4 <= d_y;
     if (TYPE == kXF32 || a.f32_out) {
-      float* y = (float*)a.y + at;
-      if (vec) *(f32x4_t*)y = f32x4_t{o[0], o[1], o[2], o[3]};
+      float* y = (float*)a.y + (long long)p * (a.f32_out ? f32_pitch(d_y) : d_y) + f;
+      if (whole || a.f32_out) *(f32x4_any*)y = f32x4_t{o[0], o[1], o[2], o[3]};
       else
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           if (f + v < d_y) y[v] = o[v];
     } else {
-      uint16_t* y = (uint16_t*)a.y + at;
-      if (vec)
-        *(u32x2_t*)y = u32x2_t{(uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16),
-                               (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16)};
+      uint16_t* y = (uint16_t*)a.y + (long long)p * d_y + f;
+      if (whole)
+        *(u32x2_any*)y = u32x2_t{(uint32_t)f32_to_bf16_bits(o[0]) | ((uint32_t)f32_to_bf16_bits(o[1]) << 16),
+                                 (uint32_t)f32_to_bf16_bits(o[2]) | ((uint32_t)f32_to_bf16_bits(o[3]) << 16)};
       else
 #pragma unroll
         for (int v = 0; v < 4; ++v)
@@ -222,7 +221,7 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0,
   if (epi.bias) epi.bias = (const uint16_t*)epi.bias + (long long)e * d_out;
   const float* ws = C::kW8 ? a.w_scale + (long long)e * d_out : nullptr;
   if constexpr (OUT == 2) {
-    store_f32<C>(acc, lds, wave, lane, v0, pw, p1, d_out, (const uint16_t*)epi.bias, ws, (float*)a.y);
+    store_f32<C>(acc, lds, wave, lane, v0, pw, p1, d_out, (const uint16_t*)epi.bias, ws, (float*)a.y, f32_pitch(d_out));
   } else {
     store_epilogue<C, GATED>(acc, lds, wave, lane, v0, pw, p1, d_out, epi, ws, a.y, [](int p) { return p; });
   }
@@ -291,31 +290,48 @@ template <typename E_>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
   const int t = blockIdx.x, c = 4 * (blockIdx.y * 256 + threadIdx.x);
   if (c >= a.d_out) return;
-  const bool vec = a.d_out % 4 == 0;
+  const bool whole = c + 4 <= a.d_out;
   float o[4] = {0.f, 0.f, 0.f, 0.f};
   const long long at = (long long)t * a.d_out + c;
+  const int pitch = f32_pitch(a.d_out);
   for (int j = 0; j < a.k; ++j) {
     const int p = a.position[(long long)t * a.k + j];
     const float w = a.weight[(long long)t * a.k + j];
     if (p < 0 || p >= a.n_pos) continue;   // uniform: no expert in this slot
-    const float* z = a.part + (long long)p * a.d_out + c;
-    if (vec) {
-      const f32x4_t v = *(const f32x4_t*)z;
+    const f32x4_t v = *(const f32x4_t*)(a.part + (long long)p * pitch + c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(w, v[i], o[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i < a.d_out) o[i] = fmaf(w, z[i], o[i]);
-    }
+    for (int i = 0; i < 4; ++i) o[i] = fmaf(w, v[i], o[i]);
   }
+  float r[4] = {0.f, 0.f, 0.f, 0.f};
+  if (a.residual) {
+    if (!whole) {
+      #pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < a.d_out) r[i] = elem_f32<E_>(a.residual, at + i);
+    } else if constexpr (sizeof(E_) == 2) {
+      const u32x2_t v = *(const u32x2_any*)((const uint16_t*)a.residual + at);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (c + i < a.d_out) {
-      if (a.residual) o[i] += elem_f32<E_>(a.residual, at + i);
-      if constexpr (sizeof(E_) == 2) ((uint16_t*)a.out)[at + i] = f32_to_bf16_bits(o[i]);
-      else ((float*)a.out)[at + i] = o[i];
+      for (int i = 0; i < 4; ++i) r[i] = __uint_as_float((i & 1) ? (v[i / 2] & 0xffff0000u) : (v[i / 2] << 16));
+    } else {
+      const f32x4_t v = *(const f32x4_any*)((const float*)a.residual + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = v[i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] += r[i];
+  }
+  if (whole) {
+    if constexpr (sizeof(E_) == 2)
+      *(u32x2_any*)((uint16_t*)a.out + at) = u32x2_t{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3])};
+    else *(f32x4_any*)((float*)a.out + at) = f32x4_t{o[0], o[1], o[2], o[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < a.d_out) {
+        if constexpr (sizeof(E_) == 2) ((uint16_t*)a.out)[at + i] = f32_to_bf16_bits(o[i]);
+        else ((float*)a.out)[at + i] = o[i];
+      }
+  }
 }
 
 // ---------------------------------------------------------------------------
