@@ -353,19 +353,30 @@ static void launch_stream_n(const ExpertsArgs& a, hipStream_t st) {
 
 // Shape of the streaming form. Few items (a token or two): 32 rows and 8 waves
 // each, so that the card is full (one token, two of eight experts of 4096 -> 2
-// x 14336: 79.5 us against 85.6 with 64 rows and 4 waves). Otherwise 64 rows
-// and 4 waves (64 tokens, 64 FP8 experts: 113 us against 134). Positions per
-// item by the mean per expert, with room for uneven ones; FP8 keeps to 16
-// longer, its x operands taking twice the registers per byte of W.
+// x 14336: 79.5 us against 85.6 with 64 rows and 4 waves); so too with more
+// positions where the items are fewer than the CUs (75 tokens, four of eight
+// experts, 4864 -> 2 x 305: 27.2 us against 36.3; 102 tokens of five experts, 4720
+// -> 335: 17.1 against 26.0; with 256 items, 24 tokens of eight experts, 4096 ->
+// 2048, 29.9 against 27.5). Otherwise 64 rows and 4 waves (64 tokens, 64 FP8
+// experts: 113 us against 134). Positions per item by the mean per expert, with
+// room for uneven ones; FP8 keeps to 16 longer, its x operands taking twice the
+// registers per byte of W.
 template <int TYPE>
 static void launch_stream(const ExpertsArgs& a, hipStream_t st) {
   const long long active = std::min(a.E, a.n_pos);
-  const long long items = (long long)((a.gated ? gated_rows(a.d_out) : a.d_out) + 63) / 64 * active;
+  const long long row_tiles = ((a.gated ? gated_rows(a.d_out) : a.d_out) + 63) / 64;
   const double mean = (double)a.n_pos / active;
-  if (items < 2048 && mean <= 4) launch_stream_n<TYPE, 2, 1, 8>(a, st);
-  else if (mean <= (TYPE == kXFp8w ? 10 : 4)) launch_stream_n<TYPE, 4, 1, 4>(a, st);
-  else if (mean <= 24) launch_stream_n<TYPE, 4, 2, 4>(a, st);
-  else launch_stream_n<TYPE, 4, 4, 4>(a, st);
+  const int nt = mean <= (TYPE == kXFp8w ? 10 : 4) ? 1 : mean <= 24 ? 2 : 4;   // blocks of 16 positions
+  const long long items = row_tiles * std::max(active, a.n_pos / (16 * nt) + active / 2);
+  if (items < 256 || (row_tiles * active < 2048 && mean <= 4)) {
+    if (nt == 1) launch_stream_n<TYPE, 2, 1, 8>(a, st);
+    else if (nt == 2) launch_stream_n<TYPE, 2, 2, 8>(a, st);
+    else launch_stream_n<TYPE, 2, 4, 8>(a, st);
+  } else {
+    if (nt == 1) launch_stream_n<TYPE, 4, 1, 4>(a, st);
+    else if (nt == 2) launch_stream_n<TYPE, 4, 2, 4>(a, st);
+    else launch_stream_n<TYPE, 4, 4, 4>(a, st);
+  }
 }
 
 template <class C>
