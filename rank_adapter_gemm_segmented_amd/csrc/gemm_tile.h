@@ -45,6 +45,8 @@ __device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32
                : "memory", "m0");
 }
 
+// Wait until at most N of this wave's vector memory operations are in flight,
+// then a workgroup barrier (LDS and scalar counters drained too; nothing else).
 template <int N>
 __device__ __forceinline__ void vm_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");

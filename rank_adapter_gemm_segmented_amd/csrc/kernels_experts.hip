@@ -283,7 +283,7 @@ void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
 //
 // The products stay in fp32 between the two kernels: with bf16 rows a token's sum
 // would carry top_k more roundings. A prefill batch (8192 rows of 4096) moves 200
-// MB here, 47 us at 4.3 TB/s, of 886 in all; a decode batch 7 us, mostly the
+// MB here, 47 us at 4.3 TB/s, of about 900 in all; a decode batch 7 us, mostly the
 // launch.
 // ---------------------------------------------------------------------------
 template <typename E_>
@@ -410,9 +410,10 @@ typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
 // Form by the rows per expert. Up to two (FP8: twenty), the streaming form; it
 // also takes fp32 and what has too few tiles for the card: fewer than 256 of 32
 // positions (24 tokens, two of eight experts, 4096 -> 2048, 128 tiles: 27.6 us
-// streamed, 33.8 tiled), fewer than 64 of more (100 tokens, 4096 -> 1024, 64 tiles:
-// 30.1 streamed, 24.0 tiled; FP8, 100 tokens over 4 experts, 32 tiles: 16.1 and
-// 20.5). Then tiles of 32, 64,
+// streamed, 33.8 tiled), fewer than 64 of more (FP8,
+// 100 tokens over 4 experts, 32 tiles: 12.8 us streamed, 20.7 tiled; two of eight
+// experts, 100 tokens, 4096 -> 1024, 64 tiles: 22.4 and 24.1; 400 tokens, 4096 -> 2 x
+// 512, 80 tiles: 43.1 and 35.1). Then tiles of 32, 64,
 // 128 and 256 positions, the smallest that holds most experts' rows: W, which
 // decides the time up to about 100 rows, is then read once, and the tile's
 // rings keep more of it requested than registers can. Two of eight experts,
