@@ -45,7 +45,9 @@ __device__ __forceinline__ int wrow_of(int v, int d_out) {
 // Activations. FAST (bf16 outputs): the hardware exponential and reciprocal,
 // about 2^-22 relative, far below bf16's half step; fp32 outputs take the
 // library's exponential and a full division. tanh(u) is written through the
-// exponential: (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)). NaN passes through.
+// exponential: (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)), and 1 + erf(a) as erfc(-a):
+// the sums cancel where z is far below 0 (1 + erf was 4% off at z = -5 and 0 from
+// -5.6 on, in fp32). NaN passes through.
 template <bool FAST>
 __device__ __forceinline__ float sigmoid_times(float z, float t) {   // z / (1 + exp(-t))
   if constexpr (FAST) {
@@ -54,12 +56,34 @@ __device__ __forceinline__ float sigmoid_times(float z, float t) {   // z / (1 +
     return z / (1.0f + expf(-t));
   }
 }
+// gelu, z Phi(z) with Phi the normal distribution. FAST: Phi(-x) = exp(-x^2 / 2) R(x)
+// for x = |z|, and R, which falls smoothly from 1/2 towards 1 / (x sqrt(2 pi)), as
+// t P(t) with t = 1 / (1 + 0.265 x): a least-maximum fit of P, within 6.5e-7 of R
+// everywhere (about 11 roundings of fp32; the library's erfcf in its place: 975 ->
+// 1767 us, 4096 tokens, 4096 -> 2 x 14336 gated).
+template <bool FAST>
+__device__ __forceinline__ float gelu(float z) {
+  if constexpr (FAST) {
+    const float x = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(0.265f, x, 1.0f));
+    float p = -0.0677952636f;
+    p = fmaf(p, t, 0.195301499f);
+    p = fmaf(p, t, -0.066401835f);
+    p = fmaf(p, t, 0.142520221f);
+    p = fmaf(p, t, 0.0829368182f);
+    p = fmaf(p, t, 0.107838527f);
+    p = fmaf(p, t, 0.105599717f);
+    const float q = p * t * __builtin_amdgcn_exp2f(-0.72134752f * x * x);   // (log2(e) / 2)
+    return z * (z < 0.f ? q : 1.0f - q);
+  } else {
+    return 0.5f * z * erfcf(z * -0.70710678118654752f);
+  }
+}
 template <bool FAST>
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {   // uniform
     case MLORA_ACT_RELU: return z < 0.f ? 0.f : z;
     case MLORA_ACT_SILU: return sigmoid_times<FAST>(z, z);
-    case MLORA_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case MLORA_ACT_GELU: return gelu<FAST>(z);
     case MLORA_ACT_GELU_TANH: return sigmoid_times<FAST>(z, 1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
     default: return z;
   }
