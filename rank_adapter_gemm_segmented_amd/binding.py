@@ -213,6 +213,21 @@ def _check_xw(x, W, pool: Pool):
         raise ValueError("x and W must be contiguous")
 
 
+def _segments(T: int, lora_on, seg_start, seg_adapter, seg_rank, seg_scale, token_index) -> int:
+    """The number of segments, which seg_adapter gives; a call with adapters needs the other
+    arrays as long (the kernels bound what they hold, and cannot bound how much)."""
+    if seg_adapter is None:
+        return 0
+    n = seg_adapter.numel()
+    if lora_on:
+        if ((seg_start is not None and seg_start.numel() <= n) or (seg_rank is not None and seg_rank.numel() < n)
+                or (seg_scale is not None and seg_scale.numel() < n)):
+            raise ValueError("seg_start must be [n_seg + 1], seg_rank and seg_scale [n_seg], with n_seg that of seg_adapter")
+        if token_index is not None and token_index.numel() < T:
+            raise ValueError("token_index must be [T]")
+    return n
+
+
 def linear(x, W, pool: Pool, seg_start=None, seg_adapter=None, seg_rank=None, seg_scale=None,
            lora_on: int = 1, token_index=None, out=None, workspace=None):
     """``mlora_linear``: y = W x + per-segment adapter term (sorted metadata)."""
@@ -418,13 +433,14 @@ def linear_epilogue(x, W, pool: Pool, seg_start=None, seg_adapter=None, seg_rank
     if seg_scale is not None and seg_scale.dtype is not _f32t:
         raise TypeError("seg_scale must be float32")
     T = x.shape[0]
+    n_seg = _segments(T, lora_on, seg_start, seg_adapter, seg_rank, seg_scale, token_index)
     code = _act_code(act, gated)
     y = _epilogue_out(x, T, d_out, gated, bias, (d_out,), residual, out)
     ws = workspace if workspace is not None else pool.workspace(T)
     epi = _Epilogue(_at(bias, dev, what), _at(residual, dev, what), code)
     rest = (pool.handle, _at_i32(seg_start, dev, what), _at_i32(seg_adapter, dev, what), _at_i32(seg_rank, dev, what),
             _at(seg_scale, dev, what), _at_i32(token_index, dev, what), T,
-            seg_adapter.numel() if seg_adapter is not None else 0, lora_on, ctypes.byref(epi), _at(y, dev, what),
+            n_seg, lora_on, ctypes.byref(epi), _at(y, dev, what),
             _at(ws, dev, what), ws.numel(), _raw_stream(dev))
     if w_scale is None:
         code = _lib.mlora_linear_epilogue(_at(x, dev, what), _at(W, dev, what), *rest)
