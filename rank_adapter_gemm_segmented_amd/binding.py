@@ -235,7 +235,7 @@ def linear(x, W, pool: Pool, seg_start=None, seg_adapter=None, seg_rank=None, se
     T = int(x.shape[0])
     y = out if out is not None else torch.empty((T, pool.d_out), dtype=pool.dtype, device=x.device)
     ws = workspace if workspace is not None else pool.workspace(T)
-    n_seg = int(seg_adapter.numel()) if seg_adapter is not None else 0
+    n_seg = _segments(T, lora_on, seg_start, seg_adapter, seg_rank, seg_scale, token_index)
     if seg_scale is not None and (seg_scale.dtype != torch.float32 or not seg_scale.is_contiguous()):
         raise TypeError("seg_scale must be contiguous float32")
     _check(_lib.mlora_linear(_ptr(x), _ptr(W), pool.handle, _ptr(_i32(seg_start, "seg_start")),
@@ -254,7 +254,7 @@ def linear_noalloc(x, W, pool: Pool, seg_start=None, seg_adapter=None, seg_rank=
     _check_xw(x, W, pool)
     T = int(x.shape[0])
     y = out if out is not None else torch.empty((T, pool.d_out), dtype=pool.dtype, device=x.device)
-    n_seg = int(seg_adapter.numel()) if seg_adapter is not None else 0
+    n_seg = _segments(T, lora_on, seg_start, seg_adapter, seg_rank, seg_scale, token_index)
     if seg_scale is not None and (seg_scale.dtype != torch.float32 or not seg_scale.is_contiguous()):
         raise TypeError("seg_scale must be contiguous float32")
     _check(_lib.mlora_linear_noalloc(_ptr(x), _ptr(W), pool.handle, _ptr(_i32(seg_start, "seg_start")),
@@ -279,7 +279,7 @@ def linear_fp8w(x, W_fp8, w_scale, pool: Pool, seg_start=None, seg_adapter=None,
     T = int(x.shape[0])
     y = out if out is not None else torch.empty((T, pool.d_out), dtype=pool.dtype, device=x.device)
     ws = workspace if workspace is not None else pool.workspace(T)
-    n_seg = int(seg_adapter.numel()) if seg_adapter is not None else 0
+    n_seg = _segments(T, lora_on, seg_start, seg_adapter, seg_rank, seg_scale, token_index)
     _check(_lib.mlora_linear_fp8w(_ptr(x), _ptr(W_fp8), _ptr(w_scale), pool.handle,
                                   _ptr(_i32(seg_start, "seg_start")), _ptr(_i32(seg_adapter, "seg_adapter")),
                                   _ptr(_i32(seg_rank, "seg_rank")), _ptr(seg_scale),
@@ -293,6 +293,8 @@ def linear_tokens(x, W, pool: Pool, token_adapter, adapter_scale, lora_on: int =
     """``mlora_linear_tokens``: the layer on an unsorted batch (library segments it)."""
     _check_xw(x, W, pool)
     T = int(x.shape[0])
+    if lora_on and token_adapter is not None and token_adapter.numel() < T:
+        raise ValueError("token_adapter must be [T]")
     y = out if out is not None else torch.empty((T, pool.d_out), dtype=pool.dtype, device=x.device)
     ws = workspace if workspace is not None else pool.workspace(T)
     _check(_lib.mlora_linear_tokens(_ptr(x), _ptr(W), pool.handle,

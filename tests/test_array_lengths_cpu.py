@@ -55,3 +55,42 @@ def test_epilogue_does_not_read_them_with_the_adapters_off(ml):
     with pytest.raises(ml.MloraError) as e:
         _epilogue(ml, lora_on=0, seg_start=0, token_index=0)
     assert e.value.code == ml.STATUS_CODE["MLORA_ERR_INVALID_ARG"]
+
+
+# ---- the plain layer and its helpers: on host tensors an accepted call ends at the check for device tensors
+
+def _plain(ml, name, lora_on=1, out=None, **short):
+    m, pool = _meta(**short), _pool(ml)
+    x, W = torch.zeros((T, D_IN), dtype=torch.bfloat16), torch.zeros((D_OUT, D_IN), dtype=torch.bfloat16)
+    ws = {} if name == "linear_noalloc" else {"workspace": torch.empty(256, dtype=torch.uint8)}
+    if name == "linear_fp8w":
+        return ml.linear_fp8w(x, W.to(torch.uint8), torch.ones(D_OUT), pool, lora_on=lora_on, out=out, **ws, **m)
+    return getattr(ml, name)(x, W, pool, lora_on=lora_on, out=out, **ws, **m)
+
+
+PLAIN = ["linear", "linear_noalloc", "linear_fp8w"]
+
+
+@pytest.mark.parametrize("call", PLAIN)
+@pytest.mark.parametrize("name,n", [("seg_start", N), ("seg_rank", N - 1), ("seg_scale", N - 1), ("token_index", T - 1),
+                                    ("seg_adapter", N + 1)])
+def test_layer_refuses_short_arrays(ml, call, name, n):
+    with pytest.raises(ValueError, match="n_seg" if name != "token_index" else "token_index"):
+        _plain(ml, call, **{name: n})
+
+
+@pytest.mark.parametrize("call", PLAIN)
+@pytest.mark.parametrize("longer", [{}, {"seg_start": N + 5}, {"token_index": T + 3}, {"lora_on": 0, "seg_rank": 0}])
+def test_layer_takes_arrays_that_hold_the_batch(ml, call, longer):
+    with pytest.raises(TypeError, match="device tensor"):
+        _plain(ml, call, **longer)
+
+
+@pytest.mark.parametrize("n", [T - 1, 0])
+def test_unsorted_layer_refuses_short_arrays(ml, n):
+    x, W = torch.zeros((T, D_IN), dtype=torch.bfloat16), torch.zeros((D_OUT, D_IN), dtype=torch.bfloat16)
+    ids, scale, ws = torch.zeros(T, dtype=torch.int32), torch.ones(4), torch.empty(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="token_adapter"):
+        ml.linear_tokens(x, W, _pool(ml), ids[:n], scale, workspace=ws)
+    with pytest.raises(TypeError, match="device tensor"):
+        ml.linear_tokens(x, W, _pool(ml), ids, scale, workspace=ws)
