@@ -136,8 +136,8 @@ PoolView view_of(const mlora_pool_s* p) {
 
 int hip_status(hipError_t e) { return e == hipSuccess ? MLORA_OK : MLORA_ERR_HIP; }
 
-// MLORA_FORCE_PATH=decode|gemm overrides the bf16 path choice (for tests and
-// measurements); unset or anything else chooses by token count.
+// MLORA_FORCE_PATH=decode|gemm|gemv overrides the bf16 path choice (for tests
+// and measurements); unset or anything else chooses by token count.
 int forced_path() {
   const char* e = getenv("MLORA_FORCE_PATH");
   if (!e) return 0;
@@ -246,7 +246,8 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
   a.epi_kind = epi_kind_of(epi);
   a.epi = epi_view_of(epi);
   if (pool->dtype == MLORA_BF16) {
-    const int fp = forced_path();
+    // (the GEMV has no form with an epilogue: such a call is not forced)
+    const int fp = a.epi_kind != kEpiNone && forced_path() == 3 ? 0 : forced_path();
     // The split-K decode path up to 64 tokens, except on wide layers from 48
     // tokens up; the tiled GEMM otherwise. Measured per path, token count and
     // pass with HBM counters in profiles/path_sweep.txt: on 4096 -> 4096 the
@@ -290,7 +291,7 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
     one.ks = 1;
     const bool one_chunk = lora_on && ((T <= 16 * a.seg_grid && pool->max_rank <= 16) || shrink_short(one));
     a.ks = one_chunk ? 1 : choose_shrink_split_bf16(pool->d_in, shrink_items_bound(T, a.seg_grid, pool->max_rank));
-    if (fp == 3 && T <= 64 && a.epi_kind == kEpiNone) {
+    if (fp == 3 && T <= 64) {
       if (log_calls())
         log_call("gemv", T, pool, sv, lora_on, a.ks, !lora_on || a.seg_grid <= 0 ? "none" : shrink_short(a) ? "short" : "mfma");
       launch_shrink_bf16(a, stream);
