@@ -24,3 +24,11 @@ def test_adapter_term_in_64x256_tiles(form, gated, monkeypatch):
     log(f"[epilogue] 257 tokens, 264 -> 6400, adapter term {form}, gated={gated}")
     monkeypatch.setenv("MLORA_EXPAND", form)
     Layer(torch.bfloat16, 257, 264, 6400, gated, seed=2, shuffled=True).check("silu")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,fp8,d_out", [(20, False, 192), (5, True, 192), (20, True, 192), (64, True, 192), (3, False, 16448), (3, True, 16448)])
+def test_fused_pools_of_a_few_tokens(T, fp8, d_out, gated):
+    log(f"[epilogue] fused pool, {T} tokens, 264 -> {d_out}, fp8={fp8} gated={gated}")
+    layer = Layer(torch.bfloat16, T, 272, d_out, gated, seed=3, ranks=(16, 16), fused=True, fp8=fp8, max_run=3)
+    layer.check("silu")
