@@ -487,7 +487,8 @@ def route_workspace(n_tokens: int, n_experts: int, top_k: int, device="cuda") ->
 def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None):
     """``mlora_route``: top-k expert choice of logits [T, E] and its segments.
     Returns (expert [T, k], weight [T, k], token_index [T k], seg_start [E + 1],
-    position [T, k]); ``out`` is such a tuple to write into."""
+    position [T, k]), views of one allocation, which any of them keeps; ``out`` is such a tuple
+    to write into."""
     what, dev = "route", _device()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
@@ -507,9 +508,9 @@ def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None
         p0 = buf.data_ptr()
         ptrs = (p0, p0 + 4 * at, p0 + 8 * at, p0 + 16 * at, p0 + 12 * at)
     else:
-        for t, n, dt in zip(out, (P, P, P, E + 1, P), (_i32t, _f32t, _i32t, _i32t, _i32t)):
-            if t.dtype is not dt or t.numel() != n:
-                raise ValueError("out must be (expert, weight, token_index, seg_start, position) of this batch")
+        want = ((P, _i32t), (P, _f32t), (P, _i32t), (E + 1, _i32t), (P, _i32t))
+        if len(out) != len(want) or any(t.numel() != n or t.dtype is not dt for t, (n, dt) in zip(out, want)):
+            raise ValueError("out must be (expert, weight, token_index, seg_start, position) of this batch")
         ptrs = [_at(t, dev, what) for t in out]
     code = _lib.mlora_route(at_logits, code, T, E, top_k, 1 if renormalize else 0, *ptrs, _at(ws, dev, what), ws.numel(),
                             _raw_stream(dev))

@@ -94,3 +94,12 @@ def test_unsorted_layer_refuses_short_arrays(ml, n):
         ml.linear_tokens(x, W, _pool(ml), ids[:n], scale, workspace=ws)
     with pytest.raises(TypeError, match="device tensor"):
         ml.linear_tokens(x, W, _pool(ml), ids, scale, workspace=ws)
+
+
+@pytest.mark.parametrize("n", [0, 4, 6])
+def test_route_refuses_another_number_of_outputs(ml, n):
+    P, E = T * 2, 8
+    out = [torch.zeros(P, dtype=torch.int32), torch.zeros(P), torch.zeros(P, dtype=torch.int32),
+           torch.zeros(E + 1, dtype=torch.int32), torch.zeros(P, dtype=torch.int32), torch.zeros(P, dtype=torch.int32)]
+    with pytest.raises(ValueError, match="out must be"):
+        ml.route(torch.zeros((T, E)), 2, out=tuple(out[:n]), workspace=torch.empty(4096, dtype=torch.uint8))
