@@ -339,7 +339,8 @@ int mlora_validate(mlora_pool_t pool, const int32_t* seg_start, const int32_t* s
  *
  * n_experts in 1 .. MLORA_MAX_EXPERTS, top_k in 1 .. MLORA_MAX_TOP_K and at
  * most n_experts, n_tokens at most MLORA_MAX_TOKENS, at most
- * MLORA_MAX_POSITIONS slots, and slots times d_out at most MLORA_MAX_PRODUCT.
+ * MLORA_MAX_POSITIONS slots (and rows of x), and slots times d_out at most
+ * MLORA_MAX_PRODUCT. MLORA_LOG says nothing of these calls.
  * ---------------------------------------------------------------------- */
 #define MLORA_MAX_EXPERTS 1024
 #define MLORA_MAX_TOP_K 64

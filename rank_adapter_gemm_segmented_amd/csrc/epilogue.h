@@ -42,8 +42,11 @@ __device__ __forceinline__ int wrow_of(int v, int d_out) {
   return GATED ? gated_wrow(v, d_out) : min(v, d_out - 1);
 }
 
-// Activations. FAST (bf16 outputs): the hardware exponential and reciprocal,
-// about 2^-22 relative, far below bf16's half step; fp32 outputs take the
+// Activations. FAST (bf16 outputs): the hardware exponential and reciprocal. The
+// exponential's argument is rounded once as it is scaled by log2(e), so the result
+// is off by about (|t| + 4) 2^-24 relative, t the argument: below 2^-17 up to 88
+// (bf16's half step is 2^-8). Past t = -88 (and where the reciprocal's result
+// would be subnormal) it is 0 in place of less than 1e-35. fp32 outputs take the
 // library's exponential and a full division. tanh(u) is written through the
 // exponential: (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)), and 1 + erf(a) as erfc(-a):
 // the sums cancel where z is far below 0 (1 + erf was 4% off at z = -5 and 0 from

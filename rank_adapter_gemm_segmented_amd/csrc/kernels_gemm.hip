@@ -867,7 +867,9 @@ void k_gemm2(LinearArgs a) {
   // (With an epilogue every tile adds it here.)
   constexpr bool kDeltaTile = EPI == kEpiNone && C::NW * WT * (4 * WR + 16) <= C::LDS_BYTES;
   constexpr bool kDeltaEarly = !kDeltaTile && C::MR * C::MT <= 4;
-  // (no dense term with as many tiles as the 4-wave form has: kDxMaxBytes is 64 of them)
+  // (no dense term with as many tiles as the 4-wave form has, at least 192: its
+  // kDxMaxBytes are 64 whole tiles, at most 128 with position tiles of one token,
+  // as at 129 or 257 tokens)
   const bool use_delta = !PIPE && a.lora_on && a.delta != nullptr;
   auto delta_ptr = [&](int n, int m, int q) {
     const int p = min(t0 + wt * WT + n * 32 + l32, T - 1);
