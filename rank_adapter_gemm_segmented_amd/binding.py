@@ -219,7 +219,7 @@ def _segments(T: int, lora_on, seg_start, seg_adapter, seg_rank, seg_scale, toke
     if seg_adapter is None:
         return 0
     n = seg_adapter.numel()
-    if lora_on:
+    if lora_on and T and n:   # (else none is read)
         if ((seg_start is not None and seg_start.numel() <= n) or (seg_rank is not None and seg_rank.numel() < n)
                 or (seg_scale is not None and seg_scale.numel() < n)):
             raise ValueError("seg_start must be [n_seg + 1], seg_rank and seg_scale [n_seg], with n_seg that of seg_adapter")

@@ -103,3 +103,14 @@ def test_route_refuses_another_number_of_outputs(ml, n):
            torch.zeros(E + 1, dtype=torch.int32), torch.zeros(P, dtype=torch.int32), torch.zeros(P, dtype=torch.int32)]
     with pytest.raises(ValueError, match="out must be"):
         ml.route(torch.zeros((T, E)), 2, out=tuple(out[:n]), workspace=torch.empty(4096, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("call", PLAIN + ["linear_epilogue"])
+def test_no_tokens_need_no_arrays(ml, call):
+    none = {k: v[:0] for k, v in _meta().items()}
+    x, W, ws = torch.zeros((0, D_IN), dtype=torch.bfloat16), torch.zeros((D_OUT, D_IN), dtype=torch.bfloat16), {}
+    if call != "linear_noalloc":
+        ws = {"workspace": torch.empty(256, dtype=torch.uint8)}
+    args = (W.to(torch.uint8), torch.ones(D_OUT)) if call == "linear_fp8w" else (W,)
+    with pytest.raises(ml.MloraError if call == "linear_epilogue" else TypeError):   # as with any batch here: no pool, no device
+        getattr(ml, call)(x, *args, _pool(ml), **ws, **none)
