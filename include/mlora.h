@@ -286,6 +286,60 @@ int mlora_linear_fp8w_epilogue(const void* x, const uint8_t* W_fp8, const float*
                                int lora_on, const mlora_epilogue_t* epilogue, void* y, void* workspace,
                                size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4)
+ *
+ * A row of d columns, a multiple of 32, is cut into blocks of 32 columns. A
+ * block has 32 E2M1 codes (a sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6) and one scale byte s that stands for 2^(s - 127); s = 255
+ * makes the whole block NaN. (OCP Microscaling Formats, MXFP4.)
+ *
+ * codes [rows, d / 2]: column 2 i in the low half of byte i, 2 i + 1 in the high.
+ * scale [ceil(d / 128), rows, 4]: byte b % 4 of plane b / 4 is the scale of
+ * block b of a row, so the four scales of 128 columns are one dword, and
+ * consecutive rows of a plane are side by side. Bytes behind a row's last block
+ * may be read, are multiplied by zero, and must not be 255.
+ * Weights of several experts and batches of matrices put their index first.
+ * ---------------------------------------------------------------------- */
+
+/* Quantise x [n_batch, n_rows, d] (dtype) to codes [n_batch, n_rows, d / 2] and
+ * scale [n_batch, ceil(d / 128), n_rows, 4]. A block's scale is 2^e, e = floor(
+ * log2 m) - 2 for its largest magnitude m, at least -127; codes are x / 2^e
+ * rounded to nearest, ties to even, magnitudes past 6 to 6. A block that holds a
+ * NaN or an infinity gets scale 255 and codes 0. Scale bytes behind a row's
+ * last block are set to 127. n_batch 0 .. MLORA_MAX_EXPERTS, n_rows 0 ..
+ * MLORA_MAX_POSITIONS, d a multiple of 32 up to MLORA_MAX_DIM.
+ * Errors: MLORA_ERR_DTYPE, MLORA_ERR_SHAPE, MLORA_ERR_INVALID_ARG. */
+int mlora_quantize_mxfp4(const void* x, int dtype, int n_batch, int n_rows, int d, uint8_t* codes,
+                         uint8_t* scale, hipStream_t stream);
+
+/* The values that codes and scales stand for, y [n_batch, n_rows, d] in dtype:
+ * exact, but that bf16 has no values from 2^128 on (s past 252: infinities).
+ * Sizes and errors as mlora_quantize_mxfp4. */
+int mlora_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, int dtype, int n_batch, int n_rows,
+                           int d, void* y, hipStream_t stream);
+
+/* The layer with the base weight in MXFP4 and the adapters in bf16:
+ *
+ *     z_i = Q x_i + scale_s * B_a (A_a x_i),    then the epilogue
+ *
+ * Q the values of W (codes [d_out, d_in / 2]) and w_scale. x, y and the pool are
+ * bf16, d_in is a multiple of 32. A value of Q is exact in bf16 (s up to 252),
+ * products accumulate in fp32, y is rounded once. With x_codes [n_tokens, d_in /
+ * 2] and x_scale (both or neither; mlora_quantize_mxfp4 of x, or of what the base
+ * weight is to see) the base product multiplies these in place of x, on the
+ * 4-bit matrix units; the adapter term reads x all the same. Batches of any
+ * size. Other arguments, workspace, epilogue (NULL: none) and errors as
+ * mlora_linear_epilogue, plus MLORA_ERR_DTYPE (pool not bf16), MLORA_ERR_SHAPE
+ * (d_in not a multiple of 32) and MLORA_ERR_INVALID_ARG (x_codes without x_scale
+ * or the reverse). */
+int mlora_linear_mxfp4(const void* x, const uint8_t* x_codes, const uint8_t* x_scale, const uint8_t* W,
+                       const uint8_t* w_scale, mlora_pool_t pool, const int32_t* seg_start,
+                       const int32_t* seg_adapter, const int32_t* seg_rank, const float* seg_scale,
+                       const int32_t* token_index, int n_tokens, int n_seg, int lora_on,
+                       const mlora_epilogue_t* epilogue, void* y, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
 /* Canonical segmentation of an unsorted batch on the device: tokens grouped
  * by adapter id in ascending id order (-1 first), tokens of one id in
  * ascending batch order. Outputs (device):
@@ -372,6 +426,36 @@ int mlora_route(const void* logits, int dtype, int n_tokens, int n_experts, int 
                 int32_t* expert, float* weight, int32_t* token_index, int32_t* seg_start, int32_t* position,
                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* How mlora_route_scored ranks and weighs experts. */
+#define MLORA_SCORES_SOFTMAX 0   /* exp(l - m) / sum exp(l' - m) over all experts, m the largest logit */
+#define MLORA_SCORES_SIGMOID 1   /* 1 / (1 + exp(-l))                                                 */
+#define MLORA_MAX_GROUPS 64
+typedef struct {
+  int scores;         /* MLORA_SCORES_*                                                      */
+  const float* bias;  /* [n_experts] device, added to the scores for the choice only; or NULL */
+  int n_groups;       /* experts in n_groups equal ranges (1: no groups)                     */
+  int top_groups;     /* of which the choice sees the best top_groups                        */
+  float scale;        /* factor of every weight                                              */
+} mlora_scoring_t;
+
+/* mlora_route with the choice made by scores s_e of the logits: among the
+ * experts of the top_groups best groups, the top_k with the largest s_e + bias_e,
+ * equal ones in expert order. A group ranks by the sum of its two largest s_e +
+ * bias_e (by one where it has no second), equal ones in group order. The weight of
+ * a chosen expert is scale * s_e over the sum of the chosen ones' s (renormalize =
+ * 1; 0 where that sum is 0) or scale * s_e (0). Scores are rounded to fp32 from 64
+ * bits, each sum above once more; choices compare those. An expert whose logit is
+ * -inf or NaN, or whose s_e + bias_e is, is never chosen and counts in no group.
+ * bias may hold +-inf. Outputs, workspace, sizes and errors as mlora_route, plus
+ * MLORA_ERR_INVALID_ARG (no scoring, unknown scores, misaligned bias) and
+ * MLORA_ERR_SHAPE (n_groups outside 1 .. MLORA_MAX_GROUPS or no divisor of
+ * n_experts, top_groups outside 1 .. n_groups, top_k larger than the experts of
+ * top_groups groups). */
+int mlora_route_scored(const void* logits, int dtype, int n_tokens, int n_experts, int top_k, int renormalize,
+                       const mlora_scoring_t* scoring, int32_t* expert, float* weight, int32_t* token_index,
+                       int32_t* seg_start, int32_t* position, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
 /* y[p] = act(W_e x[token_index[p]] + bias_e) for the sorted positions p of
  * every expert e, gated as mlora_linear_epilogue. x [n_rows, d_in] in dtype;
  * W [n_experts, d_out, d_in] in dtype or, with w_scale [n_experts, d_out]
@@ -406,6 +490,22 @@ int mlora_experts_combine(const void* h, const void* W, const float* w_scale, in
                           const int32_t* position, const float* weight, const void* bias,
                           const void* residual, void* out, void* workspace, size_t workspace_bytes,
                           hipStream_t stream);
+
+/* mlora_experts_linear and mlora_experts_combine with W in MXFP4: codes
+ * [n_experts, d_out, d_in / 2], w_scale [n_experts, ceil(d_in / 128), d_out, 4].
+ * x and h are bf16, or, with x_scale [ceil(d_in / 128), n_rows, 4] (h_scale: of n_tokens
+ * top_k rows), MXFP4 codes [rows, d_in / 2] themselves. d_in is a multiple of
+ * 32; bias, residual, y and out are bf16. Else as theirs (workspace: that of
+ * bf16). */
+int mlora_experts_linear_mxfp4(const void* x, const uint8_t* x_scale, const uint8_t* W, const uint8_t* w_scale,
+                               int n_rows, int n_experts, int d_in, int d_out, const int32_t* seg_start,
+                               const int32_t* token_index, int n_pos, const mlora_epilogue_t* epilogue, void* y,
+                               hipStream_t stream);
+int mlora_experts_combine_mxfp4(const void* h, const uint8_t* h_scale, const uint8_t* W, const uint8_t* w_scale,
+                                int n_tokens, int top_k, int n_experts, int d_in, int d_out,
+                                const int32_t* seg_start, const int32_t* position, const float* weight,
+                                const void* bias, const void* residual, void* out, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Merged weights

@@ -29,11 +29,19 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 # activations of an epilogue, by name
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _GATED = 16
+# scores of a routing, by name
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class _Epilogue(ctypes.Structure):
     """``mlora_epilogue_t``"""
     _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("act", ctypes.c_int)]
+
+
+class _Scoring(ctypes.Structure):
+    """``mlora_scoring_t``"""
+    _fields_ = [("scores", ctypes.c_int), ("bias", ctypes.c_void_p), ("n_groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class MloraError(RuntimeError):
@@ -74,6 +82,12 @@ def _load() -> ctypes.CDLL:
         "mlora_linear_fp8w_epilogue": ([P, P, P, P, P, P, P, P, P, I, I, I, P, P, P, SZ, P], I),
         "mlora_route_workspace_bytes": ([I, I, I], SZ),
         "mlora_route": ([P, I, I, I, I, I, P, P, P, P, P, P, SZ, P], I),
+        "mlora_quantize_mxfp4": ([P, I, I, I, I, P, P, P], I),
+        "mlora_dequantize_mxfp4": ([P, P, I, I, I, I, P, P], I),
+        "mlora_linear_mxfp4": ([P] * 11 + [I, I, I, P, P, P, SZ, P], I),
+        "mlora_route_scored": ([P, I, I, I, I, I, P, P, P, P, P, P, P, SZ, P], I),
+        "mlora_experts_linear_mxfp4": ([P, P, P, P, I, I, I, I, P, P, I, P, P, P], I),
+        "mlora_experts_combine_mxfp4": ([P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P, SZ, P], I),
         "mlora_experts_linear": ([P, P, P, I, I, I, I, I, P, P, I, P, P, P], I),
         "mlora_experts_workspace_bytes": ([I, I, I, I, I], SZ),
         "mlora_experts_combine": ([P, P, P, I, I, I, I, I, I, P, P, P, P, P, P, P, SZ, P], I),
@@ -397,21 +411,21 @@ def _act_code(act: str, gated: bool) -> int:
     return code | _GATED if gated else code
 
 
-def _epilogue_out(x, rows: int, d_out: int, gated: bool, bias, bias_shape, residual, out):
-    """Checks an epilogue's tensors and returns y."""
+def _epilogue_out(x, rows: int, d_out: int, gated: bool, bias, bias_shape, residual, out, dt=None):
+    """Checks an epilogue's tensors and returns y (of x's type, or dt)."""
     if gated:
         if d_out % 2:
             raise ValueError("a gated product needs an even number of weight rows")
         d_out //= 2
-    shape, dt = (rows, d_out), x.dtype
+    shape, dt = (rows, d_out), dt or x.dtype
     if bias is not None and (bias.dtype is not dt or bias.shape != bias_shape):
-        raise ValueError(f"bias must be {list(bias_shape)} of x's dtype")
+        raise ValueError(f"bias must be {list(bias_shape)} of {dt}")
     if residual is not None and (residual.dtype is not dt or residual.shape != shape):
-        raise ValueError(f"residual must be {list(shape)} of x's dtype")
+        raise ValueError(f"residual must be {list(shape)} of {dt}")
     if out is None:
-        return x.new_empty(shape)
+        return x.new_empty(shape, dtype=dt)
     if out.dtype is not dt or out.shape != shape:
-        raise ValueError(f"out must be {list(shape)} of x's dtype")
+        raise ValueError(f"out must be {list(shape)} of {dt}")
     return out
 
 
@@ -474,6 +488,109 @@ def linear_tokens_epilogue(x, W, pool: Pool, token_adapter, adapter_scale, lora_
     return y
 
 
+# ---- microscaled 4-bit floating point ----------------------------------------------
+
+def _planes(d: int) -> int:
+    return (d + 127) // 128
+
+
+def mxfp4_scale_layout(scale):
+    """Row-major MXFP4 scales (uint8 [..., rows, d / 32]) in this library's layout,
+    [..., ceil(d / 128), rows, 4]; bytes behind a row's last block are 127."""
+    if scale.dtype is not _u8t or scale.dim() < 2:
+        raise ValueError("scale must be uint8 [..., rows, d / 32]")
+    *lead, rows, n = scale.shape
+    at = scale.new_full((*lead, rows, (n + 3) // 4 * 4), 127)
+    at[..., :n] = scale
+    return at.view(*lead, rows, -1, 4).transpose(-2, -3).contiguous()
+
+
+def _check_codes(codes, scale, what: str):
+    """Checks MXFP4 codes [..., rows, d / 2] and their scales; returns (batch, rows, d)."""
+    if codes.dtype is not _u8t or scale.dtype is not _u8t:
+        raise TypeError(f"{what}: codes and scales must be uint8")
+    if codes.dim() < 2:
+        raise ValueError(f"{what}: codes must be [..., rows, d / 2]")
+    *lead, rows, half = codes.shape
+    if tuple(scale.shape) != (*lead, _planes(2 * half), rows, 4):
+        raise ValueError(f"{what}: scales must be [..., ceil(d / 128), rows, 4]")
+    batch = 1
+    for n in lead:
+        batch *= n
+    return batch, rows, 2 * half
+
+
+def quantize_mxfp4(x, out=None):
+    """``mlora_quantize_mxfp4``: x [..., rows, d], bf16 or float32, as (codes [..., rows, d / 2],
+    scale [..., ceil(d / 128), rows, 4]), both uint8; ``out`` is such a pair to write into."""
+    what, dev = "quantize_mxfp4", _device()
+    if x.dim() < 2:
+        raise ValueError("x must be [..., rows, d]")
+    code = _dtype_code(x.dtype)
+    *lead, rows, d = x.shape
+    if out is None:
+        out = x.new_empty((*lead, rows, d // 2), dtype=_u8t), x.new_empty((*lead, _planes(d), rows, 4), dtype=_u8t)
+    codes, scale = out
+    batch, r, n = _check_codes(codes, scale, what)
+    if codes.shape[:-1] != x.shape[:-1] or n != d:
+        raise ValueError("out must be (codes, scale) of x")
+    code = _lib.mlora_quantize_mxfp4(_at(x, dev, what), code, batch, r, d, _at(codes, dev, what), _at(scale, dev, what),
+                                     _raw_stream(dev))
+    if code:
+        raise MloraError(code, "mlora_quantize_mxfp4")
+    return codes, scale
+
+
+def dequantize_mxfp4(codes, scale, dtype: torch.dtype = torch.bfloat16, out=None):
+    """``mlora_dequantize_mxfp4``: the values of codes and scales, [..., rows, d] in bf16 or float32."""
+    what, dev = "dequantize_mxfp4", _device()
+    batch, rows, d = _check_codes(codes, scale, what)
+    code, shape = _dtype_code(dtype), (*codes.shape[:-1], d)
+    y = out if out is not None else codes.new_empty(shape, dtype=dtype)
+    if y.dtype is not dtype or tuple(y.shape) != shape:
+        raise ValueError(f"out must be {list(shape)} of {dtype}")
+    code = _lib.mlora_dequantize_mxfp4(_at(codes, dev, what), _at(scale, dev, what), code, batch, rows, d, _at(y, dev, what),
+                                       _raw_stream(dev))
+    if code:
+        raise MloraError(code, "mlora_dequantize_mxfp4")
+    return y
+
+
+def linear_mxfp4(x, W, w_scale, pool: Pool, seg_start=None, seg_adapter=None, seg_rank=None, seg_scale=None,
+                 lora_on: int = 1, token_index=None, x_codes=None, x_scale=None, bias=None, act: str = "none",
+                 gated: bool = False, residual=None, out=None, workspace=None):
+    """``mlora_linear_mxfp4``: ``linear_epilogue`` with the base weight in MXFP4: codes W
+    [d_out, d_in / 2] and w_scale. With x_codes and x_scale (``quantize_mxfp4`` of x) the base
+    product takes these, and the adapter term x; without, both take x."""
+    what, dev, d_out, d_in = "linear_mxfp4", _device(), pool.d_out, pool.d_in
+    if x.dtype is not _bf16t or pool.dtype is not _bf16t:
+        raise TypeError("x and the pool must be bf16")
+    if x.dim() != 2 or x.shape[1] != d_in:
+        raise ValueError("x must be [T, d_in]")
+    if _check_codes(W, w_scale, what) != (1, d_out, d_in) or W.dim() != 2:
+        raise ValueError("W must be codes [d_out, d_in / 2]")
+    T = x.shape[0]
+    if (x_codes is None) != (x_scale is None):
+        raise ValueError("x_codes and x_scale come together")
+    if x_codes is not None and (_check_codes(x_codes, x_scale, what) != (1, T, d_in) or x_codes.dim() != 2):
+        raise ValueError("x_codes must be codes [T, d_in / 2]")
+    if seg_scale is not None and seg_scale.dtype is not _f32t:
+        raise TypeError("seg_scale must be float32")
+    n_seg = _segments(T, lora_on, seg_start, seg_adapter, seg_rank, seg_scale, token_index)
+    code = _act_code(act, gated)
+    y = _epilogue_out(x, T, d_out, gated, bias, (d_out,), residual, out)
+    ws = workspace if workspace is not None else pool.workspace(T)
+    epi = _Epilogue(_at(bias, dev, what), _at(residual, dev, what), code)
+    code = _lib.mlora_linear_mxfp4(_at(x, dev, what), _at(x_codes, dev, what), _at(x_scale, dev, what), _at(W, dev, what),
+                                   _at(w_scale, dev, what), pool.handle, _at_i32(seg_start, dev, what),
+                                   _at_i32(seg_adapter, dev, what), _at_i32(seg_rank, dev, what), _at(seg_scale, dev, what),
+                                   _at_i32(token_index, dev, what), T, n_seg, lora_on, ctypes.byref(epi), _at(y, dev, what),
+                                   _at(ws, dev, what), ws.numel(), _raw_stream(dev))
+    if code:
+        raise MloraError(code, "mlora_linear_mxfp4")
+    return y
+
+
 # ---- experts ---------------------------------------------------------------------
 
 def route_workspace(n_tokens: int, n_experts: int, top_k: int, device="cuda") -> torch.Tensor:
@@ -484,11 +601,17 @@ def route_workspace(n_tokens: int, n_experts: int, top_k: int, device="cuda") ->
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None):
+def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None, scores: Optional[str] = None,
+          bias=None, n_groups: int = 1, top_groups: Optional[int] = None, scale: float = 1.0):
     """``mlora_route``: top-k expert choice of logits [T, E] and its segments.
     Returns (expert [T, k], weight [T, k], token_index [T k], seg_start [E + 1],
     position [T, k]), views of one allocation, which any of them keeps; ``out`` is such a tuple
-    to write into."""
+    to write into.
+
+    With any of ``scores`` ("softmax" or "sigmoid"), ``bias`` [E] float32, ``n_groups`` or
+    ``scale`` it is ``mlora_route_scored``: the choice goes by scores + bias among the
+    ``top_groups`` best of ``n_groups`` groups (all of them where not given), the weights by
+    scale * scores."""
     what, dev = "route", _device()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
@@ -496,6 +619,16 @@ def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None
     T, E = logits.shape
     if not 1 <= top_k <= E:
         raise MloraError(STATUS_CODE["MLORA_ERR_SHAPE"], "mlora_route")
+    scored = scores is not None or bias is not None or n_groups != 1 or scale != 1.0
+    if scored:
+        kind = SCORES.get(scores or "softmax")
+        if kind is None:
+            raise ValueError(f"scores must be one of {sorted(SCORES)}")
+        if bias is not None and (bias.dtype is not _f32t or bias.shape != (E,)):
+            raise ValueError("bias must be float32 [E]")
+        how = _Scoring(kind, _at(bias, dev, what), n_groups, n_groups if top_groups is None else top_groups, scale)
+    elif top_groups not in (None, 1):
+        raise ValueError("top_groups without n_groups")
     at_logits, P = _at(logits, dev, what), T * top_k
     ws = workspace if workspace is not None else route_workspace(T, E, top_k, logits.device)
     if out is None:
@@ -512,16 +645,34 @@ def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None
         if len(out) != len(want) or any(t.numel() != n or t.dtype is not dt for t, (n, dt) in zip(out, want)):
             raise ValueError("out must be (expert, weight, token_index, seg_start, position) of this batch")
         ptrs = [_at(t, dev, what) for t in out]
-    code = _lib.mlora_route(at_logits, code, T, E, top_k, 1 if renormalize else 0, *ptrs, _at(ws, dev, what), ws.numel(),
-                            _raw_stream(dev))
+    norm, end = 1 if renormalize else 0, (_at(ws, dev, what), ws.numel(), _raw_stream(dev))
+    if scored:
+        code = _lib.mlora_route_scored(at_logits, code, T, E, top_k, norm, ctypes.byref(how), *ptrs, *end)
+    else:
+        code = _lib.mlora_route(at_logits, code, T, E, top_k, norm, *ptrs, *end)
     if code:
-        raise MloraError(code, "mlora_route")
+        raise MloraError(code, "mlora_route_scored" if scored else "mlora_route")
     return out
 
 
-def _check_experts(x, W, seg_start, w_scale):
+def _check_experts(x, W, seg_start, w_scale, x_scale=None):
     """Checks the operands of an expert product; returns (dtype code, E, d_out, d_in)."""
     dt = x.dtype
+    if w_scale is not None and w_scale.dtype is _u8t:   # MXFP4
+        if W.dim() != 3 or x.dim() != 2:
+            raise ValueError("x must be [rows, d_in] and W codes [E, d_out, d_in / 2]")
+        E, d_out, d_in = W.shape[0], W.shape[1], 2 * W.shape[2]
+        _check_codes(W, w_scale, "MXFP4 weight")
+        if x_scale is not None:
+            if _check_codes(x, x_scale, "MXFP4 rows")[2] != d_in:
+                raise ValueError("x and W must have as many columns")
+        elif dt is not _bf16t or x.shape[1] != d_in:
+            raise ValueError("x must be bf16 [rows, d_in], or MXFP4 codes with x_scale")
+        if seg_start.dtype is not _i32t or seg_start.numel() != E + 1:
+            raise ValueError("seg_start must be int32 [E + 1]")
+        return MLORA_BF16, E, d_out, d_in
+    if x_scale is not None:
+        raise TypeError("x_scale comes with a weight in MXFP4")
     code = _dtype_code(dt)
     if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
         raise ValueError("x must be [rows, d_in] and W [E, d_out, d_in]")
@@ -540,16 +691,27 @@ def _check_experts(x, W, seg_start, w_scale):
 
 
 def experts_linear(x, W, seg_start, token_index=None, bias=None, act: str = "none", gated: bool = False,
-                   w_scale=None, out=None):
+                   w_scale=None, out=None, x_scale=None):
     """``mlora_experts_linear``: act(W_e x[token_index[p]] + bias_e) for the sorted
     positions p of every expert e (``route``'s seg_start and token_index), gated as
-    ``linear_epilogue``. Rows of the result behind seg_start[-1] are not written."""
+    ``linear_epilogue``. Rows of the result behind seg_start[-1] are not written. W holds e4m3
+    codes with a float32 ``w_scale``, MXFP4 codes with a uint8 one (``mlora_experts_linear_mxfp4``),
+    and then x may too, with its ``x_scale``."""
     what, dev = "experts_linear", _device()
-    code, E, d_out, d_in = _check_experts(x, W, seg_start, w_scale)
+    code, E, d_out, d_in = _check_experts(x, W, seg_start, w_scale, x_scale)
+    mx = w_scale is not None and w_scale.dtype is _u8t
     n_rows = x.shape[0]
     n_pos = token_index.numel() if token_index is not None else n_rows
     epi = _Epilogue(_at(bias, dev, what), None, _act_code(act, gated))
-    y = _epilogue_out(x, n_pos, d_out, gated, bias, (E, d_out), None, out)
+    y = _epilogue_out(x, n_pos, d_out, gated, bias, (E, d_out), None, out, _bf16t if mx else None)
+    if mx:
+        code = _lib.mlora_experts_linear_mxfp4(_at(x, dev, what), _at(x_scale, dev, what), _at(W, dev, what),
+                                               _at(w_scale, dev, what), n_rows, E, d_in, d_out, _at(seg_start, dev, what),
+                                               _at_i32(token_index, dev, what), n_pos, ctypes.byref(epi), _at(y, dev, what),
+                                               _raw_stream(dev))
+        if code:
+            raise MloraError(code, "mlora_experts_linear_mxfp4")
+        return y
     code = _lib.mlora_experts_linear(_at(x, dev, what), _at(W, dev, what), _at(w_scale, dev, what), code, n_rows, E, d_in,
                                      d_out, _at(seg_start, dev, what), _at_i32(token_index, dev, what), n_pos,
                                      ctypes.byref(epi), _at(y, dev, what), _raw_stream(dev))
@@ -568,11 +730,13 @@ def experts_workspace(n_tokens: int, top_k: int, n_experts: int, d_out: int, dty
 
 
 def experts_combine(h, W, seg_start, position, weight, bias=None, residual=None, w_scale=None, out=None,
-                    workspace=None):
+                    workspace=None, x_scale=None):
     """``mlora_experts_combine``: residual[t] + sum_j weight[t, j] (W_e h[position[t, j]] + bias_e),
-    with ``route``'s seg_start, position and weight. ``residual`` may be ``out`` itself."""
+    with ``route``'s seg_start, position and weight. ``residual`` may be ``out`` itself. MXFP4
+    weights and rows (x_scale: those of h) as ``experts_linear`` (``mlora_experts_combine_mxfp4``)."""
     what, dev = "experts_combine", _device()
-    code, E, d_out, d_in = _check_experts(h, W, seg_start, w_scale)
+    code, E, d_out, d_in = _check_experts(h, W, seg_start, w_scale, x_scale)
+    mx = w_scale is not None and w_scale.dtype is _u8t
     if position.dim() != 2 or position.dtype is not _i32t:
         raise ValueError("position must be int32 [T, k]")
     T, k = position.shape
@@ -580,8 +744,17 @@ def experts_combine(h, W, seg_start, position, weight, bias=None, residual=None,
         raise ValueError("weight must be float32 [T, k]")
     if h.shape[0] != T * k:
         raise ValueError("h must hold a row per slot: [T k, d_in]")
-    y = _epilogue_out(h, T, d_out, False, bias, (E, d_out), residual, out)
-    ws = workspace if workspace is not None else experts_workspace(T, k, E, d_out, h.dtype, h.device)
+    y = _epilogue_out(h, T, d_out, False, bias, (E, d_out), residual, out, _bf16t if mx else None)
+    ws = workspace if workspace is not None else experts_workspace(T, k, E, d_out, y.dtype, h.device)
+    if mx:
+        code = _lib.mlora_experts_combine_mxfp4(_at(h, dev, what), _at(x_scale, dev, what), _at(W, dev, what),
+                                                _at(w_scale, dev, what), T, k, E, d_in, d_out, _at(seg_start, dev, what),
+                                                _at(position, dev, what), _at(weight, dev, what), _at(bias, dev, what),
+                                                _at(residual, dev, what), _at(y, dev, what), _at(ws, dev, what), ws.numel(),
+                                                _raw_stream(dev))
+        if code:
+            raise MloraError(code, "mlora_experts_combine_mxfp4")
+        return y
     code = _lib.mlora_experts_combine(_at(h, dev, what), _at(W, dev, what), _at(w_scale, dev, what), code, T, k, E, d_in,
                                       d_out, _at(seg_start, dev, what), _at(position, dev, what), _at(weight, dev, what),
                                       _at(bias, dev, what), _at(residual, dev, what), _at(y, dev, what),

@@ -13,6 +13,7 @@
 
 #include "../../include/mlora.h"
 #include "launch.h"
+#include "mxfp4.h"
 
 using namespace mlora;
 
@@ -217,13 +218,21 @@ bool use_dense_expand(const mlora_pool_s* p, const SegView& sv, int T, int lora_
   return p->max_rank >= 32;
 }
 
+// MXFP4 operands of a call: W's scales, and x's codes and scales or null.
+struct MxArgs {
+  const uint8_t* w_scale;
+  const uint8_t* x_codes;
+  const uint8_t* x_scale;
+};
+
 // Launch the layer on sorted metadata already resident on the device.
 // w_scale != null: W holds FP8 e4m3 codes with a float32 scale per row (bf16
 // pool, split-K decode path only; the caller has checked the shape).
 // epi != null: what follows the layer, already checked (epi_status).
+// mx != null: W holds MXFP4 codes (bf16 pool; the caller has checked the shape).
 int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& sv, int T,
                int lora_on, void* y, char* ws, hipStream_t stream, const float* w_scale = nullptr,
-               const mlora_epilogue_t* epi = nullptr) {
+               const mlora_epilogue_t* epi = nullptr, const MxArgs* mx = nullptr) {
   const WsLayout L = ws_layout(pool, T);
   LinearArgs a;
   a.x = x;
@@ -245,9 +254,14 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
   a.wnt = 0;
   a.epi_kind = epi_kind_of(epi);
   a.epi = epi_view_of(epi);
+  if (mx) {
+    a.w_mx = mx->w_scale;
+    a.x_codes = mx->x_codes;
+    a.x_mx = mx->x_scale;
+  }
   if (pool->dtype == MLORA_BF16) {
-    // (the GEMV has no form with an epilogue: such a call is not forced)
-    const int fp = a.epi_kind != kEpiNone && forced_path() == 3 ? 0 : forced_path();
+    // (the GEMV has no form with an epilogue or an MXFP4 weight: such a call is not forced)
+    const int fp = (a.epi_kind != kEpiNone || mx) && forced_path() == 3 ? 0 : forced_path();
     // The split-K decode path up to 64 tokens, except on wide layers from 48
     // tokens up; the tiled GEMM otherwise. Measured per path, token count and
     // pass with HBM counters in profiles/path_sweep.txt: on 4096 -> 4096 the
@@ -257,7 +271,7 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
     // passes of a shape and token count take the same path, so a zero B
     // reproduces the LoRA-off bits.
     const bool wide = T >= 48 && pool->d_out >= 8192;
-    const bool dec_ok = decode_supported(T, lora_on ? sv.n_seg : 0, pool->d_out, pool->max_rank);
+    const bool dec_ok = decode_supported(T, lora_on ? sv.n_seg : 0, pool->d_out, pool->max_rank) && !a.x_mx;
     if (w_scale || (dec_ok && (fp == 1 || (fp == 0 && !wide)))) {
       DecodeArgs d;
       d.x = x;
@@ -275,11 +289,13 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
       d.r_ws = a.r_ws;
       d.epi_kind = a.epi_kind;
       d.epi = a.epi;
-      decode_plan(pool->d_in, pool->d_out, &d.n_tiles, &d.kc, &d.n_chunks);
+      // (chunks of whole planes of scales are as many or fewer, so the workspace holds them)
+      decode_plan(pool->d_in, pool->d_out, &d.n_tiles, &d.kc, &d.n_chunks, mx ? kMxPlane : 64);
       d.unit_rows = decode_unit_rows(lora_on ? sv.n_seg : 0, pool->max_rank, d.n_tiles);
       d.w_scale = w_scale;
+      d.w_mx = a.w_mx;
       if (log_calls())
-        log_call(w_scale ? "decode-fp8w" : "decode", T, pool, sv, lora_on, d.n_chunks, lora_on ? "fused" : "none");
+        log_call(w_scale ? "decode-fp8w" : mx ? "decode-mxfp4" : "decode", T, pool, sv, lora_on, d.n_chunks, lora_on ? "fused" : "none");
       launch_decode_bf16(d, stream);
       return check_launch();
     }
@@ -300,7 +316,7 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
     }
     if (use_dense_expand(pool, sv, T, lora_on)) a.delta = (float*)(ws + L.delta);
     if (log_calls())
-      log_call(a.delta ? "gemm-dense-expand" : "gemm", T, pool, sv, lora_on, a.ks,
+      log_call(a.delta ? (mx ? "gemm-mxfp4-dense-expand" : "gemm-dense-expand") : mx ? "gemm-mxfp4" : "gemm", T, pool, sv, lora_on, a.ks,
                !lora_on || a.seg_grid <= 0 ? "none" : shrink_short(a) ? "short" : "mfma");
     launch_linear_bf16(a, stream);
   } else {
@@ -662,6 +678,47 @@ int mlora_linear_fp8w(const void* x, const uint8_t* W_fp8, const float* w_scale,
   return mlora_linear_fp8w_epilogue(x, W_fp8, w_scale, pool, seg_start, seg_adapter, seg_rank, seg_scale,
                                     token_index, n_tokens, n_seg, lora_on, nullptr, y, workspace,
                                     workspace_bytes, stream);
+}
+
+int mlora_linear_mxfp4(const void* x, const uint8_t* x_codes, const uint8_t* x_scale, const uint8_t* W,
+                       const uint8_t* w_scale, mlora_pool_t pool, const int32_t* seg_start,
+                       const int32_t* seg_adapter, const int32_t* seg_rank, const float* seg_scale,
+                       const int32_t* token_index, int n_tokens, int n_seg, int lora_on,
+                       const mlora_epilogue_t* epilogue, void* y, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream) {
+  if (!pool) return MLORA_ERR_INVALID_ARG;
+  if (pool->dtype != MLORA_BF16) return MLORA_ERR_DTYPE;
+  if (const int st = epi_status(epilogue, pool->d_out)) return st;
+  if (lora_on != 0 && lora_on != 1) return MLORA_ERR_INVALID_ARG;
+  if (n_tokens < 0 || n_tokens > MLORA_MAX_TOKENS) return MLORA_ERR_SHAPE;
+  if (pool->d_in % kMxBlock != 0) return MLORA_ERR_SHAPE;
+  if (!x_codes != !x_scale) return MLORA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return MLORA_OK;
+  if (!x || !W || !w_scale || !y || !workspace) return MLORA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(x_codes) || !aligned16(x_scale) || !aligned16(W) || !aligned16(w_scale) ||
+      !aligned16(y) || !aligned16(workspace))
+    return MLORA_ERR_INVALID_ARG;
+  if (workspace_bytes < ws_layout(pool, n_tokens).total) return MLORA_ERR_WORKSPACE;
+  SegView sv{};
+  if (lora_on) {
+    if (!seg_start || !seg_adapter || !seg_rank || !seg_scale) return MLORA_ERR_INVALID_ARG;
+    if (n_seg < 1) return MLORA_ERR_METADATA;
+    if (n_seg > MLORA_MAX_SEGMENTS) return MLORA_ERR_SHAPE;
+    sv.seg_start = seg_start;
+    sv.seg_adapter = seg_adapter;
+    sv.seg_rank = seg_rank;
+    sv.seg_scale = seg_scale;
+    sv.token_index = token_index;
+    sv.n_seg_dev = nullptr;
+    sv.n_seg = n_seg;
+    if (debug_validate()) {
+      const int st = mlora_validate(pool, seg_start, seg_adapter, seg_rank, token_index, n_tokens, n_seg,
+                                    workspace, workspace_bytes, stream);
+      if (st != MLORA_OK) return st;
+    }
+  }
+  const MxArgs mx{w_scale, x_codes, x_scale};
+  return run_linear(x, W, pool, sv, n_tokens, lora_on, y, (char*)workspace, stream, nullptr, epilogue, &mx);
 }
 
 int mlora_build_segments(const int32_t* token_adapter, const float* adapter_scale, int n_tokens,

@@ -18,6 +18,11 @@ struct RouteArgs {
   int32_t* position;      // [T, k]
   int32_t* hist;          // workspace: slots per expert of every block's tokens [blocks][E]
   int tpb;                // tokens per block
+  // choice by scores (mlora_route_scored); scored = 0: by logits
+  int scored, sigmoid;
+  const float* bias;      // [E] or null
+  int groups, top_groups;
+  float scale;
 };
 size_t route_workspace_bytes(int T, int E);
 void launch_route(const RouteArgs& a, bool bf16, hipStream_t st);
@@ -27,6 +32,8 @@ struct ExpertsArgs {
   const void* x;                // [n_rows, d_in]
   const void* W;                // [E, d_out, d_in]
   const float* w_scale;         // [E, d_out]: W holds e4m3 codes; null: W in x's type
+  const uint8_t* w_mx;          // [E, planes, d_out, 4]: W holds MXFP4 codes, these are their scales
+  const uint8_t* x_mx;          // [planes, n_rows, 4]: x holds MXFP4 codes too (with w_mx only)
   void* y;                      // [n_pos, d_y]; where f32_out fp32 [n_pos, f32_pitch(d_out)]
   const int32_t* seg_start;     // [E + 1]
   const int32_t* token_index;   // [n_pos] or null

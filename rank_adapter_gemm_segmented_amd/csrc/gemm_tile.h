@@ -5,6 +5,7 @@
 
 #include "common.h"
 #include "epilogue.h"
+#include "mxfp4.h"
 
 namespace mlora {
 
@@ -39,6 +40,12 @@ __device__ __forceinline__ void dma16_nt(const void* g, uint32_t m0) {
                : "memory", "m0");
 }
 
+// Four bytes per lane, lane l's at byte m0 + 4 l.
+__device__ __forceinline__ void dma4(const void* g, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(m0)
+               : "memory", "m0");
+}
+
 // The same with a uniform base and a 32-bit byte offset per lane.
 __device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t m0) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m0)
@@ -59,26 +66,36 @@ __device__ __forceinline__ void vm_barrier() {
 // are 2 KB bytes (KB bf16), unpadded, and 16-byte chunk c of row r sits in slot
 // c ^ gswz(r) of the row, so the rows read together by one fragment load fall
 // in distinct LDS banks.
-// W8: the W rows are FP8 codes of KB bytes (one per column), in the same ring.
-template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, bool W8 = false>
+// WQ: how W is stored. kWFp8: the W rows are FP8 codes of KB bytes (one per column),
+// in the same ring. kWMx: MXFP4 codes of KB / 2 bytes. kWMxX: the positions' rows
+// are MXFP4 codes too. The scales come along in a third ring (NX slots), a part per
+// wave: the dwords of its own rows, DPW_S loads of 256 bytes per stage.
+constexpr int kWBf16 = 0, kWFp8 = 1, kWMx = 2, kWMxX = 3;
+
+template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, int WQ = kWBf16>
 struct GCfg {
-  static constexpr bool kW8 = W8;
-  static constexpr int WRB = W8 ? KB : 2 * KB;             // bytes per LDS row of W
+  static constexpr int kWQ = WQ;
+  static constexpr bool kW8 = WQ == kWFp8;
+  static constexpr int WRB = WQ >= kWMx ? KB / 2 : WQ == kWFp8 ? KB : 2 * KB;   // bytes per LDS row of W
   static constexpr int kBR = BR, kBT = BT, kWR = WR, kWT = WT, kNB = NB, kKB = KB, kNX = NX;
   static constexpr int NWR = BR / WR, NWT = BT / WT;
   static constexpr int NW = NWR * NWT;
   static constexpr int NT = NW * kWave;
   static constexpr int MR = WR / 32, MT = WT / 32;        // 32x32 blocks per wave
-  static constexpr int RB = 2 * KB;                        // bytes per LDS row of positions
+  static constexpr int RB = WQ == kWMxX ? KB / 2 : 2 * KB;  // bytes per LDS row of positions
   static constexpr int WSTAGE_B = BR * WRB, XSTAGE_B = BT * RB;   // ring slots
   static constexpr int DPW_W = BR * WRB / 1024 / NW;    // 1 KB loads per wave per stage: W rows
-  static constexpr int DPW_X = BT * 2 * KB / 1024 / NW;    // and positions
+  static constexpr int DPW_X = BT * RB / 1024 / NW;        // and positions
   static constexpr int DPW = DPW_W + DPW_X;
+  // loads of scales: 64 of the wave's W rows each, or (kWMxX) two planes of 32 rows of either side
+  static constexpr int DPW_S = WQ == kWMx ? (WR + 63) / 64 : WQ == kWMxX ? MR + MT : 0;
+  static constexpr int SSTAGE_B = NW * DPW_S * 256;
   static constexpr int XRING = NB * WSTAGE_B;              // byte offset of the position ring
-  static constexpr int MAIN_BYTES = NB * WSTAGE_B + NX * XSTAGE_B;
+  static constexpr int SRING = XRING + NX * XSTAGE_B;      // and of the ring of scales
+  static constexpr int MAIN_BYTES = SRING + NX * SSTAGE_B;
   // DMAs a wave has issued after stage st's position DMAs when stage st is
   // multiplied (its W DMAs were issued earlier still)
-  static constexpr int VMC = (NX - 2) * DPW;
+  static constexpr int VMC = (NX - 2) * (DPW + DPW_S);
   // small row tiles get extra LDS so the epilogue stages many segment runs at
   // once; the y tile of the store passes through the same LDS
   static constexpr int YT_BYTES = NW * WT * (2 * WR + 16);
@@ -89,8 +106,8 @@ struct GCfg {
   static constexpr int EPI_MC = MR >= 2 ? MR / 2 : 1;
   static constexpr int EPI_BYTES = NW * 32 * (EPI_MC * 128 + 16);
   static constexpr int TILE_BYTES = MAIN_BYTES > EPI_BYTES ? MAIN_BYTES : EPI_BYTES;
-  static_assert(KB == 32 || KB == 64 || (W8 && KB == 128), "stage depth");
-  static_assert((BR * WRB) % (1024 * NW) == 0 && (BT * 2 * KB) % (1024 * NW) == 0,
+  static_assert(WQ == kWMxX ? KB == 256 : KB == 64 || (WQ == kWBf16 && KB == 32) || (WQ != kWBf16 && KB == 128), "stage depth");
+  static_assert((BR * WRB) % (1024 * NW) == 0 && (BT * RB) % (1024 * NW) == 0,
                 "each ring's stage splits into whole loads per wave");
   static_assert(NB >= 2 && NX >= 2 && NB >= NX && VMC <= 63, "ring depths and vmcnt range");
 };
@@ -103,10 +120,11 @@ struct GCfg {
 // the parity flips the slot's top bit. KB = 32: four rows per 256 bytes,
 // separated through r >> 2. Both were checked with the LDS bank-conflict
 // counter on a read-pattern probe (no conflicts), where the plain r & 7 and
-// (r >> 1) & 3 permutations conflicted two ways.
+// (r >> 1) & 3 permutations conflicted two ways. (KB goes by the row's bytes: half of
+// them. 16: rows of 32 bytes, MXFP4 codes of 64 columns.)
 template <int KB>
 __device__ __forceinline__ int gswz(int r) {
-  return KB == 128 ? r & 15 : KB == 64 ? (((r >> 1) ^ ((r & 1) << 2)) & 7) : ((r >> 2) & 3);
+  return KB == 128 ? r & 15 : KB == 64 ? (((r >> 1) ^ ((r & 1) << 2)) & 7) : KB == 32 ? ((r >> 2) & 3) : ((r >> 3) & 1);
 }
 
 // Scheduling hint for one k-step: the R fragment reads of the next k-step
@@ -126,11 +144,15 @@ __device__ __forceinline__ void sched_reads_over_mfma() {
 // 1024 J + 16 l of the slot, i.e. one 16-byte slot of a row r, and so fetches
 // chunk (slot ^ swizzle of r) of that row. wrow(r) and xrow(r) give the address
 // of the tile's r-th W row and position.
+// (MXFP4: set_scales gives the addresses of the scales that a wave loads.)
 template <class C>
 struct TileSrc {
-  static constexpr int kWSw = C::WRB / 2;                 // (gswz goes by the row's bytes)
+  static constexpr int kWSw = C::WRB / 2, kXSw = C::RB / 2;   // (gswz goes by the row's bytes)
+  static constexpr int kWCols = C::kWQ >= kWMx ? 32 : C::kW8 ? 16 : 8, kXCols = C::kWQ == kWMxX ? 32 : 8;   // columns per 16 bytes
   const char* src[C::DPW];
   int scol[C::DPW];                                       // first column of the lane's chunk
+  const char* ssrc[C::DPW_S > 0 ? C::DPW_S : 1];          // scales: the lane's row, plane 0
+  long long wplane, xplane;                               // bytes from a plane of scales to the next
   template <class WRow, class XRow>
   __device__ __forceinline__ void set(int wave, int lane, WRow wrow, XRow xrow) {
 #pragma unroll
@@ -138,14 +160,27 @@ struct TileSrc {
       const bool isx = i >= C::DPW_W;
       const int at = ((isx ? i - C::DPW_W : i) * C::NW + wave) * 64 + lane;   // 16-byte slot of the ring slot
       if (isx) {
-        const int r = at / (C::RB / 16), c = (at % (C::RB / 16)) ^ gswz<C::kKB>(r);
+        const int r = at / (C::RB / 16), c = (at % (C::RB / 16)) ^ gswz<kXSw>(r);
         src[i] = (const char*)xrow(r) + 16 * c;
-        scol[i] = 8 * c;
+        scol[i] = kXCols * c;
       } else {
         const int r = at / (C::WRB / 16), c = (at % (C::WRB / 16)) ^ gswz<kWSw>(r);
         src[i] = (const char*)wrow(r) + 16 * c;
-        scol[i] = (C::kW8 ? 16 : 8) * c;
+        scol[i] = kWCols * c;
       }
+    }
+  }
+  // wscale(r), xscale(r): the scales of the tile's r-th W row and position in plane 0
+  template <class WScale, class XScale>
+  __device__ __forceinline__ void set_scales(int wave, int lane, long long wplane_, long long xplane_, WScale wscale, XScale xscale) {
+    const int wr = wave / C::NWT, wt = wave % C::NWT;
+    wplane = wplane_;
+    xplane = xplane_;
+#pragma unroll
+    for (int i = 0; i < C::DPW_S; ++i) {
+      if constexpr (C::kWQ == kWMx) ssrc[i] = (const char*)wscale(wr * C::kWR + (C::kWR < 64 ? lane % C::kWR : 64 * i + lane));
+      else if (i < C::MR) ssrc[i] = (const char*)wscale(wr * C::kWR + 32 * i + lane % 32);
+      else ssrc[i] = (const char*)xscale(wt * C::kWT + 32 * (i - C::MR) + lane % 32);
     }
   }
   // load I of stage st (W rows for I < DPW_W, else positions) into the ring;
@@ -157,8 +192,17 @@ struct TileSrc {
     const uint32_t slot = isx ? lds0 + C::XRING + (uint32_t)(st % C::kNX) * C::XSTAGE_B
                               : lds0 + (uint32_t)(st % C::kNB) * C::WSTAGE_B;
     const int k0 = st * C::kKB;
-    dma16(sel_addr(k0 + scol[I] < d_in, src[I] + k0 * (isx || !C::kW8 ? 2 : 1), zeros),
+    dma16(sel_addr(k0 + scol[I] < d_in, src[I] + st * (isx ? C::RB : C::WRB), zeros),
           slot + (uint32_t)(j * C::NW + wave) * 1024);
+  }
+  // load I of stage st's scales: the plane that holds the stage's columns, or
+  // (kWMxX) lane half h's of the stage's two
+  template <int I>
+  __device__ __forceinline__ void issue_scale(int st, uint32_t lds0, int wave, int lane, int d_in, const void* zeros) const {
+    const int plane = C::kWQ == kWMx ? st * C::kKB / kMxPlane : 2 * st + lane / 32;
+    const bool isx = C::kWQ == kWMxX && I >= C::MR;
+    dma4(sel_addr(plane * kMxPlane < d_in, ssrc[I] + plane * (isx ? xplane : wplane), zeros),
+         lds0 + C::SRING + (uint32_t)(st % C::kNX) * C::SSTAGE_B + (uint32_t)(wave * C::DPW_S + I) * 256);
   }
 };
 
@@ -170,7 +214,7 @@ struct TileSrc {
 // The caller keeps W's tile and all of x within 4 GB of their bases.
 template <class C>
 struct PipeSrc {
-  static_assert(C::NW == 4 && C::kNB >= C::kNX && !C::kW8, "one chunk column per lane");
+  static_assert(C::NW == 4 && C::kNB >= C::kNX && C::kWQ == kWBf16, "one chunk column per lane");
   static constexpr int RPC = 1024 / C::RB, CPR = C::RB / 16;   // rows of a 1 KB chunk, 16-byte chunks of a row
   const char* wb;
   const char* xb;
@@ -332,17 +376,31 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
 // 16 h .. + 15 of step pair q, so the position fragments of steps 2 q and 2 q + 1
 // are columns 32 q + 16 h .. + 7 and + 8 .. + 15: which column sits in which k slot
 // of an MFMA does not matter as long as both operands agree.
+//
+// MXFP4 W (kWMx): a lane reads 32 codes at once, the block 2 j + h of step group j
+// (64 columns, 4 k-steps) for lane half h, and converts 8 of them per step with
+// their scale, exactly; the position fragment of step q of the group is columns 32
+// (2 j + h) + 8 q .. + 7.
+//
+// MXFP4 positions too (kWMxX): a stage is 256 columns in rows of 128 bytes, as a
+// bf16 stage of 64, and a 16-byte fragment one block, multiplied with its scale by
+// the matrix unit. K-step kk takes block 4 h + kk for lane half h, so that the half's
+// four scales of a stage are one dword: the row's, of plane 2 st + h.
 template <class C>
 __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, const void* zeros, char* lds,
                                               int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
-  constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = KB / 16;
+  constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX;
+  constexpr int KS = C::kWQ == kWMxX ? KB / 64 : KB / 16;
   const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   int fx[KS], fw[KS];                                     // byte of the lane's chunk in its row
 #pragma unroll
   for (int kk = 0; kk < KS; ++kk) {
-    fx[kk] = ((C::kW8 ? (kk >> 1) * 4 + 2 * kh + (kk & 1) : kk * 2 + kh) ^ gswz<KB>(l32)) * 16;
-    fw[kk] = ((C::kW8 ? (kk >> 1) * 2 + kh : kk * 2 + kh) ^ gswz<TileSrc<C>::kWSw>(l32)) * 16;
+    const int cx = C::kWQ == kWMxX ? 4 * kh + kk : C::kWQ == kWMx ? (kk >> 2) * 8 + 4 * kh + (kk & 3)
+                   : C::kW8 ? (kk >> 1) * 4 + 2 * kh + (kk & 1) : kk * 2 + kh;
+    const int cw = C::kWQ == kWMxX ? 4 * kh + kk : C::kWQ == kWMx ? (kk >> 2) * 2 + kh : C::kW8 ? (kk >> 1) * 2 + kh : kk * 2 + kh;
+    fx[kk] = (cx ^ gswz<TileSrc<C>::kXSw>(l32)) * 16;
+    fw[kk] = (cw ^ gswz<TileSrc<C>::kWSw>(l32)) * 16;
   }
   auto load_w = [&](int st) {
     [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<I>(st, lds0, wave, d_in, zeros), ...); }
@@ -351,6 +409,8 @@ __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, con
   auto load_x = [&](int st) {
     [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue<C::DPW_W + I>(st, lds0, wave, d_in, zeros), ...); }
     (std::make_integer_sequence<int, C::DPW_X>{});
+    [&]<int... I>(std::integer_sequence<int, I...>) { (s.template issue_scale<I>(st, lds0, wave, lane, d_in, zeros), ...); }
+    (std::make_integer_sequence<int, C::DPW_S>{});
   };
 #pragma unroll
   for (int t = 0; t < NB - 1; ++t) {
@@ -364,34 +424,54 @@ __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, con
     load_x(st + NX - 1);
     const char* Lw = lds + (st % NB) * C::WSTAGE_B + (wr * C::kWR + l32) * C::WRB;
     const char* Lx = lds + C::XRING + (st % NX) * C::XSTAGE_B + (wt * C::kWT + l32) * C::RB;
-    u32x4_t fa[2][C::MR], fb[2][C::MT];                   // (FP8: fa by step pair)
+    const char* Ls = lds + C::SRING + (st % NX) * C::SSTAGE_B + wave * C::DPW_S * 256;
+    u32x4_t fa[2][C::MR], fb[2][C::MT];                   // (FP8: fa by step pair, kWMx: by step group)
+    constexpr int WG = C::kWQ == kWMx ? 4 : C::kW8 ? 2 : 1;   // k-steps per W fragment
     auto frag = [&](int kk) {
-      if (!C::kW8 || kk % 2 == 0) {
+      if (kk % WG == 0) {
 #pragma unroll
-        for (int m = 0; m < C::MR; ++m)
-          fa[C::kW8 ? (kk >> 1) & 1 : kk & 1][m] = *(const u32x4_t*)(Lw + m * 32 * C::WRB + fw[kk]);
+        for (int m = 0; m < C::MR; ++m) fa[(kk / WG) & 1][m] = *(const u32x4_t*)(Lw + m * 32 * C::WRB + fw[kk]);
       }
 #pragma unroll
       for (int n = 0; n < C::MT; ++n) fb[kk & 1][n] = *(const u32x4_t*)(Lx + n * 32 * C::RB + fx[kk]);
     };
-    frag(0);
+    uint32_t sw[C::kWQ >= kWMx ? C::MR : 1], sx[C::kWQ == kWMxX ? C::MT : 1];
+    if constexpr (C::kWQ == kWMx) {
 #pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
-      if (kk + 1 < KS) frag(kk + 1);
+      for (int m = 0; m < C::MR; ++m) sw[m] = *(const uint32_t*)(Ls + (m * 32 + l32) * 4) >> (8 * kh + (KB == 64 ? 16 * (st & 1) : 0));
+    } else if constexpr (C::kWQ == kWMxX) {
+#pragma unroll
+      for (int m = 0; m < C::MR; ++m) sw[m] = *(const uint32_t*)(Ls + m * 256 + lane * 4);
+#pragma unroll
+      for (int n = 0; n < C::MT; ++n) sx[n] = *(const uint32_t*)(Ls + (C::MR + n) * 256 + lane * 4);
+    }
+    frag(0);
+    auto step = [&](auto kc) {
+      constexpr int kk = decltype(kc)::value;
+      if constexpr (kk + 1 < KS) frag(kk + 1);
 #pragma unroll
       for (int m = 0; m < C::MR; ++m) {
-        u32x4_t wa;
-        if constexpr (C::kW8) {
-          const u32x4_t raw = fa[(kk >> 1) & 1][m];
-          wa = (kk & 1) ? e4m3x8_bf16(raw.z, raw.w) : e4m3x8_bf16(raw.x, raw.y);
-        } else {
-          wa = fa[kk & 1][m];
-        }
+        if constexpr (C::kWQ == kWMxX) {
 #pragma unroll
-        for (int n = 0; n < C::MT; ++n) acc[m][n] = mfma32g(wa, fb[kk & 1][n], acc[m][n]);
+          for (int n = 0; n < C::MT; ++n) acc[m][n] = mfma32mx<kk, kk>(fa[kk & 1][m], sw[m], fb[kk & 1][n], sx[n], acc[m][n]);
+        } else {
+          u32x4_t wa;
+          if constexpr (C::kW8) {
+            const u32x4_t raw = fa[(kk >> 1) & 1][m];
+            wa = (kk & 1) ? e4m3x8_bf16(raw.z, raw.w) : e4m3x8_bf16(raw.x, raw.y);
+          } else if constexpr (C::kWQ == kWMx) {
+            wa = mx_bf16x8(fa[(kk >> 2) & 1][m][kk & 3], mx_scale_at(sw[m], 2 * (kk >> 2)));
+          } else {
+            wa = fa[kk & 1][m];
+          }
+#pragma unroll
+          for (int n = 0; n < C::MT; ++n) acc[m][n] = mfma32g(wa, fb[kk & 1][n], acc[m][n]);
+        }
       }
-    }
-    if constexpr (!C::kW8) {
+    };
+    [&]<int... K>(std::integer_sequence<int, K...>) { (step(std::integral_constant<int, K>{}), ...); }
+    (std::make_integer_sequence<int, KS>{});
+    if constexpr (C::kWQ == kWBf16) {
       __builtin_amdgcn_sched_group_barrier(0x100, C::MR + C::MT, 0);
 #pragma unroll
       for (int kk = 0; kk + 1 < KS; ++kk) sched_reads_over_mfma<C::MR + C::MT, C::MR * C::MT>();

@@ -23,6 +23,7 @@
 // 8*(l/16)..+7 of each operand; result register v of lane l is row
 // 4*(l/16)+v, column l%16.
 #include "common.h"
+#include "gemm_tile.h"
 #include "launch.h"
 #include "stream_tile.h"
 
@@ -52,18 +53,22 @@ __device__ __forceinline__ long long part_off(int c, int i, int rb, int tb, int 
   return ((((long long)c * n_tiles + i) * 4 + rb) * ntb + tb) * 256;
 }
 
-// W8: W holds FP8 e4m3 codes (one byte per element, a float32 scale per row
+// WQ = kWFp8: W holds FP8 e4m3 codes (one byte per element, a float32 scale per row
 // applied by k_finish). A lane's 16-byte load then covers 16 columns, which
 // serve two consecutive k-steps: lane group g = l / 16 of the step pair
 // (2q, 2q + 1) starting at column C takes columns C + 16 g .. + 7 in step 2q
 // and C + 16 g + 8 .. + 15 in step 2q + 1, and reads x at the same columns.
+// WQ = kWMx: MXFP4 codes, 32 columns to a 16-byte load, one block with its scale:
+// lane group g of four k-steps starting at column C takes columns C + 32 g + 8 q
+// .. + 7 in step q (chunks are whole planes of scales).
 // GATED: the items' rows are virtual rows (epilogue.h). NT: W loads marked
 // nontemporal. With an epilogue they are not, but for 64 tokens on a long d_in:
 // a row's 128-byte line comes by two loads, and the mark loses it in between
 // (64 tokens, 4096 -> 4096: 18.2 us marked, 17.0 not; one token, gate|up in FP8:
 // 40.6 and 38.6; 64 tokens, 14336 -> 4096: 51.1 and 53.5).
-template <int TT, bool W8, bool GATED, bool NT>
+template <int TT, int WQ, bool GATED, bool NT>
 __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
+  constexpr bool W8 = WQ == kWFp8, MX = WQ == kWMx;
   constexpr int NTB = TT / 16;
   constexpr int XP = kDecXPitch;
   constexpr int XCH = TT * (kDecMaxKc / 8) / kDecThreads;  // 16-byte x pieces per thread
@@ -146,16 +151,26 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
   const int rb = wave & 3, kh = wave >> 2;
   const int nrow = tile * kDecRows + rb * 16 + l16;
   // (FP8: the first half ends on an even step, so no step pair straddles the halves)
-  const int half_steps = W8 ? (((nks + 1) / 2 + 1) & ~1) : (nks + 1) / 2;
+  // (and MXFP4: on a whole group of four)
+  const int half_steps = MX ? (((nks + 1) / 2 + 3) & ~3) : W8 ? (((nks + 1) / 2 + 1) & ~1) : (nks + 1) / 2;
   const int ks_begin = kh ? half_steps : 0;
   const int ks_end = kh ? nks : half_steps;
   const uint16_t* wrow = W + (long long)wrow_of<GATED>(nrow, d_out) * d_in + k0;
   const uint8_t* wrow8 = (const uint8_t*)a.W + (long long)wrow_of<GATED>(nrow, d_out) * d_in + k0;
+  const uint8_t* wrow4 = (const uint8_t*)a.W + ((long long)wrow_of<GATED>(nrow, d_out) * d_in + k0) / 2;
+  const uint8_t* wsc4 = MX ? a.w_mx + 4 * ((long long)(k0 / kMxPlane) * d_out + wrow_of<GATED>(nrow, d_out)) : nullptr;
   u32x4_t wr[kDecWSteps];
+  uint32_t ws[MX ? kDecWSteps / 4 : 1];            // MXFP4: the load's dword of scales
   auto ld_w = [](const void* p) { return NT ? ld_nt16(p) : ld16(p); };
   auto load_w = [&](int s) {
     // steps of the other k-half read the pool's zero block (address select)
-    if constexpr (W8) {   // slot s holds step pair (2s, 2s + 1)
+    if constexpr (MX) {   // slot s holds steps 4 s .. 4 s + 3
+      const int k = min((ks_begin + 4 * s) * 32 + 4 * kq, kc - 32);
+      const bool in = ks_begin + 4 * s < ks_end;
+      wr[s] = ld_w(in ? (const void*)(wrow4 + k / 2) : (const void*)((const uint16_t*)a.pv.zeros + kq));
+      // (the block's byte, shifted down where it is used)
+      ws[s] = *(const uint32_t*)(in ? (const void*)(wsc4 + 4ll * (k / kMxPlane) * d_out) : (const void*)zi);
+    } else if constexpr (W8) {   // slot s holds step pair (2s, 2s + 1)
       const int k = (ks_begin + 2 * s) * 32 + 2 * kq;
       wr[s] = ld_w(ks_begin + 2 * s < ks_end ? (const void*)(wrow8 + min(k, kc - 16))
                                                 : (const void*)((const uint16_t*)a.pv.zeros + kq));
@@ -167,8 +182,8 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
   // FP8: the 16 steps are 8 loads; half of them are requested ahead of the
   // x barrier, as for the bf16 weight (8 ahead: 16.7 us LoRA-on, 4: 16.2 us,
   // 2: 16.5 us on the decode batch)
-  constexpr int kWLoads = W8 ? kDecWSteps / 2 : kDecWSteps;
-  constexpr int kWPre = W8 ? kWLoads / 2 : kDecWPre;
+  constexpr int kWLoads = MX ? kDecWSteps / 4 : W8 ? kDecWSteps / 2 : kDecWSteps;
+  constexpr int kWPre = MX ? kWLoads : W8 ? kWLoads / 2 : kDecWPre;
 #pragma unroll
   for (int s = 0; s < kWPre; ++s) load_w(s);
   // nothing below is hoisted between these loads (it would wait for the
@@ -238,7 +253,8 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
   for (int tb = 0; tb < NTB; ++tb) acc[tb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < kDecWSteps; ++s) {
-    if constexpr (W8) {
+    if constexpr (MX) {   // (all requested)
+    } else if constexpr (W8) {
       if ((s & 1) == 0 && s / 2 + kWPre < kWLoads) load_w(s / 2 + kWPre);
     } else {
       if (s + kDecWPre < kDecWSteps) load_w(s + kDecWPre);
@@ -247,7 +263,13 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
     // the LDS chunk are clamped onto such columns
     int xc;
     u32x4_t wop;
-    if constexpr (W8) {
+    if constexpr (MX) {
+      const int kp = min(ks_begin + (s & ~3), kDecMaxKc / 32 - 4);   // the group's first step
+      xc = kp * 32 + 4 * kq + 8 * (s & 3);
+      // (a block past the chunk is the chunk's last, against zero x)
+      const int blk = min(kp * 32 + 4 * kq, kc - 32) / kMxBlock;
+      wop = mx_bf16x8(wr[s / 4][s & 3], mx_scale_at(ws[s / 4], blk & 3));
+    } else if constexpr (W8) {
       const int kp = min(ks_begin + (s & ~1), kDecMaxKc / 32 - 2);   // the step pair's first step
       xc = kp * 32 + 2 * kq + 8 * (s & 1);
       const u32x4_t raw = wr[s / 2];
@@ -351,8 +373,9 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kWideWaves = 8;
 
-template <bool W8, bool GATED>
+template <int WQ, bool GATED>
 __global__ __launch_bounds__(kWideWaves * kWave) void k_stream_wide(DecodeArgs a, int n_units) {
+  constexpr int TYPE = WQ == kWMx ? kXMx : WQ == kWFp8 ? kXFp8w : kXBf16;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int l16 = lane % 16, g = lane / 16;
   const int T = a.T, d_in = a.d_in, d_out = a.d_out;
@@ -391,17 +414,26 @@ __global__ __launch_bounds__(kWideWaves * kWave) void k_stream_wide(DecodeArgs a
     return;
   }
   __shared__ f32x4_t red[kWideWaves][2][kWave];
-  constexpr int EB = W8 ? 1 : 2;
+  const long long wrb = w_row_bytes<TYPE>(d_in);
   const int v0 = 32 * (b - n_units);
-  const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out;
-  const char* wbase = (const char*)a.W + (long long)min(f0, nf - 1) * d_in * EB;
-  uint32_t wo[GATED ? 1 : 2];
+  const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out, fb = min(f0, nf - 1);
+  constexpr int NO = GATED ? 1 : 2;
+  const char* wbase = (const char*)a.W + fb * wrb;
+  uint32_t wo[NO], so[NO];
 #pragma unroll
-  for (int r = 0; r < (GATED ? 1 : 2); ++r)
-    wo[r] = (uint32_t)max(min(16 * r + l16, nf - 1 - f0), 0) * (uint32_t)(d_in * EB) + 16 * g;
-  const char* xp[1] = {xrow + (W8 ? 32 : 16) * g};
+  for (int r = 0; r < NO; ++r) {
+    const uint32_t f = (uint32_t)max(min(16 * r + l16, nf - 1 - f0), 0);
+    wo[r] = f * (uint32_t)wrb + 16 * g;
+    so[r] = 4 * f;
+  }
+  const char* xp[1] = {xrow + x_group_bytes<TYPE>() * g};
   f32x4_t acc[2][1];
-  stream_product<W8 ? kXFp8w : kXBf16, 2, 1, kWideWaves, GATED>(wbase, (long long)nf * d_in * EB, wo, xp, d_in, wave, g, acc);
+  if constexpr (TYPE == kXMx) {
+    const MxScales ms{(const char*)a.w_mx + 4ll * fb, 4ll * nf, 4ll * d_out, 0};
+    stream_product_mx<TYPE, 2, 1, kWideWaves, GATED>(wbase, nf * wrb, wo, xp, ms, so, nullptr, d_in, wave, g, acc);
+  } else {
+    stream_product<TYPE, 2, 1, kWideWaves, GATED>(wbase, nf * wrb, wo, xp, d_in, wave, g, acc);
+  }
   red[wave][0][lane] = acc[0][0];
   red[wave][1][lane] = acc[1][0];
   __syncthreads();
@@ -710,14 +742,14 @@ int decode_unit_rows(int n_seg_bound, int max_rank, int n_tiles) {
   return 16;
 }
 
-// d_in chunk: a multiple of 64 (at most the LDS x chunk), small enough that
+// d_in chunk: a multiple of `unit` (at most the LDS x chunk), small enough that
 // n_tiles * n_chunks covers the 256 CUs.
-void decode_plan(int d_in, int d_out, int* n_tiles, int* kc, int* n_chunks) {
+void decode_plan(int d_in, int d_out, int* n_tiles, int* kc, int* n_chunks, int unit) {
   *n_tiles = (d_out + kDecRows - 1) / kDecRows;
   int chunks = (d_in + kDecMaxKc - 1) / kDecMaxKc;
   while (*n_tiles * chunks < 256 && d_in / (chunks + 1) >= 256) ++chunks;
   int k = (d_in + chunks - 1) / chunks;
-  k = (k + 63) / 64 * 64;
+  k = (k + unit - 1) / unit * unit;
   if (k > kDecMaxKc) k = kDecMaxKc;
   *kc = k;
   *n_chunks = (d_in + k - 1) / k;
@@ -730,48 +762,54 @@ void decode_plan(int d_in, int d_out, int* n_tiles, int* kc, int* n_chunks) {
 // 22.0 against 19.0.
 constexpr int kWideTiles = 256, kWideTokens = 8;
 
-template <int TT, bool W8, int EPI>
+template <int TT, int WQ, int EPI>
 static void launch_decode_epi(DecodeArgs a, hipStream_t st) {
   constexpr bool GATED = EPI == kEpiGated;
   const dim3 items(a.n_tiles * a.n_chunks);
   if constexpr (EPI == kEpiNone) {
-    hipLaunchKernelGGL((k_stream_bf16<TT, W8, false, true>), items, dim3(kDecThreads), 0, st, a);
+    hipLaunchKernelGGL((k_stream_bf16<TT, WQ, false, true>), items, dim3(kDecThreads), 0, st, a);
   } else {
     bool done = false;
     if constexpr (TT == 16) {
       if (a.T <= kWideTokens && a.n_tiles >= kWideTiles) {
         a.n_chunks = 1;   // what k_finish adds up
         const int units = a.lora_on ? a.sv.n_seg * ((a.pv.max_rank + 15) / 16) : 0;
-        hipLaunchKernelGGL((k_stream_wide<W8, GATED>), dim3(units + 2 * a.n_tiles), dim3(kWideWaves * kWave), 0, st, a, units);
+        hipLaunchKernelGGL((k_stream_wide<WQ, GATED>), dim3(units + 2 * a.n_tiles), dim3(kWideWaves * kWave), 0, st, a, units);
         done = true;
       }
     }
     if constexpr (TT == 64) {
       if (a.d_in > 8192) {
-        hipLaunchKernelGGL((k_stream_bf16<TT, W8, GATED, true>), items, dim3(kDecThreads), 0, st, a);
+        hipLaunchKernelGGL((k_stream_bf16<TT, WQ, GATED, true>), items, dim3(kDecThreads), 0, st, a);
         done = true;
       }
     }
-    if (!done) hipLaunchKernelGGL((k_stream_bf16<TT, W8, GATED, false>), items, dim3(kDecThreads), 0, st, a);
+    if (!done) hipLaunchKernelGGL((k_stream_bf16<TT, WQ, GATED, false>), items, dim3(kDecThreads), 0, st, a);
   }
   if (a.lora_on && a.pv.n_slices > 0)
-    hipLaunchKernelGGL((k_finish_bf16<TT, W8, true, EPI>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_finish_bf16<TT, WQ == kWFp8, true, EPI>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((k_finish_bf16<TT, W8, false, EPI>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_finish_bf16<TT, WQ == kWFp8, false, EPI>), dim3(a.n_tiles * (TT / 16)), dim3(256), 0, st, a);
 }
 
-template <int TT, bool W8>
+template <int TT, int WQ>
 static void launch_decode_tt(const DecodeArgs& a, hipStream_t st) {
-  if (a.epi_kind == kEpiGated) launch_decode_epi<TT, W8, kEpiGated>(a, st);
-  else if (a.epi_kind == kEpiPlain) launch_decode_epi<TT, W8, kEpiPlain>(a, st);
-  else launch_decode_epi<TT, W8, kEpiNone>(a, st);
+  if (a.epi_kind == kEpiGated) launch_decode_epi<TT, WQ, kEpiGated>(a, st);
+  else if (a.epi_kind == kEpiPlain) launch_decode_epi<TT, WQ, kEpiPlain>(a, st);
+  else launch_decode_epi<TT, WQ, kEpiNone>(a, st);
+}
+
+template <int TT>
+static void launch_decode_wq(const DecodeArgs& a, hipStream_t st) {
+  if (a.w_mx) launch_decode_tt<TT, kWMx>(a, st);
+  else if (a.w_scale) launch_decode_tt<TT, kWFp8>(a, st);
+  else launch_decode_tt<TT, kWBf16>(a, st);
 }
 
 void launch_decode_bf16(const DecodeArgs& a, hipStream_t st) {
-  const bool w8 = a.w_scale != nullptr;
-  if (a.T <= 16) w8 ? launch_decode_tt<16, true>(a, st) : launch_decode_tt<16, false>(a, st);
-  else if (a.T <= 32) w8 ? launch_decode_tt<32, true>(a, st) : launch_decode_tt<32, false>(a, st);
-  else w8 ? launch_decode_tt<64, true>(a, st) : launch_decode_tt<64, false>(a, st);
+  if (a.T <= 16) launch_decode_wq<16>(a, st);
+  else if (a.T <= 32) launch_decode_wq<32>(a, st);
+  else launch_decode_wq<64>(a, st);
 }
 
 }  // namespace mlora

@@ -34,10 +34,6 @@ constexpr int kGridY = 32768;   // runs per grid row (y is limited; z takes the 
 
 template <int TYPE, int NR, int NTB, int NW, bool GATED>
 __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
-  constexpr int EB = TYPE == kXFp8w ? 1 : TYPE == kXF32 ? 4 : 2;   // bytes per W element
-  constexpr int XB = TYPE == kXF32 ? 4 : 2;                        // and per x element
-  constexpr int UC = 128 / EB;                                     // columns per unit
-  constexpr int XL = XB / EB;                                      // x loads per W load
   __shared__ f32x4_t red[NW][NR * NTB][kWave];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int l16 = lane % 16, g = lane / 16;
@@ -53,21 +49,32 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
   // W: a uniform base and 32-bit offsets; rows past the last are clamped to it
   constexpr int NO = GATED ? NR / 2 : NR;                          // distinct row blocks
   const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out;
-  const char* wbase = (const char*)a.W + ((long long)e * d_out + f0) * d_in * EB;
-  const long long up = (long long)nf * d_in * EB;                  // gated: from a gate row to its up row
+  const long long wrb = w_row_bytes<TYPE>(d_in), xrb = x_row_bytes<TYPE>(d_in);
+  const char* wbase = (const char*)a.W + ((long long)e * d_out + f0) * wrb;
+  const long long up = nf * wrb;                                   // gated: from a gate row to its up row
   uint32_t wo[NO];
 #pragma unroll
-  for (int r = 0; r < NO; ++r) wo[r] = (uint32_t)min(16 * r + l16, nf - 1 - f0) * (uint32_t)(d_in * EB) + 16 * g;
+  for (int r = 0; r < NO; ++r) wo[r] = (uint32_t)min(16 * r + l16, nf - 1 - f0) * (uint32_t)wrb + 16 * g;
   const char* xp[NTB];
+  const char* xsp[NTB];                                            // (kXMxX: the rows' scales)
 #pragma unroll
   for (int t = 0; t < NTB; ++t) {
     const int p = min(p0 + 16 * t + l16, p1 - 1);                  // (absent positions repeat the last)
-    const int row = a.token_index ? a.token_index[p] : p;
-    xp[t] = (const char*)a.x + (long long)min(max(row, 0), a.n_rows - 1) * d_in * XB + 16 * XL * g;
+    const int row = min(max(a.token_index ? a.token_index[p] : p, 0), a.n_rows - 1);
+    xp[t] = (const char*)a.x + row * xrb + x_group_bytes<TYPE>() * g;
+    xsp[t] = (const char*)a.x_mx + 4ll * row;
   }
 
   f32x4_t acc[NR][NTB];
-  stream_product<TYPE, NR, NTB, NW, GATED>(wbase, up, wo, xp, d_in, wave, g, acc);
+  if constexpr (TYPE >= kXMx) {
+    uint32_t so[NO];
+#pragma unroll
+    for (int r = 0; r < NO; ++r) so[r] = 4u * (uint32_t)min(16 * r + l16, nf - 1 - f0);
+    const MxScales ms{(const char*)a.w_mx + 4 * ((long long)e * mx_planes(d_in) * d_out + f0), 4ll * nf, 4ll * d_out, 4ll * a.n_rows};
+    stream_product_mx<TYPE, NR, NTB, NW, GATED>(wbase, up, wo, xp, ms, so, xsp, d_in, wave, g, acc);
+  } else {
+    stream_product<TYPE, NR, NTB, NW, GATED>(wbase, up, wo, xp, d_in, wave, g, acc);
+  }
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -182,11 +189,12 @@ __device__ __forceinline__ int xcd_tile(const ExpertsArgs& a, const RunScan& fir
 template <class C, int OUT, bool PIPE>
 __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0, int p1, int r0, char* lds) {
   constexpr bool GATED = OUT == 1;
-  constexpr int WB = C::kW8 ? 1 : 2;                     // bytes per W element
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int d_in = a.d_in, d_out = a.d_out;
-  const char* __restrict__ W = (const char*)a.W + (long long)e * d_out * d_in * WB;
-  const uint16_t* __restrict__ x = (const uint16_t*)a.x;
+  // bytes of a row of W and of x
+  const long long wrb = C::kWQ >= kWMx ? d_in / 2 : C::kW8 ? d_in : 2ll * d_in, xrb = C::kWQ == kWMxX ? d_in / 2 : 2ll * d_in;
+  const char* __restrict__ W = (const char*)a.W + e * (d_out * wrb);
+  const char* __restrict__ x = (const char*)a.x;
   auto row_of = [&](int r) {
     const int p = min(p0 + r, p1 - 1);                   // (absent positions repeat the last)
     const int row = a.token_index ? a.token_index[p] : p;
@@ -210,8 +218,12 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0,
     pipe_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
   } else {
     TileSrc<C> src;
-    src.set(wave, lane, [&](int r) { return W + (long long)wrow_of<GATED>(r0 + r, d_out) * d_in * WB; },
-            [&](int r) { return x + (long long)row_of(r) * d_in; });
+    src.set(wave, lane, [&](int r) { return W + wrow_of<GATED>(r0 + r, d_out) * wrb; }, [&](int r) { return x + row_of(r) * xrb; });
+    if constexpr (C::kWQ >= kWMx) {
+      const uint8_t* ws = a.w_mx + 4ll * e * mx_planes(d_in) * d_out;
+      src.set_scales(wave, lane, 4ll * d_out, 4ll * a.n_rows, [&](int r) { return ws + 4ll * wrow_of<GATED>(r0 + r, d_out); },
+                     [&](int r) { return a.x_mx + 4ll * row_of(r); });
+    }
     ring_mainloop<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
   }
 
@@ -403,9 +415,14 @@ static void launch_tile256(const ExpertsArgs& a, hipStream_t st) {
   else hipLaunchKernelGGL(k_experts_tile256<0>, grid, block, 0, st, a, n_rt, max_runs);
 }
 
-template <bool W8> using Tile128 = GCfg<128, 128, 64, 32, 3, W8 ? 128 : 64, W8 ? 2 : 3, W8>;
-template <bool W8> using Tile64 = GCfg<128, 64, 32, 32, 4, W8 ? 128 : 64, 4, W8>;
+template <bool W8> using Tile128 = GCfg<128, 128, 64, 32, 3, W8 ? 128 : 64, W8 ? 2 : 3, W8 ? kWFp8 : kWBf16>;
+template <bool W8> using Tile64 = GCfg<128, 64, 32, 32, 4, W8 ? 128 : 64, 4, W8 ? kWFp8 : kWBf16>;
 typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
+// MXFP4: W alone, and the rows of x too
+template <bool XMX> using Mx32 = GCfg<128, 32, 32, 32, 4, XMX ? 256 : 128, 4, XMX ? kWMxX : kWMx>;
+template <bool XMX> using Mx64 = GCfg<128, 64, 32, 32, 4, XMX ? 256 : 128, 4, XMX ? kWMxX : kWMx>;
+template <bool XMX> using Mx128 = GCfg<128, 128, 64, 32, 3, XMX ? 256 : 128, 3, XMX ? kWMxX : kWMx>;
+template <bool XMX> using Mx256 = GCfg<256, 256, 128, 64, XMX ? 2 : 3, XMX ? 256 : 64, XMX ? 2 : 3, XMX ? kWMxX : kWMx>;
 
 // Form by the rows per expert. Up to two (FP8: twenty), the streaming form; it
 // also takes fp32 and what has too few tiles for the card: fewer than 256 of 32
@@ -442,9 +459,25 @@ static void launch_bf16(const ExpertsArgs& a, hipStream_t st) {
   else launch_tile<Tile128<W8>>(a, st);
 }
 
+template <bool XMX>
+static void launch_mx(const ExpertsArgs& a, hipStream_t st) {
+  const long long active = std::min(a.E, a.n_pos);
+  const double mean = (double)a.n_pos / active;
+  const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  const long long tiles256 = (rows + 255) / 256 * (a.n_pos / 256 + active / 2);
+  const int bt = mean <= 8 ? 32 : mean <= 48 ? 64 : 128;
+  const long long tiles = (rows + 127) / 128 * std::max(active, a.n_pos / bt + active / 2);
+  if (mean <= 2 || tiles < (mean <= 8 ? 256 : 64)) launch_stream<XMX ? kXMxX : kXMx>(a, st);
+  else if (mean <= 8) launch_tile<Mx32<XMX>>(a, st);
+  else if (mean >= 192 || (mean >= 112 && tiles256 >= 1024)) launch_tile<Mx256<XMX>>(a, st);
+  else if (mean <= 48) launch_tile<Mx64<XMX>>(a, st);
+  else launch_tile<Mx128<XMX>>(a, st);
+}
+
 void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st) {
   if (a.n_pos <= 0) return;
   if (!bf16) launch_stream<kXF32>(a, st);
+  else if (a.w_mx) a.x_mx ? launch_mx<true>(a, st) : launch_mx<false>(a, st);
   else if (a.w_scale) launch_bf16<true>(a, st);
   else launch_bf16<false>(a, st);
 }

@@ -674,22 +674,24 @@ constexpr int kEpiMaxUnits = 128;   // work units one wave lists per rank chunk 
 // wave per SIMD for 4 waves, two for 8).
 // EPI: kEpiNone stores the layer's result; kEpiPlain and kEpiGated apply
 // a.epi to it first (epilogue.h; gated: the tile's rows are virtual rows).
-template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, int EPI>
+// WQ: kWBf16, or an MXFP4 weight (kWMx, kWMxX: gemm_tile.h).
+template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, int EPI, int WQ>
 __global__ __launch_bounds__((BR / WR) * (BT / WT) * kWave)
 __attribute__((amdgpu_waves_per_eu((BR / WR) * (BT / WT) / 4, (BR / WR) * (BT / WT) / 4)))
 void k_gemm2(LinearArgs a) {
   constexpr bool GATED = EPI == kEpiGated;
   constexpr bool PIPE = BR == 256 && (BR / WR) * (BT / WT) == 4;   // (one wave per SIMD)
-  using C = GCfg<BR, BT, WR, WT, NB, KB, NX>;
+  using C = GCfg<BR, BT, WR, WT, NB, KB, NX, WQ>;
   // the rings, then what the expand lists: the tile's position entries, each
   // wave's work units of a rank chunk and run starts. PIPE: the rings take all of
   // the LDS, and the lists lie in it behind the staged v.
   constexpr int WRUNS = WT + 1;
   constexpr int UDESC_AT = BT * 16, WSTART_AT = UDESC_AT + C::NW * kEpiMaxUnits * 16;
   constexpr int LIST_BYTES = WSTART_AT + (C::NW * WRUNS * 4 + 15) / 16 * 16;
-  constexpr int LIST_AT = PIPE ? 96 * 1024 : C::LDS_BYTES;
-  static_assert(!PIPE || (LIST_AT + LIST_BYTES <= C::LDS_BYTES && BT * (64 + 8) * 4 <= LIST_AT), "v and the lists fit the LDS");
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[(C::LDS_BYTES + (PIPE ? 0 : LIST_BYTES)) / 2];
+  constexpr bool INRING = PIPE || C::LDS_BYTES + LIST_BYTES > 160 * 1024;   // (MXFP4 on both sides: all of it too)
+  constexpr int LIST_AT = INRING ? 96 * 1024 : C::LDS_BYTES;
+  static_assert(!INRING || (LIST_AT + LIST_BYTES <= C::LDS_BYTES && BT * (64 + 8) * 4 <= LIST_AT), "v and the lists fit the LDS");
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[(C::LDS_BYTES + (INRING ? 0 : LIST_BYTES)) / 2];
   int4* pinfo = (int4*)((char*)lds + LIST_AT);
 
   // wave index made scalar: every per-wave quantity below is then uniform
@@ -747,6 +749,20 @@ void k_gemm2(LinearArgs a) {
               return (uint32_t)min(max(row, 0), T - 1) * (uint32_t)(2 * d_in);
             });
     pipe_mainloop<C>(src, d_in, zeros, (char*)lds, wave, lane, acc);
+  } else if constexpr (WQ >= kWMx) {   // MXFP4: the ring of gemm_tile.h
+    auto row_of = [&](int r) {
+      const int p = min(t0 + r, T - 1);
+      const int row = a.sv.token_index ? a.sv.token_index[p] : p;
+      return (long long)min(max(row, 0), T - 1);
+    };
+    const char* xq = WQ == kWMxX ? (const char*)a.x_codes : (const char*)a.x;
+    const long long wrb = d_in / 2, xrb = WQ == kWMxX ? d_in / 2 : 2ll * d_in;
+    TileSrc<C> src;
+    src.set(wave, lane, [&](int r) { return (const char*)a.W + wrow_of<GATED>(r0 + r, d_out) * wrb; },
+            [&](int r) { return xq + row_of(r) * xrb; });
+    src.set_scales(wave, lane, 4ll * d_out, 4ll * T, [&](int r) { return a.w_mx + 4ll * wrow_of<GATED>(r0 + r, d_out); },
+                   [&](int r) { return a.x_mx + 4 * row_of(r); });
+    ring_mainloop<C>(src, d_in, zeros, (char*)lds, wave, lane, acc);
   } else {
   // loader: load i < DPW_W of wave w fills the W slot's 1 KB chunk
   // J = i NW + w, load DPW_W + i the position slot's chunk J; lane l writes
@@ -1249,7 +1265,7 @@ int shrink_items_bound(int T, int n_seg_bound, int max_rank) {
 // projection at the verify batch (448 128x128 tiles over 28672 rows), where
 // row tiles fastest left most row tiles' two position tiles in different
 // rounds and read W twice.
-template <int BR, int BT, int WR, int WT, int NB, int KB, int NX>
+template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, int WQ = kWBf16>
 static void launch_g(const LinearArgs& a, hipStream_t st, bool grouped_order) {
   const int n_rt = ((a.epi_kind == kEpiGated ? gated_rows(a.d_out) : a.d_out) + BR - 1) / BR;
   const int n_tt = (a.T + BT - 1) / BT;
@@ -1257,18 +1273,18 @@ static void launch_g(const LinearArgs& a, hipStream_t st, bool grouped_order) {
   g.gorder = grouped_order && n_tt > 1 && n_rt % 8 == 0 && (long long)n_rt * n_tt > 256;
   if (BR == 256 && n_rt % 4 == 0 && n_tt % 2 == 0 && (long long)n_rt * n_tt <= 256) g.gorder = 2;
   g.wnt = n_tt <= 2;
-  const dim3 grid(n_rt * n_tt), block(GCfg<BR, BT, WR, WT, NB, KB, NX>::NT);
+  const dim3 grid(n_rt * n_tt), block(GCfg<BR, BT, WR, WT, NB, KB, NX, WQ>::NT);
   // (of the 256 x 256 tiles, the 8-wave one runs without an epilogue, the 4-wave one with)
-  constexpr bool kWithEpi = BR < 256 || WT == 128, kWithout = BR < 256 || WT < 128;
+  constexpr bool kWithEpi = WQ != kWBf16 || BR < 256 || WT == 128, kWithout = WQ != kWBf16 || BR < 256 || WT < 128;
   if constexpr (kWithEpi) {
     if (a.epi_kind == kEpiGated)
-      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiGated>), grid, block, 0, st, g);
+      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiGated, WQ>), grid, block, 0, st, g);
     else if (a.epi_kind == kEpiPlain)
-      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiPlain>), grid, block, 0, st, g);
+      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiPlain, WQ>), grid, block, 0, st, g);
   }
   if constexpr (kWithout) {
     if (a.epi_kind == kEpiNone)
-      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiNone>), grid, block, 0, st, g);
+      hipLaunchKernelGGL((k_gemm2<BR, BT, WR, WT, NB, KB, NX, kEpiNone, WQ>), grid, block, 0, st, g);
   }
 }
 
@@ -1349,6 +1365,18 @@ void launch_linear_bf16(const LinearArgs& a, hipStream_t st) {
   // loop of gemm_tile.h, which addresses x and its rows of W by 32-bit offsets
   // (past them: 128x128 tiles).
   const bool large = a.T > 128 && tiles(256, 256) >= kFill, epi = a.epi_kind != kEpiNone;
+  if (a.w_mx && a.x_mx) {
+    if (large) launch_g<256, 256, 128, 64, 2, 256, 2, kWMxX>(a, st, true);
+    else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 256, 3, kWMxX>(a, st, true);
+    else launch_g<64, 128, 32, 32, 4, 256, 3, kWMxX>(a, st, true);
+    return;
+  }
+  if (a.w_mx) {
+    if (large) launch_g<256, 256, 128, 64, 3, 64, 3, kWMx>(a, st, true);
+    else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 128, 3, kWMx>(a, st, true);
+    else launch_g<64, 128, 32, 64, 4, 128, 3, kWMx>(a, st, true);
+    return;
+  }
   const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
                     (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
   if (large && epi && near) launch_g<256, 256, 128, 128, 3, 64, 2>(a, st, true);

@@ -175,6 +175,110 @@ __device__ __forceinline__ void choose4(const RouteArgs& a, int t, bool there, i
   *w = my_id >= 0 ? mine / sum : 0.f;
 }
 
+// Choice of one token by one wave by scores (mlora_route_scored). The scores decide
+// which of two near experts is chosen, so their rounding is part of the result: they
+// are computed in 64 bits and rounded once to fp32, where the bias is added (one
+// rounding) and a group's two best are (another). `key_lds`: E words of the wave's own.
+// Lane g holds group g: at most 64 groups.
+template <typename E_, int NV>
+__device__ __forceinline__ void choose_scored(const RouteArgs& a, int t, int lane, uint32_t* key_lds, int* id, float* w) {
+  const E_* __restrict__ row = (const E_*)a.logits + (long long)t * a.E;
+  float l[NV], s[NV];
+  uint32_t key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + kWave * i;
+    l[i] = elem_f32<E_>(row, min(e, a.E - 1));
+    if (e >= a.E || !(l[i] > -INFINITY)) l[i] = -INFINITY;   // (NaN: as -inf)
+  }
+  if (a.sigmoid) {   // uniform
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] = (float)(1.0 / (1.0 + exp(-(double)l[i])));
+  } else {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+    double p[NV], sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      p[i] = !(l[i] > -INFINITY) ? 0.0 : l[i] == m ? 1.0 : exp((double)l[i] - (double)m);
+      sum += p[i];
+    }
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) sum += __shfl_xor(sum, off, kWave);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] = (float)(p[i] / sum);   // (a row of no expert: NaN, chosen by none)
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + kWave * i;
+    const float c = a.bias ? s[i] + a.bias[min(e, a.E - 1)] : s[i];
+    key[i] = l[i] > -INFINITY ? logit_key(c) : 0u;
+  }
+  if (a.groups > 1) {   // uniform
+    const int per = a.E / a.groups;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane + kWave * i < a.E) key_lds[lane + kWave * i] = key[i];
+    // (the wave's own LDS writes are ordered before its reads)
+    uint32_t k1 = 0u, k2 = 0u;
+    if (lane < a.groups) {
+      for (int j = 0; j < per; ++j) {
+        const uint32_t k = key_lds[lane * per + j];
+        k2 = max(k2, min(k1, k));
+        k1 = max(k1, k);
+      }
+    }
+    // (a group with an expert is above none, whatever its sum)
+    uint32_t gk = k1 == 0u ? 0u : max(1u, logit_key(k2 == 0u ? key_logit(k1) : key_logit(k1) + key_logit(k2)));
+    unsigned long long kept = 0ull;
+    for (int j = 0; j < a.top_groups; ++j) {
+      const uint32_t m = wave_max(gk);
+      if (m == 0u) break;   // uniform
+      const int win = (int)__builtin_ctzll(__ballot(gk == m));
+      kept |= 1ull << win;
+      if (lane == win) gk = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (!((kept >> (min(lane + kWave * i, a.E - 1) / per)) & 1ull)) key[i] = 0u;
+  }
+  int my_id = -1;
+  float mine = 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
+    const uint32_t m = wave_max(best);                 // uniform
+    if (m == 0u) break;                                // nothing left to choose
+    int win = -1;                                      // uniform
+#pragma unroll
+    for (int i = NV - 1; i >= 0; --i) {
+      const unsigned long long h = __ballot(key[i] == m);
+      if (h) win = kWave * i + (int)__builtin_ctzll(h);
+    }
+    float sw = s[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) sw = win / kWave == i ? s[i] : sw;
+    sw = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sw), win % kWave));
+    if (lane == j) {
+      my_id = win;
+      mine = sw;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (win == lane + kWave * i) key[i] = 0u;
+  }
+  if (a.renorm) {   // uniform
+    const float sum = wave_sum(mine);
+    mine = sum > 0.f ? mine / sum : 0.f;
+  }
+  *id = my_id;
+  *w = a.scale * mine;
+}
+
 // LDS of the grouping: counts per wave [kRtWaves][E], then per expert [E + 1],
 // then, in the one-launch form, the choices [T k].
 __host__ __device__ inline size_t route_lds_bytes(int E) { return ((size_t)(kRtWaves + 1) * E + 1) * 4; }
@@ -250,9 +354,12 @@ __device__ __forceinline__ int scan_experts(int* n, int E) {
 
 // The choice for a block of a.tpb tokens; the block's slots per expert are
 // left in LDS (base), and its choices where `ids` is given.
-// QUAD: four tokens per wave (choose4), else one (choose1).
-template <typename E_, int NV, bool QUAD>
-__device__ __forceinline__ void choose_block(const RouteArgs& a, int* base, int* ids) {
+// FORM: four tokens per wave (choose4), one (choose1), or one by scores
+// (choose_scored, with `keys`: E words per wave).
+constexpr int kRtOne = 0, kRtQuad = 1, kRtScored = 2;
+template <typename E_, int NV, int FORM>
+__device__ __forceinline__ void choose_block(const RouteArgs& a, int* base, int* ids, int* keys) {
+  constexpr bool QUAD = FORM == kRtQuad;
   constexpr int TPW = QUAD ? 4 : 1;                      // tokens of a wave at a time
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, waves = blockDim.x / kWave;
   for (int i = tid; i < a.E; i += blockDim.x) base[i] = 0;
@@ -264,6 +371,7 @@ __device__ __forceinline__ void choose_block(const RouteArgs& a, int* base, int*
     int id;
     float w;
     if constexpr (QUAD) choose4<E_, NV>(a, min(t, t1 - 1), t < t1, l, &id, &w);
+    else if constexpr (FORM == kRtScored) choose_scored<E_, NV>(a, t, l, (uint32_t*)keys + wave * a.E, &id, &w);
     else choose1<E_, NV>(a, t, l, &id, &w);
     if (t < t1 && l < a.k) {
       a.expert[(long long)t * a.k + l] = id;
@@ -276,13 +384,13 @@ __device__ __forceinline__ void choose_block(const RouteArgs& a, int* base, int*
 }
 
 // One workgroup holds the batch: choice and grouping in one launch.
-template <typename E_, int NV, bool QUAD>
+template <typename E_, int NV, int FORM>
 __global__ __launch_bounds__(kRtThreads) void k_route_one(RouteArgs a) {
   extern __shared__ int sm[];
   int* cnt = sm;
   int* base = sm + kRtWaves * a.E;
   int* ids = base + a.E + 1;
-  choose_block<E_, NV, QUAD>(a, base, ids);
+  choose_block<E_, NV, FORM>(a, base, ids, cnt);   // (the counts come later)
   const int total = scan_experts(base, a.E);
   const int tid = threadIdx.x, P = a.T * a.k;
   for (int e = tid; e <= a.E; e += kRtThreads) a.seg_start[e] = e < a.E ? base[e] : total;
@@ -293,10 +401,10 @@ __global__ __launch_bounds__(kRtThreads) void k_route_one(RouteArgs a) {
 
 constexpr int kRcThreads = 512;
 
-template <typename E_, int NV, bool QUAD>
+template <typename E_, int NV, int FORM>
 __global__ __launch_bounds__(kRcThreads) void k_route_choose(RouteArgs a) {
   extern __shared__ int sm[];
-  choose_block<E_, NV, QUAD>(a, sm, nullptr);
+  choose_block<E_, NV, FORM>(a, sm, nullptr, sm + a.E);
   for (int e = threadIdx.x; e < a.E; e += kRcThreads) a.hist[(long long)blockIdx.x * a.E + e] = sm[e];
 }
 
@@ -366,26 +474,31 @@ size_t route_workspace_bytes(int T, int E) {
 // them at 4096 tokens, hardly less at a few).
 constexpr int kRtOneTokens = 128;
 
-template <typename E_, int NV, bool QUAD>
+template <typename E_, int NV, int FORM>
 static void launch_route_nv(RouteArgs a, hipStream_t st) {
   const size_t lds = route_lds_bytes(a.E);
   if (a.T <= kRtOneTokens) {
     a.tpb = a.T;
-    hipLaunchKernelGGL((k_route_one<E_, NV, QUAD>), dim3(1), dim3(kRtThreads), lds + (size_t)a.T * a.k * 4, st, a);
+    hipLaunchKernelGGL((k_route_one<E_, NV, FORM>), dim3(1), dim3(kRtThreads), lds + (size_t)a.T * a.k * 4, st, a);
     return;
   }
   a.tpb = route_tokens_per_block(a.T);
   const dim3 grid((a.T + a.tpb - 1) / a.tpb);
-  hipLaunchKernelGGL((k_route_choose<E_, NV, QUAD>), grid, dim3(kRcThreads), (size_t)a.E * 4, st, a);
+  hipLaunchKernelGGL((k_route_choose<E_, NV, FORM>), grid, dim3(kRcThreads),
+                     (size_t)a.E * 4 * (FORM == kRtScored ? 1 + kRcThreads / kWave : 1), st, a);
   hipLaunchKernelGGL(k_route_group, grid, dim3(kRtThreads), lds, st, a);
 }
 
 template <typename E_>
 static void launch_route_t(const RouteArgs& a, hipStream_t st) {
-  if (a.E > 256 || a.k > 16) launch_route_nv<E_, MLORA_MAX_EXPERTS / kWave, false>(a, st);
-  else if (a.E <= 64) launch_route_nv<E_, 4, true>(a, st);
-  else if (a.E <= 128) launch_route_nv<E_, 8, true>(a, st);
-  else launch_route_nv<E_, 16, true>(a, st);
+  if (a.scored) {
+    if (a.E <= 64) launch_route_nv<E_, 1, kRtScored>(a, st);
+    else if (a.E <= 256) launch_route_nv<E_, 4, kRtScored>(a, st);
+    else launch_route_nv<E_, MLORA_MAX_EXPERTS / kWave, kRtScored>(a, st);
+  } else if (a.E > 256 || a.k > 16) launch_route_nv<E_, MLORA_MAX_EXPERTS / kWave, kRtOne>(a, st);
+  else if (a.E <= 64) launch_route_nv<E_, 4, kRtQuad>(a, st);
+  else if (a.E <= 128) launch_route_nv<E_, 8, kRtQuad>(a, st);
+  else launch_route_nv<E_, 16, kRtQuad>(a, st);
 }
 
 void launch_route(const RouteArgs& a, bool bf16, hipStream_t st) {

@@ -33,6 +33,11 @@ struct LinearArgs {
   // what follows the layer: kEpiNone (nothing; epi is not read), kEpiPlain or kEpiGated
   int epi_kind;
   EpiView epi;
+  // MXFP4 (mxfp4.h): W holds codes, w_mx their scales; with x_mx the base product takes
+  // x_codes [T, d_in / 2] in x's place (the adapter term always reads x). Null: not.
+  const uint8_t* w_mx = nullptr;
+  const uint8_t* x_codes = nullptr;
+  const uint8_t* x_mx = nullptr;
 };
 
 constexpr int kEpiNone = 0, kEpiPlain = 1, kEpiGated = 2;
@@ -63,7 +68,8 @@ struct DecodeArgs {
   int kc;          // d_in chunk width (multiple of 64)
   int n_chunks;    // ceil(d_in / kc)
   int unit_rows;   // rank rows per shrink unit (4, 8 or 16)
-  const float* w_scale;   // FP8 weight: float32 scale per W row (W holds e4m3 codes); null: bf16 W
+  const float* w_scale;   // FP8 weight: float32 scale per W row (W holds e4m3 codes); null: not
+  const uint8_t* w_mx;    // MXFP4 weight: its scales (W holds codes); null: not
   int epi_kind;           // as in LinearArgs
   EpiView epi;
 };
@@ -112,7 +118,8 @@ bool shrink_short(const LinearArgs& a);
 // decode path (kernels_decode.hip)
 bool decode_supported(int T, int n_seg_bound, int d_out, int max_rank);
 int decode_unit_rows(int n_seg_bound, int max_rank, int n_tiles);
-void decode_plan(int d_in, int d_out, int* n_tiles, int* kc, int* n_chunks);
+// (unit: what the d_in chunks are multiples of; MXFP4 weights take 128, a plane of scales)
+void decode_plan(int d_in, int d_out, int* n_tiles, int* kc, int* n_chunks, int unit = 64);
 void launch_decode_bf16(const DecodeArgs& a, hipStream_t st);
 
 // fp32 path (kernels_f32.hip)

@@ -5,7 +5,10 @@
 // register v of lane l is row 4 (l / 16) + v, column l % 16. Rows are W rows,
 // columns tokens.
 #pragma once
+#include <type_traits>
+
 #include "common.h"
+#include "mxfp4.h"
 
 namespace mlora {
 
@@ -13,7 +16,21 @@ __device__ __forceinline__ f32x4_t mfma16e(u32x4_t a, u32x4_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-constexpr int kXBf16 = 0, kXFp8w = 1, kXF32 = 2;   // element types: bf16, bf16 with an FP8 W, fp32
+// element types: bf16, bf16 with an FP8 W, fp32, bf16 with an MXFP4 W, both in MXFP4
+constexpr int kXBf16 = 0, kXFp8w = 1, kXF32 = 2, kXMx = 3, kXMxX = 4;
+
+// Bytes of a row of d_in columns of W and of x.
+template <int TYPE>
+__device__ __forceinline__ long long w_row_bytes(int d_in) {
+  return TYPE >= kXMx ? d_in / 2 : (long long)d_in * (TYPE == kXFp8w ? 1 : TYPE == kXF32 ? 4 : 2);
+}
+template <int TYPE>
+__device__ __forceinline__ long long x_row_bytes(int d_in) {
+  return TYPE == kXMxX ? d_in / 2 : (long long)d_in * (TYPE == kXF32 ? 4 : 2);
+}
+// Bytes between the x columns of lane groups g and g + 1: those of 16 bytes of W.
+template <int TYPE>
+constexpr int x_group_bytes() { return TYPE == kXFp8w ? 32 : TYPE == kXMx ? 64 : 16; }
 
 // acc[r][t] = this wave's part of rows 16 r .. 16 r + 15 times tokens 16 t .. 16 t
 // + 15: NW waves take a contiguous part of d_in each, in units of 128 bytes of a
@@ -107,6 +124,94 @@ __device__ __forceinline__ void stream_product(const char* wbase, long long up, 
         for (int t = 0; t < NTB; ++t)
           x[h][i][t] = in ? ld16(xp[t] + (long long)nu * (UC * XB) + h * (UC / 2 * XB) + 16 * i) : zero_u32x4();
     }
+    multiply();
+  }
+}
+
+// The same with W in MXFP4 (kXMx) or both in MXFP4 (kXMxX). A unit is 256 columns,
+// 128 bytes of a W row in two 16-byte loads, each a block with one scale: lane group
+// g's byte of the dword that a plane of scales holds for the row. kXMx: a block's codes
+// become four bf16 operands of 8 columns; kXMxX: the matrix unit takes both sides'
+// codes and scales.
+//
+// sbase: plane 0 of W's scales at the first row (gated: `sup` bytes further those of the up
+// rows), so[]: byte offsets as wo[], splane: from a plane to the next. xsp[], xsplane:
+// the same for x (kXMxX).
+struct MxScales {
+  const char* sbase;
+  long long sup, splane, xsplane;
+};
+template <int TYPE, int NR, int NTB, int NW, bool GATED>
+__device__ __forceinline__ void stream_product_mx(const char* wbase, long long up, const uint32_t* wo, const char* const* xp,
+                                                  const MxScales& ms, const uint32_t* so, const char* const* xsp, int d_in,
+                                                  int wave, int g, f32x4_t (&acc)[NR][NTB]) {
+  static_assert(TYPE == kXMx || TYPE == kXMxX, "MXFP4");
+  constexpr int UC = 256;                                          // columns per unit
+  constexpr int XL = TYPE == kXMx ? 4 : 1;                         // x loads per W load
+  constexpr int XH = TYPE == kXMx ? 256 : 64;                      // bytes of x of half a unit
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int t = 0; t < NTB; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  u32x4_t w[2][NR], x[2][XL][NTB];
+  uint32_t sw[2][NR], sx[2][NTB];
+  auto load = [&](int u, auto whole) {                             // unit u; not whole: columns past d_in are zero
+    const char* wu = wbase + (long long)u * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = decltype(whole)::value || u * UC + h * 128 + 32 * g < d_in;
+      const char* su = ms.sbase + (2 * u + h) * ms.splane;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const uint32_t o = wo[GATED ? r / 2 : r];
+        w[h][r] = in ? ld16((GATED && (r & 1) ? wu + up : wu) + o + 64 * h) : zero_u32x4();
+        sw[h][r] = in ? *(const uint32_t*)((GATED && (r & 1) ? su + ms.sup : su) + so[GATED ? r / 2 : r]) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < XL; ++i)
+#pragma unroll
+        for (int t = 0; t < NTB; ++t) x[h][i][t] = in ? ld16(xp[t] + (long long)u * (2 * XH) + h * XH + 16 * i) : zero_u32x4();
+      if constexpr (TYPE == kXMxX) {
+#pragma unroll
+        for (int t = 0; t < NTB; ++t) sx[h][t] = in ? *(const uint32_t*)(xsp[t] + (2 * u + h) * ms.xsplane) : 0u;
+      }
+    }
+  };
+  auto multiply = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const uint32_t s = sw[h][r] >> (8 * g);
+        if constexpr (TYPE == kXMx) {
+          const float sc = mx_scale_at(s, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const u32x4_t wa = mx_bf16x8(w[h][r][i], sc);
+#pragma unroll
+            for (int t = 0; t < NTB; ++t) acc[r][t] = mfma16e(wa, x[h][i][t], acc[r][t]);
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < NTB; ++t) acc[r][t] = mfma16mx(w[h][r], s, x[h][0][t], sx[h][t] >> (8 * g), acc[r][t]);
+        }
+      }
+    }
+  };
+  const int nu = d_in / UC;                                        // whole units
+  const int ub = nu * wave / NW, ue = nu * (wave + 1) / NW;        // this wave's
+  if (ub < ue) {   // uniform
+    load(ub, std::true_type{});
+    for (int u = ub; u + 1 < ue; ++u) {
+      multiply();
+      load(u + 1, std::true_type{});
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    multiply();
+  }
+  if (nu * UC < d_in && wave == NW - 1) {   // uniform: the columns behind the last whole unit
+    load(nu, std::false_type{});
     multiply();
   }
 }
