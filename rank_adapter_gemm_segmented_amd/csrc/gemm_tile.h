@@ -46,7 +46,12 @@ __device__ __forceinline__ void dma4(const void* g, uint32_t m0) {
                : "memory", "m0");
 }
 
-// The same with a uniform base and a 32-bit byte offset per lane.
+__device__ __forceinline__ void dma4_off(const void* base, uint32_t off, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(m0)
+               : "memory", "m0");
+}
+
+// dma16 with a uniform base and a 32-bit byte offset per lane.
 __device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t m0) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(m0)
                : "memory", "m0");
@@ -87,8 +92,13 @@ struct GCfg {
   static constexpr int DPW_W = BR * WRB / 1024 / NW;    // 1 KB loads per wave per stage: W rows
   static constexpr int DPW_X = BT * RB / 1024 / NW;        // and positions
   static constexpr int DPW = DPW_W + DPW_X;
-  // loads of scales: 64 of the wave's W rows each, or (kWMxX) two planes of 32 rows of either side
-  static constexpr int DPW_S = WQ == kWMx ? (WR + 63) / 64 : WQ == kWMxX ? MR + MT : 0;
+  // loads of scales, per wave: 64 of its W rows each, or (kWMxX) two planes of 32 rows
+  // of either side. The hand-laid loop (kPipe) loads the tile's once for all waves, W's
+  // rows plane by plane, then the positions'.
+  static constexpr bool kPipe = NWR == 2 && NWT == 2 && BR >= BT;
+  static constexpr int SCALES = WQ == kWMx ? BR : WQ == kWMxX ? 2 * (BR + BT) : 0;   // of a tile's stage
+  static constexpr int DPW_S = WQ == kWMx ? (kPipe ? (BR + 255) / 256 : (WR + 63) / 64)
+                             : WQ == kWMxX ? (kPipe ? SCALES / 256 : MR + MT) : 0;
   static constexpr int SSTAGE_B = NW * DPW_S * 256;
   static constexpr int XRING = NB * WSTAGE_B;              // byte offset of the position ring
   static constexpr int SRING = XRING + NX * XSTAGE_B;      // and of the ring of scales
@@ -362,6 +372,221 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
   vm_barrier<VMC + D1>();
 #pragma unroll
   for (int f = 0; f < NF; ++f) frag(0, 0, 0, f);
+  int st = 0;
+  for (; st + NB < nwhole; ++st) stage(std::true_type{}, st);   // every request is a whole stage
+  for (; st < nst; ++st) stage(part, st);
+  vm_barrier<0>();   // the ring's last loads (zeros) land before the LDS is reused
+}
+
+// The rows of the largest tile with MXFP4 operands: as PipeSrc, and the scales, a dword
+// per row and plane. What a stage needs of scales is entries 0 .. SCALES - 1: W's rows
+// (kWMxX: those of its first plane, then of its second), then the positions'. Load i
+// of wave w brings entries 64 (i NW + w) + lane.
+template <class C>
+struct PipeSrcMx {
+  static_assert(C::NW == 4 && C::kNB >= C::kNX && C::kWQ >= kWMx && C::RB == 128, "one chunk column per lane");
+  static constexpr int WRPC = 1024 / C::WRB, WCPR = C::WRB / 16;   // W rows of a 1 KB chunk, 16-byte chunks of a row
+  static constexpr int XRPC = 1024 / C::RB, XCPR = C::RB / 16;
+  static constexpr int N = C::DPW + C::DPW_S;
+  const char *wb, *xb, *wsb, *xsb;                        // W, x and their scales, plane 0
+  long long wplane, xplane;                               // bytes from a plane of scales to the next
+  uint32_t off[N];                                        // positions, scales, W rows
+  int wcol, xcol;                                         // first column of the lane's chunks
+  template <class WRow, class XRow>
+  __device__ __forceinline__ void set(int wave, int lane, const void* w, const void* x, const void* ws, const void* xs, long long wplane_,
+                                      long long xplane_, int d_in, WRow wrow, XRow xrow) {   // rows: from the bases' first
+    wb = (const char*)w;
+    xb = (const char*)x;
+    wsb = (const char*)ws;
+    xsb = (const char*)xs;
+    wplane = wplane_;
+    xplane = xplane_;
+    const uint32_t wrb = (uint32_t)d_in / 2, xrb = C::kWQ == kWMxX ? (uint32_t)d_in / 2 : 2u * d_in;
+    // (a row's swizzle does not go by the load: 4 chunks of rows are a multiple of 16 rows)
+    const int cw = (lane % WCPR) ^ gswz<C::WRB / 2>(wave * WRPC + lane / WCPR);
+    const int cx = (lane % XCPR) ^ gswz<C::RB / 2>(wave * XRPC + lane / XCPR);
+    wcol = 32 * cw;
+    xcol = (C::kWQ == kWMxX ? 32 : 8) * cx;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i < C::DPW_X) {
+        off[i] = (uint32_t)xrow((i * C::NW + wave) * XRPC + lane / XCPR) * xrb + 16 * cx;
+      } else if (i < C::DPW_X + C::DPW_S) {
+        const int e = ((i - C::DPW_X) * C::NW + wave) * 64 + lane;
+        const bool isx = C::kWQ == kWMxX && (i - C::DPW_X) * 256 >= 2 * C::kBR;
+        off[i] = 4u * (uint32_t)(isx ? xrow((e - 2 * C::kBR) % C::kBT) : wrow(e % C::kBR));
+      } else {
+        off[i] = (uint32_t)wrow(((i - C::DPW_X - C::DPW_S) * C::NW + wave) * WRPC + lane / WCPR) * wrb + 16 * cw;
+      }
+    }
+  }
+  // load I of iteration t: positions and scales of stage t + NX before W rows of stage t + NB
+  template <int I, bool WHOLE>
+  __device__ __forceinline__ void issue(int t, uint32_t lds0, int wave, int d_in, const void* zeros) const {
+    constexpr bool isx = I < C::DPW_X, iss = !isx && I < C::DPW_X + C::DPW_S;
+    const int st = t + (isx || iss ? C::kNX : C::kNB);
+    if ((isx || iss) && C::kNB > C::kNX && st < 0) return;   // (before the first position stage)
+    if constexpr (iss) {
+      constexpr int i = I - C::DPW_X;
+      constexpr bool sx = C::kWQ == kWMxX && i * 256 >= 2 * C::kBR;
+      constexpr int rows = sx ? C::kBT : C::kBR;
+      const int e = (i * C::NW + wave) * 64 - (sx ? 2 * C::kBR : 0);
+      const int plane = C::kWQ == kWMx ? st * C::kKB / kMxPlane : 2 * st + e / rows;
+      const char* base = (sx ? xsb : wsb) + plane * (sx ? xplane : wplane);
+      const uint32_t at = lds0 + C::SRING + (uint32_t)(st % C::kNX) * C::SSTAGE_B + (uint32_t)(i * C::NW + wave) * 256;
+      if constexpr (WHOLE) dma4_off(base, off[I], at);
+      else dma4(sel_addr(plane * kMxPlane < d_in, base + off[I], zeros), at);
+    } else {
+      constexpr int j = isx ? I : I - C::DPW_X - C::DPW_S;
+      const uint32_t at = (isx ? lds0 + C::XRING + (uint32_t)(st % C::kNX) * C::XSTAGE_B
+                               : lds0 + (uint32_t)(st % C::kNB) * C::WSTAGE_B) + (uint32_t)(j * C::NW + wave) * 1024;
+      const char* base = (isx ? xb : wb) + (long long)st * (isx ? C::RB : C::WRB);
+      if constexpr (WHOLE) dma16_off(base, off[I], at);
+      else dma16(sel_addr(st * C::kKB + (isx ? xcol : wcol) < d_in, base + off[I], zeros), at);
+    }
+  }
+};
+
+// Main loop of the largest tile with MXFP4 operands, laid out as pipe_mainloop: 4
+// k-steps per stage, a stage boundary inside the last.
+//
+// kWMxX: the rows have a bf16 stage's bytes, so LDS traffic per MFMA is the same
+// at four times the columns. The stage's scales, a dword per row block, are read past
+// the boundary with the first fragments.
+// kWMx: a row block's codes of the whole stage are one 16-byte read past the boundary,
+// converted for k-step kk + 1 while k-step kk is multiplied (four conversions where
+// bf16 W has a 16-byte LDS read); x alone fills the rings, in three stages.
+template <class C>
+__device__ __forceinline__ void pipe_mainloop_mx(const PipeSrcMx<C>& s, int d_in, const void* zeros, char* lds,
+                                                 int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
+  constexpr bool XMX = C::kWQ == kWMxX;
+  constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = 4;
+  static_assert(KB == (XMX ? 256 : 64), "4 k-steps");
+  constexpr int MR = C::MR, MT = C::MT, NM = MR * MT, NF = MR + MT;
+  constexpr int H = NM / 4;
+  constexpr int NL = C::DPW + C::DPW_S;                  // loads of an iteration
+  constexpr int LATER = NB > NX ? C::DPW_W : 0, VMC = (NX - 2) * NL + LATER;
+  const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  int fcol[KS];                                          // of a 128-byte row
+#pragma unroll
+  for (int kk = 0; kk < KS; ++kk) fcol[kk] = ((4 * kh + kk) ^ gswz<64>(l32)) * 16;
+  const int wbase = (wr * C::kWR + l32) * C::WRB + (XMX ? 0 : (kh ^ gswz<C::WRB / 2>(l32)) * 16);
+  const int xbase = C::XRING + (wt * C::kWT + l32) * C::RB;
+  const int wsbase = C::SRING + ((XMX ? kh * C::kBR : 0) + wr * C::kWR + l32) * 4;
+  const int xsbase = C::SRING + (2 * C::kBR + kh * C::kBT + wt * C::kWT + l32) * 4;
+
+  u32x4_t fa[2][MR], fb[2][MT];
+  uint32_t sw[2][MR], sx[2][MT];                         // scales: this stage's, the next one's
+  u32x4_t raw[2][MR];                                    // kWMx: codes, the same
+  auto read_x = [&](int st, int kk, int set, int n) {
+    fb[set][n] = *(const u32x4_t*)(lds + (st % NX) * C::XSTAGE_B + xbase + n * 32 * C::RB + fcol[kk]);
+  };
+  auto read_w = [&](int st, int kk, int set, int m) {
+    fa[set][m] = *(const u32x4_t*)(lds + (st % NB) * C::WSTAGE_B + wbase + m * 32 * C::WRB + fcol[kk]);
+  };
+  auto convert = [&](int kk, int set, int m, int next) { fa[set][m] = mx_bf16x8(raw[next][m][kk], __uint_as_float(sw[next][m])); };
+  // task f of k-step kk's fragments: W 0, positions 0 .. MT - 1, W 1 ..
+  auto frag = [&](int st, int kk, int set, int f) {
+    if (f == 0 || f > MT) {
+      if constexpr (XMX) read_w(st, kk, set, f == 0 ? 0 : f - MT);
+      else convert(kk, set, f == 0 ? 0 : f - MT, 0);
+    } else {
+      read_x(st, kk, set, f - 1);
+    }
+  };
+  // tasks past a boundary: stage st's scales (and codes), then its first fragments
+  constexpr int NT0 = XMX ? 2 * NF : 3 * MR + MT;
+  auto first = [&](int st, int f) {
+    const char* S = lds + (st % NX) * C::SSTAGE_B;
+    if constexpr (XMX) {
+      if (f < MR) sw[1][f] = *(const uint32_t*)(S + wsbase + f * 128);
+      else if (f < NF) sx[1][f - MR] = *(const uint32_t*)(S + xsbase + (f - MR) * 128);
+      else frag(st, 0, 0, f - NF);
+    } else {
+      if (f < 2 * MR) {
+        const int m = f / 2;
+        if (f % 2 == 0) raw[1][m] = *(const u32x4_t*)(lds + (st % NB) * C::WSTAGE_B + wbase + m * 32 * C::WRB);
+        else sw[1][m] = *(const uint32_t*)(S + wsbase + m * 128);
+      } else if (f < 2 * MR + MT) {
+        read_x(st, 0, 0, f - 2 * MR);
+      } else {
+        const int m = f - 2 * MR - MT;
+        // the block's byte as a float (the plane holds two stages)
+        sw[1][m] = ((sw[1][m] >> (8 * kh + 16 * (st & 1))) & 0xffu) << 23;
+        convert(0, 0, m, 1);
+      }
+    }
+  };
+  auto turn = [&]() {                                    // the next stage's scales and codes become this one's
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      sw[0][m] = sw[1][m];
+      if constexpr (!XMX) raw[0][m] = raw[1][m];
+    }
+    if constexpr (XMX) {
+#pragma unroll
+      for (int n = 0; n < MT; ++n) sx[0][n] = sx[1][n];
+    }
+  };
+  auto mfma = [&]<int KK, int I>(std::integral_constant<int, KK>, std::integral_constant<int, I>) {
+    constexpr int m = I / MT, n = I % MT;
+    if constexpr (XMX) acc[m][n] = mfma32mx<KK, KK>(fa[KK & 1][m], sw[0][m], fb[KK & 1][n], sx[0][n], acc[m][n]);
+    else acc[m][n] = mfma32g(fa[KK & 1][m], fb[KK & 1][n], acc[m][n]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  constexpr int NS = KS * NM;                            // MFMAs of a stage
+  constexpr int SP = NS * 3 / 4;                         // over which its requests are spread
+  auto upto = [](int i) constexpr { return i >= SP ? NL : i * NL / SP; };
+  constexpr int D1 = upto(NM - H);
+  auto request = [&]<bool WHOLE, int L0, int N>(std::bool_constant<WHOLE>, int t, std::integral_constant<int, L0>,
+                                                std::integral_constant<int, N>) {
+    [&]<int... J>(std::integer_sequence<int, J...>) { (s.template issue<L0 + J, WHOLE>(t, lds0, wave, d_in, zeros), ...); }
+    (std::make_integer_sequence<int, N>{});
+    if constexpr (N > 0) __builtin_amdgcn_sched_barrier(0);
+  };
+  auto request_at = [&]<int I>(auto whole, int t, std::integral_constant<int, I>) {   // after MFMA I of a stage
+    constexpr int L0 = upto(I), L1 = upto(I + 1);
+    request(whole, t, std::integral_constant<int, L0>{}, std::integral_constant<int, L1 - L0>{});
+  };
+  auto each = []<int... I>(std::integer_sequence<int, I...>, auto f) { (f(std::integral_constant<int, I>{}), ...); };
+  auto stage = [&](auto whole, int st) {
+    each(std::make_integer_sequence<int, (KS - 1) * NM>{}, [&](auto ic) {
+      constexpr int I = ic.value, kk = I / NM, i = I % NM;
+      mfma(std::integral_constant<int, kk>{}, std::integral_constant<int, i>{});
+      if constexpr (i * NF / NM != (i + 1) * NF / NM) {
+        frag(st, kk + 1, (kk + 1) & 1, i * NF / NM);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      request_at(whole, st - 1, std::integral_constant<int, NM - H + I>{});
+    });
+    each(std::make_integer_sequence<int, H>{}, [&](auto ic) {
+      mfma(std::integral_constant<int, KS - 1>{}, ic);
+      request_at(whole, st - 1, std::integral_constant<int, NS - H + ic.value>{});
+    });
+    vm_barrier<VMC>();
+    __builtin_amdgcn_sched_barrier(0);
+    each(std::make_integer_sequence<int, NM - H>{}, [&](auto ic) {
+      constexpr int I = ic.value;
+      mfma(std::integral_constant<int, KS - 1>{}, std::integral_constant<int, H + I>{});
+#pragma unroll
+      for (int f = I * NT0 / (NM - H); f < (I + 1) * NT0 / (NM - H); ++f) first(st + 1, f);
+      __builtin_amdgcn_sched_barrier(0);
+      request_at(whole, st, ic);
+    });
+    turn();
+  };
+
+  const int nst = (d_in + KB - 1) / KB, nwhole = d_in / KB;
+  constexpr std::false_type part{};
+#pragma unroll
+  for (int t = -NB; t < -1; ++t) request(part, t, std::integral_constant<int, 0>{}, std::integral_constant<int, NL>{});
+  request(part, -1, std::integral_constant<int, 0>{}, std::integral_constant<int, D1>{});
+  vm_barrier<VMC + D1>();
+#pragma unroll
+  for (int f = 0; f < NT0; ++f) first(0, f);
+  turn();
   int st = 0;
   for (; st + NB < nwhole; ++st) stage(std::true_type{}, st);   // every request is a whole stage
   for (; st < nst; ++st) stage(part, st);

@@ -207,7 +207,13 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0,
     for (int n = 0; n < C::MT; ++n)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.f;
-  if constexpr (PIPE) {
+  if constexpr (PIPE && C::kWQ >= kWMx) {
+    const int w0 = wrow_of<GATED>(r0, d_out);
+    PipeSrcMx<C> src;
+    src.set(wave, lane, W + w0 * wrb, x, a.w_mx + 4 * ((long long)e * mx_planes(d_in) * d_out + w0), a.x_mx, 4ll * d_out, 4ll * a.n_rows, d_in,
+            [&](int r) { return wrow_of<GATED>(r0 + r, d_out) - w0; }, row_of);
+    pipe_mainloop_mx<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
+  } else if constexpr (PIPE) {
     // W offsets from the tile's first row (gated: its first gate row; the up
     // rows lie d_out / 2 rows further)
     const int w0 = wrow_of<GATED>(r0, d_out);
@@ -258,14 +264,32 @@ void k_experts_tile(ExpertsArgs a, int n_rt, int max_runs, bool by_expert) {
 // half of them busy are cut into four (128 x 128) or two (256 x 128) for all of
 // them (the way back of a prefill batch, 72 tiles per XCD: 1072 -> 1007 us). A run
 // of at most 128 positions takes the 256 x 128 form too.
-typedef GCfg<256, 256, 128, 128, 3, 64, 2> Tile256;
-typedef GCfg<256, 128, 128, 64, 3, 64, 3> Tile256Half;
-typedef GCfg<128, 128, 64, 64, 4, 64, 4> Tile256Quarter;
+template <int WQ>
+struct Tiles256 {
+  typedef GCfg<256, 256, 128, 128, 3, 64, 2> Whole;
+  typedef GCfg<256, 128, 128, 64, 3, 64, 3> Half;
+  typedef GCfg<128, 128, 64, 64, 4, 64, 4> Quarter;
+};
+template <>
+struct Tiles256<kWMx> {
+  typedef GCfg<256, 256, 128, 128, 3, 64, 3, kWMx> Whole;
+  typedef GCfg<256, 128, 128, 64, 3, 64, 3, kWMx> Half;
+  typedef GCfg<128, 128, 64, 64, 4, 64, 4, kWMx> Quarter;
+};
+template <>
+struct Tiles256<kWMxX> {
+  typedef GCfg<256, 256, 128, 128, 2, 256, 2, kWMxX> Whole;
+  typedef GCfg<256, 128, 128, 64, 3, 256, 3, kWMxX> Half;
+  typedef GCfg<128, 128, 64, 64, 4, 256, 4, kWMxX> Quarter;
+};
 constexpr int kXcdCus = 32;
 
-template <int OUT>
+template <int OUT, int WQ>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_experts_tile256(ExpertsArgs a, int n_rt, int max_runs) {
+  using Tile256 = typename Tiles256<WQ>::Whole;
+  using Tile256Half = typename Tiles256<WQ>::Half;
+  using Tile256Quarter = typename Tiles256<WQ>::Quarter;
   __shared__ __attribute__((aligned(1024))) char lds[160 * 1024];
   static_assert(Tile256::TILE_BYTES <= sizeof(lds) && Tile256Half::TILE_BYTES <= sizeof(lds) && Tile256Quarter::TILE_BYTES <= sizeof(lds), "one LDS block");
   const RunScan first = scan_runs(a.seg_start, a.E, a.n_pos, 256, 0);
@@ -403,6 +427,7 @@ static void launch_tile(const ExpertsArgs& a, hipStream_t st) {
   else hipLaunchKernelGGL((k_experts_tile<C, 0>), grid, block, 0, st, a, n_rt, max_runs, by_expert);
 }
 
+template <int WQ>
 static void launch_tile256(const ExpertsArgs& a, hipStream_t st) {
   const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
   const int n_rt = (rows + 255) / 256;
@@ -410,9 +435,9 @@ static void launch_tile256(const ExpertsArgs& a, hipStream_t st) {
   // 24 pieces more
   const int max_runs = (int)run_bound(a, 256);
   const dim3 grid(8 * (xcd_tiles(0, max_runs, n_rt) + 24)), block(256);
-  if (a.f32_out) hipLaunchKernelGGL(k_experts_tile256<2>, grid, block, 0, st, a, n_rt, max_runs);
-  else if (a.gated) hipLaunchKernelGGL(k_experts_tile256<1>, grid, block, 0, st, a, n_rt, max_runs);
-  else hipLaunchKernelGGL(k_experts_tile256<0>, grid, block, 0, st, a, n_rt, max_runs);
+  if (a.f32_out) hipLaunchKernelGGL((k_experts_tile256<2, WQ>), grid, block, 0, st, a, n_rt, max_runs);
+  else if (a.gated) hipLaunchKernelGGL((k_experts_tile256<1, WQ>), grid, block, 0, st, a, n_rt, max_runs);
+  else hipLaunchKernelGGL((k_experts_tile256<0, WQ>), grid, block, 0, st, a, n_rt, max_runs);
 }
 
 template <bool W8> using Tile128 = GCfg<128, 128, 64, 32, 3, W8 ? 128 : 64, W8 ? 2 : 3, W8 ? kWFp8 : kWBf16>;
@@ -422,7 +447,6 @@ typedef GCfg<128, 32, 32, 32, 5, 64, 5> Tile32;
 template <bool XMX> using Mx32 = GCfg<128, 32, 32, 32, 4, XMX ? 256 : 128, 4, XMX ? kWMxX : kWMx>;
 template <bool XMX> using Mx64 = GCfg<128, 64, 32, 32, 4, XMX ? 256 : 128, 4, XMX ? kWMxX : kWMx>;
 template <bool XMX> using Mx128 = GCfg<128, 128, 64, 32, 3, XMX ? 256 : 128, 3, XMX ? kWMxX : kWMx>;
-template <bool XMX> using Mx256 = GCfg<256, 256, 128, 64, XMX ? 2 : 3, XMX ? 256 : 64, XMX ? 2 : 3, XMX ? kWMxX : kWMx>;
 
 // Form by the rows per expert. Up to two (FP8: twenty), the streaming form; it
 // also takes fp32 and what has too few tiles for the card: fewer than 256 of 32
@@ -453,7 +477,7 @@ static void launch_bf16(const ExpertsArgs& a, hipStream_t st) {
   if (mean <= (W8 ? 20 : 2) || tiles < (mean <= 8 ? 256 : 64)) return launch_stream<W8 ? kXFp8w : kXBf16>(a, st);
   if constexpr (!W8) {
     if (mean <= 8) return launch_tile<Tile32>(a, st);
-    if (near && (mean >= 192 || (mean >= 112 && tiles256 >= 1024))) return launch_tile256(a, st);
+    if (near && (mean >= 192 || (mean >= 112 && tiles256 >= 1024))) return launch_tile256<kWBf16>(a, st);
   }
   if (mean <= 48) launch_tile<Tile64<W8>>(a, st);
   else launch_tile<Tile128<W8>>(a, st);
@@ -464,12 +488,13 @@ static void launch_mx(const ExpertsArgs& a, hipStream_t st) {
   const long long active = std::min(a.E, a.n_pos);
   const double mean = (double)a.n_pos / active;
   const int rows = a.gated ? gated_rows(a.d_out) : a.d_out;
+  const bool near = 2ll * a.n_rows * a.d_in < (1ll << 32) && (a.gated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
   const long long tiles256 = (rows + 255) / 256 * (a.n_pos / 256 + active / 2);
   const int bt = mean <= 8 ? 32 : mean <= 48 ? 64 : 128;
   const long long tiles = (rows + 127) / 128 * std::max(active, a.n_pos / bt + active / 2);
   if (mean <= 2 || tiles < (mean <= 8 ? 256 : 64)) launch_stream<XMX ? kXMxX : kXMx>(a, st);
   else if (mean <= 8) launch_tile<Mx32<XMX>>(a, st);
-  else if (mean >= 192 || (mean >= 112 && tiles256 >= 1024)) launch_tile<Mx256<XMX>>(a, st);
+  else if (near && (mean >= 192 || (mean >= 112 && tiles256 >= 1024))) launch_tile256<XMX ? kWMxX : kWMx>(a, st);
   else if (mean <= 48) launch_tile<Mx64<XMX>>(a, st);
   else launch_tile<Mx128<XMX>>(a, st);
 }

@@ -738,7 +738,18 @@ void k_gemm2(LinearArgs a) {
       for (int v = 0; v < 16; ++v) acc[m][n][v] = 0.f;
 
   // Main loop. PIPE: that of the largest tile (gemm_tile.h).
-  if constexpr (PIPE) {
+  if constexpr (PIPE && WQ >= kWMx) {
+    const int w0 = wrow_of<GATED>(r0, d_out);
+    PipeSrcMx<C> src;
+    src.set(wave, lane, (const char*)a.W + (long long)w0 * (d_in / 2), WQ == kWMxX ? (const void*)a.x_codes : a.x, a.w_mx + 4ll * w0, a.x_mx,
+            4ll * d_out, 4ll * T, d_in, [&](int r) { return wrow_of<GATED>(r0 + r, d_out) - w0; },
+            [&](int r) {
+              const int p = min(t0 + r, T - 1);
+              const int row = a.sv.token_index ? a.sv.token_index[p] : p;
+              return min(max(row, 0), T - 1);
+            });
+    pipe_mainloop_mx<C>(src, d_in, zeros, (char*)lds, wave, lane, acc);
+  } else if constexpr (PIPE) {
     const int w0 = wrow_of<GATED>(r0, d_out);
     PipeSrc<C> src;
     src.set(wave, lane, W + (long long)w0 * d_in, x,
@@ -1365,20 +1376,20 @@ void launch_linear_bf16(const LinearArgs& a, hipStream_t st) {
   // loop of gemm_tile.h, which addresses x and its rows of W by 32-bit offsets
   // (past them: 128x128 tiles).
   const bool large = a.T > 128 && tiles(256, 256) >= kFill, epi = a.epi_kind != kEpiNone;
+  const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
+                    (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
   if (a.w_mx && a.x_mx) {
-    if (large) launch_g<256, 256, 128, 64, 2, 256, 2, kWMxX>(a, st, true);
+    if (large && near) launch_g<256, 256, 128, 128, 2, 256, 2, kWMxX>(a, st, true);
     else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 256, 3, kWMxX>(a, st, true);
     else launch_g<64, 128, 32, 32, 4, 256, 3, kWMxX>(a, st, true);
     return;
   }
   if (a.w_mx) {
-    if (large) launch_g<256, 256, 128, 64, 3, 64, 3, kWMx>(a, st, true);
+    if (large && near) launch_g<256, 256, 128, 128, 3, 64, 3, kWMx>(a, st, true);
     else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 128, 3, kWMx>(a, st, true);
     else launch_g<64, 128, 32, 64, 4, 128, 3, kWMx>(a, st, true);
     return;
   }
-  const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
-                    (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
   if (large && epi && near) launch_g<256, 256, 128, 128, 3, 64, 2>(a, st, true);
   else if (large && !epi) launch_g<256, 256, 128, 64, 2, 64, 2>(a, st, false);
   else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 64, 3>(a, st, true);
