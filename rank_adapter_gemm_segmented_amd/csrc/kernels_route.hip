@@ -49,6 +49,25 @@ __device__ __forceinline__ float wave_sum(float f) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), kWave - 1));
 }
 
+// The same in 64 bits: the two halves of each lane's addend shift separately.
+__device__ __forceinline__ double wave_sum64(double f) {
+  auto add = [](double x, auto shift) {
+    const unsigned long long u = __double_as_longlong(x);
+    const uint32_t lo = shift((uint32_t)u), hi = shift((uint32_t)(u >> 32));
+    return x + __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+  };
+  f = add(f, [](uint32_t v) { return dpp<0x111, 0xf>(0u, v); });
+  f = add(f, [](uint32_t v) { return dpp<0x112, 0xf>(0u, v); });
+  f = add(f, [](uint32_t v) { return dpp<0x114, 0xf>(0u, v); });
+  f = add(f, [](uint32_t v) { return dpp<0x118, 0xf>(0u, v); });
+  f = add(f, [](uint32_t v) { return dpp<0x142, 0xa>(0u, v); });
+  f = add(f, [](uint32_t v) { return dpp<0x143, 0xc>(0u, v); });
+  const unsigned long long u = __double_as_longlong(f);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, kWave - 1);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), kWave - 1);
+  return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
+
 // Order of a logit: larger is better, ties go to the lowest expert. NaN and
 // -inf get 0 and are never chosen.
 __device__ __forceinline__ uint32_t logit_key(float l) {
@@ -175,6 +194,15 @@ __device__ __forceinline__ void choose4(const RouteArgs& a, int t, bool there, i
   *w = my_id >= 0 ? mine / sum : 0.f;
 }
 
+// 1 / x to within two roundings, x in [1, 1e300]: the hardware's estimate (2^-14 or
+// better) and two Newton steps, without the full division's scaling.
+__device__ __forceinline__ double reciprocal64(double x) {
+  double r = __builtin_amdgcn_rcp(x);
+  r = fma(fma(-x, r, 1.0), r, r);
+  r = fma(fma(-x, r, 1.0), r, r);
+  return fma(fma(-x, r, 1.0), r, r);
+}
+
 // Choice of one token by one wave by scores (mlora_route_scored). The scores decide
 // which of two near experts is chosen, so their rounding is part of the result: they
 // are computed in 64 bits and rounded once to fp32, where the bias is added (one
@@ -183,38 +211,36 @@ __device__ __forceinline__ void choose4(const RouteArgs& a, int t, bool there, i
 template <typename E_, int NV>
 __device__ __forceinline__ void choose_scored(const RouteArgs& a, int t, int lane, uint32_t* key_lds, int* id, float* w) {
   const E_* __restrict__ row = (const E_*)a.logits + (long long)t * a.E;
-  float l[NV], s[NV];
+  float l[NV], s[NV], b[NV];
   uint32_t key[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + kWave * i;
-    l[i] = elem_f32<E_>(row, min(e, a.E - 1));
-    if (e >= a.E || !(l[i] > -INFINITY)) l[i] = -INFINITY;   // (NaN: as -inf)
-  }
+  for (int i = 0; i < NV; ++i) l[i] = elem_f32<E_>(row, min(lane + kWave * i, a.E - 1));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) b[i] = a.bias ? a.bias[min(lane + kWave * i, a.E - 1)] : 0.f;   // (requested with the logits)
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (lane + kWave * i >= a.E || !(l[i] > -INFINITY)) l[i] = -INFINITY;   // (NaN: as -inf)
   if (a.sigmoid) {   // uniform
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = (float)(1.0 / (1.0 + exp(-(double)l[i])));
+    for (int i = 0; i < NV; ++i) s[i] = (float)reciprocal64(1.0 + exp(fmin(-(double)l[i], 200.0)));   // (0 in fp32 from 104 on)
   } else {
-    float m = l[0];
+    uint32_t mk = logit_key(l[0]);
 #pragma unroll
-    for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+    for (int i = 1; i < NV; ++i) mk = max(mk, logit_key(l[i]));
+    const float m = key_logit(wave_max(mk));             // (a row of no expert: NaN)
     double p[NV], sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       p[i] = !(l[i] > -INFINITY) ? 0.0 : l[i] == m ? 1.0 : exp((double)l[i] - (double)m);
       sum += p[i];
     }
+    const double inv = 1.0 / wave_sum64(sum);
 #pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) sum += __shfl_xor(sum, off, kWave);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = (float)(p[i] / sum);   // (a row of no expert: NaN, chosen by none)
+    for (int i = 0; i < NV; ++i) s[i] = (float)(p[i] * inv);   // (a row of no expert: NaN, chosen by none)
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + kWave * i;
-    const float c = a.bias ? s[i] + a.bias[min(e, a.E - 1)] : s[i];
+    const float c = a.bias ? s[i] + b[i] : s[i];
     key[i] = l[i] > -INFINITY ? logit_key(c) : 0u;
   }
   if (a.groups > 1) {   // uniform
@@ -223,24 +249,29 @@ __device__ __forceinline__ void choose_scored(const RouteArgs& a, int t, int lan
     for (int i = 0; i < NV; ++i)
       if (lane + kWave * i < a.E) key_lds[lane + kWave * i] = key[i];
     // (the wave's own LDS writes are ordered before its reads)
+    // lane g: the two best of group g, eight entries in flight
     uint32_t k1 = 0u, k2 = 0u;
-    if (lane < a.groups) {
-      for (int j = 0; j < per; ++j) {
-        const uint32_t k = key_lds[lane * per + j];
-        k2 = max(k2, min(k1, k));
-        k1 = max(k1, k);
+    const int first = min(lane, a.groups - 1) * per;
+    for (int j0 = 0; j0 < per; j0 += 8) {
+      uint32_t k[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) k[u] = key_lds[first + min(j0 + u, per - 1)];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t v = j0 + u < per ? k[u] : 0u;
+        k2 = max(k2, min(k1, v));
+        k1 = max(k1, v);
       }
     }
     // (a group with an expert is above none, whatever its sum)
-    uint32_t gk = k1 == 0u ? 0u : max(1u, logit_key(k2 == 0u ? key_logit(k1) : key_logit(k1) + key_logit(k2)));
-    unsigned long long kept = 0ull;
-    for (int j = 0; j < a.top_groups; ++j) {
-      const uint32_t m = wave_max(gk);
-      if (m == 0u) break;   // uniform
-      const int win = (int)__builtin_ctzll(__ballot(gk == m));
-      kept |= 1ull << win;
-      if (lane == win) gk = 0u;
+    const uint32_t gk = lane >= a.groups || k1 == 0u ? 0u
+                        : max(1u, logit_key(k2 == 0u ? key_logit(k1) : key_logit(k1) + key_logit(k2)));
+    int above = 0;   // groups before this one in the order
+    for (int g = 0; g < a.groups; ++g) {
+      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, g);
+      above += o > gk || (o == gk && g < lane);
     }
+    const unsigned long long kept = __ballot(gk != 0u && above < a.top_groups);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (!((kept >> (min(lane + kWave * i, a.E - 1) / per)) & 1ull)) key[i] = 0u;
@@ -402,10 +433,10 @@ __global__ __launch_bounds__(kRtThreads) void k_route_one(RouteArgs a) {
 constexpr int kRcThreads = 512;
 
 template <typename E_, int NV, int FORM>
-__global__ __launch_bounds__(kRcThreads) void k_route_choose(RouteArgs a) {
+__global__ __launch_bounds__(FORM == kRtScored ? kRtThreads : kRcThreads) void k_route_choose(RouteArgs a) {
   extern __shared__ int sm[];
   choose_block<E_, NV, FORM>(a, sm, nullptr, sm + a.E);
-  for (int e = threadIdx.x; e < a.E; e += kRcThreads) a.hist[(long long)blockIdx.x * a.E + e] = sm[e];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(long long)blockIdx.x * a.E + e] = sm[e];
 }
 
 // Grouping by the blocks' counts: block b's first position of expert e is the
@@ -462,10 +493,18 @@ static int route_tokens_per_block(int T) {
   return (t + kRtMinTokens - 1) / kRtMinTokens * kRtMinTokens;
 }
 
+// By scores a wave takes a token (its score alone is some 60 instructions in 64
+// bits), so the choice spreads over more and smaller blocks.
+constexpr int kRsMinTokens = 4;
+static int scored_tokens_per_block(int T) {
+  const int t = (T + kRtMaxBlocks - 1) / kRtMaxBlocks;
+  return t > kRsMinTokens ? t : kRsMinTokens;
+}
+
 // Counts of the most blocks that a batch of up to T tokens is cut into: a larger
 // batch never has a smaller workspace (8193 tokens are fewer blocks than 8192).
 size_t route_workspace_bytes(int T, int E) {
-  const int blocks = (T + kRtMinTokens - 1) / kRtMinTokens;
+  const int blocks = (T + kRsMinTokens - 1) / kRsMinTokens;
   return ((size_t)(blocks < kRtMaxBlocks ? blocks : kRtMaxBlocks) * E * 4 + 255) / 256 * 256;
 }
 
@@ -477,6 +516,16 @@ constexpr int kRtOneTokens = 128;
 template <typename E_, int NV, int FORM>
 static void launch_route_nv(RouteArgs a, hipStream_t st) {
   const size_t lds = route_lds_bytes(a.E);
+  if constexpr (FORM == kRtScored) {
+    if (a.T > kRtWaves) {
+      a.tpb = scored_tokens_per_block(a.T);
+      const dim3 grid((a.T + a.tpb - 1) / a.tpb);
+      const int waves = a.tpb < kRtWaves ? a.tpb : kRtWaves;
+      hipLaunchKernelGGL((k_route_choose<E_, NV, FORM>), grid, dim3(waves * kWave), (size_t)a.E * 4 * (1 + waves), st, a);
+      hipLaunchKernelGGL(k_route_group, grid, dim3(kRtThreads), lds, st, a);
+      return;
+    }
+  }
   if (a.T <= kRtOneTokens) {
     a.tpb = a.T;
     hipLaunchKernelGGL((k_route_one<E_, NV, FORM>), dim3(1), dim3(kRtThreads), lds + (size_t)a.T * a.k * 4, st, a);
@@ -484,8 +533,7 @@ static void launch_route_nv(RouteArgs a, hipStream_t st) {
   }
   a.tpb = route_tokens_per_block(a.T);
   const dim3 grid((a.T + a.tpb - 1) / a.tpb);
-  hipLaunchKernelGGL((k_route_choose<E_, NV, FORM>), grid, dim3(kRcThreads),
-                     (size_t)a.E * 4 * (FORM == kRtScored ? 1 + kRcThreads / kWave : 1), st, a);
+  hipLaunchKernelGGL((k_route_choose<E_, NV, FORM>), grid, dim3(kRcThreads), (size_t)a.E * 4, st, a);
   hipLaunchKernelGGL(k_route_group, grid, dim3(kRtThreads), lds, st, a);
 }
 
@@ -493,7 +541,10 @@ template <typename E_>
 static void launch_route_t(const RouteArgs& a, hipStream_t st) {
   if (a.scored) {
     if (a.E <= 64) launch_route_nv<E_, 1, kRtScored>(a, st);
+    else if (a.E <= 128) launch_route_nv<E_, 2, kRtScored>(a, st);
+    else if (a.E <= 192) launch_route_nv<E_, 3, kRtScored>(a, st);
     else if (a.E <= 256) launch_route_nv<E_, 4, kRtScored>(a, st);
+    else if (a.E <= 512) launch_route_nv<E_, 8, kRtScored>(a, st);
     else launch_route_nv<E_, MLORA_MAX_EXPERTS / kWave, kRtScored>(a, st);
   } else if (a.E > 256 || a.k > 16) launch_route_nv<E_, MLORA_MAX_EXPERTS / kWave, kRtOne>(a, st);
   else if (a.E <= 64) launch_route_nv<E_, 4, kRtQuad>(a, st);
