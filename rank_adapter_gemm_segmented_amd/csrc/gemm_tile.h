@@ -77,7 +77,9 @@ __device__ __forceinline__ void vm_barrier() {
 // wave: the dwords of its own rows, DPW_S loads of 256 bytes per stage.
 constexpr int kWBf16 = 0, kWFp8 = 1, kWMx = 2, kWMxX = 3;
 
-template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, int WQ = kWBf16>
+// SHARED: the tile's scales are loaded once for all waves (the hand-laid loop), W's
+// rows plane by plane, then the positions'.
+template <int BR, int BT, int WR, int WT, int NB, int KB, int NX, int WQ = kWBf16, bool SHARED = false>
 struct GCfg {
   static constexpr int kWQ = WQ;
   static constexpr bool kW8 = WQ == kWFp8;
@@ -93,12 +95,10 @@ struct GCfg {
   static constexpr int DPW_X = BT * RB / 1024 / NW;        // and positions
   static constexpr int DPW = DPW_W + DPW_X;
   // loads of scales, per wave: 64 of its W rows each, or (kWMxX) two planes of 32 rows
-  // of either side. The hand-laid loop (kPipe) loads the tile's once for all waves, W's
-  // rows plane by plane, then the positions'.
-  static constexpr bool kPipe = NWR == 2 && NWT == 2 && BR >= BT;
+  // of either side; SHARED: 64 entries of the tile's list.
   static constexpr int SCALES = WQ == kWMx ? BR : WQ == kWMxX ? 2 * (BR + BT) : 0;   // of a tile's stage
-  static constexpr int DPW_S = WQ == kWMx ? (kPipe ? (BR + 255) / 256 : (WR + 63) / 64)
-                             : WQ == kWMxX ? (kPipe ? SCALES / 256 : MR + MT) : 0;
+  static constexpr int DPW_S = WQ == kWMx ? (SHARED ? (BR + 255) / 256 : (WR + 63) / 64)
+                             : WQ == kWMxX ? (SHARED ? SCALES / 256 : MR + MT) : 0;
   static constexpr int SSTAGE_B = NW * DPW_S * 256;
   static constexpr int XRING = NB * WSTAGE_B;              // byte offset of the position ring
   static constexpr int SRING = XRING + NX * XSTAGE_B;      // and of the ring of scales

@@ -681,7 +681,7 @@ __attribute__((amdgpu_waves_per_eu((BR / WR) * (BT / WT) / 4, (BR / WR) * (BT / 
 void k_gemm2(LinearArgs a) {
   constexpr bool GATED = EPI == kEpiGated;
   constexpr bool PIPE = BR == 256 && (BR / WR) * (BT / WT) == 4;   // (one wave per SIMD)
-  using C = GCfg<BR, BT, WR, WT, NB, KB, NX, WQ>;
+  using C = GCfg<BR, BT, WR, WT, NB, KB, NX, WQ, PIPE>;
   // the rings, then what the expand lists: the tile's position entries, each
   // wave's work units of a rank chunk and run starts. PIPE: the rings take all of
   // the LDS, and the lists lie in it behind the staged v.
@@ -1284,7 +1284,7 @@ static void launch_g(const LinearArgs& a, hipStream_t st, bool grouped_order) {
   g.gorder = grouped_order && n_tt > 1 && n_rt % 8 == 0 && (long long)n_rt * n_tt > 256;
   if (BR == 256 && n_rt % 4 == 0 && n_tt % 2 == 0 && (long long)n_rt * n_tt <= 256) g.gorder = 2;
   g.wnt = n_tt <= 2;
-  const dim3 grid(n_rt * n_tt), block(GCfg<BR, BT, WR, WT, NB, KB, NX, WQ>::NT);
+  const dim3 grid(n_rt * n_tt), block((BR / WR) * (BT / WT) * kWave);
   // (of the 256 x 256 tiles, the 8-wave one runs without an epilogue, the 4-wave one with)
   constexpr bool kWithEpi = WQ != kWBf16 || BR < 256 || WT == 128, kWithout = WQ != kWBf16 || BR < 256 || WT < 128;
   if constexpr (kWithEpi) {
