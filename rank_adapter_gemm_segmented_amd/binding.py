@@ -490,8 +490,11 @@ def linear_tokens_epilogue(x, W, pool: Pool, token_adapter, adapter_scale, lora_
 
 # ---- microscaled 4-bit floating point ----------------------------------------------
 
-def _planes(d: int) -> int:
-    return (d + 127) // 128
+def _batch(lead) -> int:
+    n = 1
+    for i in lead:
+        n *= i
+    return n
 
 
 def mxfp4_scale_layout(scale):
@@ -509,32 +512,39 @@ def _check_codes(codes, scale, what: str):
     """Checks MXFP4 codes [..., rows, d / 2] and their scales; returns (batch, rows, d)."""
     if codes.dtype is not _u8t or scale.dtype is not _u8t:
         raise TypeError(f"{what}: codes and scales must be uint8")
-    if codes.dim() < 2:
+    c, s = codes.shape, scale.shape
+    if len(c) == 2:
+        rows, half = c
+        if s != ((half + 63) // 64, rows, 4):
+            raise ValueError(f"{what}: scales must be [ceil(d / 128), rows, 4]")
+        return 1, rows, 2 * half
+    lead = len(c) - 2
+    if lead < 0:
         raise ValueError(f"{what}: codes must be [..., rows, d / 2]")
-    *lead, rows, half = codes.shape
-    if tuple(scale.shape) != (*lead, _planes(2 * half), rows, 4):
+    rows, d = c[lead], 2 * c[lead + 1]
+    if s[lead:] != ((d + 127) // 128, rows, 4) or s[:lead] != c[:lead]:
         raise ValueError(f"{what}: scales must be [..., ceil(d / 128), rows, 4]")
-    batch = 1
-    for n in lead:
-        batch *= n
-    return batch, rows, 2 * half
+    return _batch(c[:lead]), rows, d
 
 
 def quantize_mxfp4(x, out=None):
     """``mlora_quantize_mxfp4``: x [..., rows, d], bf16 or float32, as (codes [..., rows, d / 2],
     scale [..., ceil(d / 128), rows, 4]), both uint8; ``out`` is such a pair to write into."""
-    what, dev = "quantize_mxfp4", _device()
-    if x.dim() < 2:
+    what, dev, dt, shape = "quantize_mxfp4", _device(), x.dtype, x.shape
+    lead = len(shape) - 2
+    if lead < 0:
         raise ValueError("x must be [..., rows, d]")
-    code = _dtype_code(x.dtype)
-    *lead, rows, d = x.shape
+    code = MLORA_BF16 if dt is _bf16t else _dtype_code(dt)
+    rows, d = shape[lead], shape[lead + 1]
+    batch = _batch(shape[:lead]) if lead else 1
     if out is None:
-        out = x.new_empty((*lead, rows, d // 2), dtype=_u8t), x.new_empty((*lead, _planes(d), rows, 4), dtype=_u8t)
-    codes, scale = out
-    batch, r, n = _check_codes(codes, scale, what)
-    if codes.shape[:-1] != x.shape[:-1] or n != d:
-        raise ValueError("out must be (codes, scale) of x")
-    code = _lib.mlora_quantize_mxfp4(_at(x, dev, what), code, batch, r, d, _at(codes, dev, what), _at(scale, dev, what),
+        more = shape[:lead]
+        codes, scale = x.new_empty((*more, rows, d // 2), dtype=_u8t), x.new_empty((*more, (d + 127) // 128, rows, 4), dtype=_u8t)
+    else:
+        codes, scale = out
+        if _check_codes(codes, scale, what) != (batch, rows, d) or codes.shape[:-1] != shape[:-1]:
+            raise ValueError("out must be (codes, scale) of x")
+    code = _lib.mlora_quantize_mxfp4(_at(x, dev, what), code, batch, rows, d, _at(codes, dev, what), _at(scale, dev, what),
                                      _raw_stream(dev))
     if code:
         raise MloraError(code, "mlora_quantize_mxfp4")
@@ -545,15 +555,16 @@ def dequantize_mxfp4(codes, scale, dtype: torch.dtype = torch.bfloat16, out=None
     """``mlora_dequantize_mxfp4``: the values of codes and scales, [..., rows, d] in bf16 or float32."""
     what, dev = "dequantize_mxfp4", _device()
     batch, rows, d = _check_codes(codes, scale, what)
-    code, shape = _dtype_code(dtype), (*codes.shape[:-1], d)
-    y = out if out is not None else codes.new_empty(shape, dtype=dtype)
-    if y.dtype is not dtype or tuple(y.shape) != shape:
-        raise ValueError(f"out must be {list(shape)} of {dtype}")
-    code = _lib.mlora_dequantize_mxfp4(_at(codes, dev, what), _at(scale, dev, what), code, batch, rows, d, _at(y, dev, what),
+    code = MLORA_BF16 if dtype is _bf16t else _dtype_code(dtype)
+    if out is None:
+        out = codes.new_empty((*codes.shape[:-1], d), dtype=dtype)
+    elif out.dtype is not dtype or out.shape != (*codes.shape[:-1], d):
+        raise ValueError(f"out must be {[*codes.shape[:-1], d]} of {dtype}")
+    code = _lib.mlora_dequantize_mxfp4(_at(codes, dev, what), _at(scale, dev, what), code, batch, rows, d, _at(out, dev, what),
                                        _raw_stream(dev))
     if code:
         raise MloraError(code, "mlora_dequantize_mxfp4")
-    return y
+    return out
 
 
 def linear_mxfp4(x, W, w_scale, pool: Pool, seg_start=None, seg_adapter=None, seg_rank=None, seg_scale=None,
