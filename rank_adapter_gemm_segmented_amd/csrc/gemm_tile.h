@@ -456,9 +456,12 @@ struct PipeSrcMx {
 // kWMx: a row block's codes of the whole stage are one 16-byte read past the boundary,
 // converted for k-step kk + 1 while k-step kk is multiplied (four conversions where
 // bf16 W has a 16-byte LDS read); x alone fills the rings, in three stages.
-template <class C>
+//
+// meanwhile(): run once the first loads are requested, while they are in flight (it
+// may use the LDS behind MAIN_BYTES).
+template <class C, class Meanwhile>
 __device__ __forceinline__ void pipe_mainloop_mx(const PipeSrcMx<C>& s, int d_in, const void* zeros, char* lds,
-                                                 int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
+                                                 int wave, int lane, f32x16_t (&acc)[C::MR][C::MT], Meanwhile meanwhile) {
   constexpr bool XMX = C::kWQ == kWMxX;
   constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX, KS = 4;
   static_assert(KB == (XMX ? 256 : 64), "4 k-steps");
@@ -583,6 +586,7 @@ __device__ __forceinline__ void pipe_mainloop_mx(const PipeSrcMx<C>& s, int d_in
 #pragma unroll
   for (int t = -NB; t < -1; ++t) request(part, t, std::integral_constant<int, 0>{}, std::integral_constant<int, NL>{});
   request(part, -1, std::integral_constant<int, 0>{}, std::integral_constant<int, D1>{});
+  meanwhile();
   vm_barrier<VMC + D1>();
 #pragma unroll
   for (int f = 0; f < NT0; ++f) first(0, f);

@@ -212,7 +212,7 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0,
     PipeSrcMx<C> src;
     src.set(wave, lane, W + w0 * wrb, x, a.w_mx + 4 * ((long long)e * mx_planes(d_in) * d_out + w0), a.x_mx, 4ll * d_out, 4ll * a.n_rows, d_in,
             [&](int r) { return wrow_of<GATED>(r0 + r, d_out) - w0; }, row_of);
-    pipe_mainloop_mx<C>(src, d_in, expert_zeros, lds, wave, lane, acc);
+    pipe_mainloop_mx<C>(src, d_in, expert_zeros, lds, wave, lane, acc, []() {});
   } else if constexpr (PIPE) {
     // W offsets from the tile's first row (gated: its first gate row; the up
     // rows lie d_out / 2 rows further)

@@ -526,6 +526,18 @@ __global__ __launch_bounds__(256) void k_shrink_short(LinearArgs a) {
 // chunk loads are in flight at once. Every row tile of the GEMM then reads
 // one v per position instead of re-reading the chunk partials.
 // ---------------------------------------------------------------------------
+// Columns j .. j + 3 of a row as bf16 high and low parts (about 16 bits of the value).
+__device__ __forceinline__ void store_split(uint16_t* row, int r_ws, int j, f32x4_t v) {
+  uint32_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    h[i] = cvt_pk_bf16(v[2 * i], v[2 * i + 1]);
+    l[i] = cvt_pk_bf16(v[2 * i] - __uint_as_float(h[i] << 16), v[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+  }
+  *(u32x2_t*)(row + j) = u32x2_t{h[0], h[1]};
+  *(u32x2_t*)(row + r_ws + j) = u32x2_t{l[0], l[1]};
+}
+
 __global__ __launch_bounds__(256) void k_vfinal(LinearArgs a) {
   const int e = blockIdx.x * 256 + threadIdx.x;
   const int q4 = a.r_ws / 4;
@@ -553,7 +565,19 @@ __global__ __launch_bounds__(256) void k_vfinal(LinearArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum[i] = (j + i < rk) ? sum[i] * sc : 0.f;
   }
-  *(f32x4_t*)(a.v_fin + (long long)p * a.r_ws + j) = sum;
+  float* row = a.v_fin + (long long)p * a.r_ws;
+  if (a.v_split) store_split((uint16_t*)row, a.r_ws, j, sum);   // uniform
+  else *(f32x4_t*)(row + j) = sum;
+}
+
+// Rows of v_fin that the shrink left in fp32, as bf16 parts in place (a wave per row).
+__global__ __launch_bounds__(kWave) void k_vsplit(LinearArgs a) {
+  const int j = 4 * threadIdx.x;
+  float* row = a.v_fin + (long long)blockIdx.x * a.r_ws;
+  f32x4_t v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (j < a.r_ws) v = *(const f32x4_t*)(row + j);
+  __syncthreads();   // the row is in registers
+  if (j < a.r_ws) store_split((uint16_t*)row, a.r_ws, j, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -669,6 +693,139 @@ constexpr int kBatch = 8;           // independent loads per thread in bulk LDS 
 constexpr int kEpiRing = 16;        // B operand loads in flight per lane in the expand epilogue
 constexpr int kEpiMaxUnits = 128;   // work units one wave lists per rank chunk (more: further passes)
 
+// Expand of the largest tile over an MXFP4 weight: acc += B_a (scale v) per segment run,
+// by stages of the LDS like the main loop's.
+//
+// With a 4-bit base product the main loop of a prefill tile is short (16 stages for
+// d_in = 4096), and an expand that reads B into registers a few units ahead of its
+// products took a third of the kernel. Here a stage is a run's B, all of the tile's rows
+// by 64 rank columns (32 KB, one request), the tile's v stays in LDS, and the next
+// run's B is in flight while this one is multiplied.
+//
+// LDS: v's high parts [256][64], low parts, two slots of B [256][64]; rows of 128 bytes
+// with the ring's swizzle. Behind them the list: position entries, then the live runs
+// {first, end, adapter, rank}, then their number.
+struct MxExpand {
+  static constexpr int V = 0, VL = 32 * 1024, B = 64 * 1024, SLOT = 32 * 1024;
+  static constexpr int PINFO = 136 * 1024, RUNS = PINFO + 256 * 16, COUNT = RUNS + 256 * 16, END = COUNT + 64;
+};
+
+// The tile's runs, listed while the main loop's first loads are in flight. pi: the
+// thread's position entry.
+__device__ __forceinline__ void mx_list_runs(const LinearArgs& a, char* lds, int t0, int wave, int lane, int4 pi) {
+  int4* pinfo = (int4*)(lds + MxExpand::PINFO);
+  int4* runs = (int4*)(lds + MxExpand::RUNS);
+  int* count = (int*)(lds + MxExpand::COUNT);   // [0..3] runs per wave, [4..7] first starts, [8] all
+  const int t = wave * kWave + lane, teff = min(256, a.T - t0);
+  if (t >= teff || pi.y < 0 || pi.y >= a.pv.capacity || pi.z <= 0) {   // (clamps whatever the table holds)
+    pi.y = -1;
+    pi.z = 0;
+  }
+  if (t >= teff) pi.x = -1;
+  pi.z = min(pi.z, a.pv.max_rank);
+  pinfo[t] = pi;
+  lds_barrier();
+  const bool start = t < teff && (t == 0 || pinfo[t].x != pinfo[max(t - 1, 0)].x);
+  const unsigned long long m = __ballot(start), live = __ballot(start && pi.y >= 0);
+  if (lane == 0) {
+    count[wave] = (int)__popcll(live);
+    count[4 + wave] = m ? wave * kWave + (int)__builtin_ctzll(m) : teff;   // (none: the next wave's, below)
+  }
+  lds_barrier();
+  int before = 0, next = teff;
+  for (int w = 0; w < wave; ++w) before += count[w];
+  for (int w = 3; w > wave; --w)
+    if (count[4 + w] < teff) next = count[4 + w];
+  const unsigned long long above = lane == kWave - 1 ? 0ull : m & (~0ull << (lane + 1));
+  const int end = above ? wave * kWave + (int)__builtin_ctzll(above) : next;
+  if (start && pi.y >= 0) runs[before + (int)__popcll(live & ((1ull << lane) - 1ull))] = make_int4(t, end, pi.y, pi.z);
+  if (t == 0) count[8] = count[0] + count[1] + count[2] + count[3];
+}
+
+template <class C, bool GATED>
+__device__ __forceinline__ void mx_expand(const LinearArgs& a, char* lds, const void* zeros, int t0, int r0, int wave, int lane,
+                                          f32x16_t (&acc)[C::MR][C::MT]) {
+  constexpr int MR = C::MR, MT = C::MT, WR = C::kWR, WT = C::kWT;
+  const int4* runs = (const int4*)(lds + MxExpand::RUNS);
+  const int nr = __builtin_amdgcn_readfirstlane(((const int*)(lds + MxExpand::COUNT))[8]);
+  const int T = a.T, d_out = a.d_out, r_ws = a.r_ws;
+  const int wr = wave / C::NWT, wt = wave % C::NWT, wb = wt * WT, l32 = lane % 32, kh = lane / 32;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  // load j of a stage: rows (4 j + wave) 8 + lane / 8, one 16-byte chunk each
+  const int rl = wave * 8 + lane / 8, c = (lane % 8) ^ gswz<64>(rl);
+  auto run_of = [&](int i) {
+    const int4 d = runs[i];
+    return make_int4(__builtin_amdgcn_readfirstlane(d.x), __builtin_amdgcn_readfirstlane(d.y),
+                     __builtin_amdgcn_readfirstlane(d.z), __builtin_amdgcn_readfirstlane(d.w));
+  };
+  for (int jc0 = 0; jc0 < r_ws; jc0 += 64) {
+    const int col = jc0 + 8 * c;
+    auto next_run = [&](int i) {   // the next of a rank past jc0
+      while (i < nr && __builtin_amdgcn_readfirstlane(runs[i].w) <= jc0) ++i;
+      return i;
+    };
+    auto load_b = [&](int i, int slot) {
+      const int4 d = run_of(i);
+      const uint16_t* b = (const uint16_t*)a.pv.base + (long long)d.z * a.pv.slot_elems + a.pv.b_offset;
+      const bool in = col < round_up8(d.w);   // (columns past the rank are zeros)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = wrow_of<GATED>(r0 + 32 * j + rl, d_out);
+        dma16(sel_addr(in, b + bblk_off(row, col, d_out), zeros), lds0 + MxExpand::B + slot * MxExpand::SLOT + (uint32_t)(4 * j + wave) * 1024);
+      }
+    };
+    int cur = next_run(0), slot = 0;
+    if (cur >= nr) break;          // uniform: no run has as high a rank
+    if (jc0 > 0) lds_barrier();    // (every wave is done with v)
+    load_b(cur, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint16_t* v = (const uint16_t*)(a.v_fin + (long long)min(t0 + 32 * j + rl, T - 1) * r_ws) + col;
+      dma16(sel_addr(col < r_ws, v, zeros), lds0 + MxExpand::V + (uint32_t)(4 * j + wave) * 1024);
+      dma16(sel_addr(col < r_ws, v + r_ws, zeros), lds0 + MxExpand::VL + (uint32_t)(4 * j + wave) * 1024);
+    }
+    while (cur < nr) {             // uniform
+      const int4 d = run_of(cur);
+      const int nxt = next_run(cur + 1);
+      vm_barrier<0>();             // the run's B is there, and the other slot's last reader done
+      if (nxt < nr) load_b(nxt, slot ^ 1);
+      const int n_lo = (max(d.x - wb, 0)) / 32, n_hi = (min(d.y - wb, WT) + 31) / 32;   // position blocks of the run
+      // the wave's rows inside one slice of a fused pool: that slice's columns alone
+      int w0 = 0, w1 = d.w;
+      if (!GATED) slice_window(a.pv, r0 + wr * WR, min(r0 + wr * WR + WR, d_out), d.w, &w0, &w1);
+      const int k_lo = max(w0 - jc0, 0) / 16, k_hi = (min(min(w1, d.w) - jc0, 64) + 15) / 16;
+      if (n_lo < n_hi && k_lo < k_hi) {   // uniform
+        const char* Lb = lds + MxExpand::B + slot * MxExpand::SLOT + (wr * WR + l32) * 128;
+        const char* Lv = lds + MxExpand::V + (wb + l32) * 128;
+        for (int k = k_lo; k < k_hi; ++k) {
+          const int at = ((2 * k + kh) ^ gswz<64>(l32)) * 16;
+          u32x4_t fb[MR], vh[MT], vl[MT];
+#pragma unroll
+          for (int m = 0; m < MR; ++m) fb[m] = *(const u32x4_t*)(Lb + m * 32 * 128 + at);
+#pragma unroll
+          for (int n = 0; n < MT; ++n) {
+            vh[n] = *(const u32x4_t*)(Lv + n * 32 * 128 + at);
+            vl[n] = *(const u32x4_t*)(Lv + MxExpand::VL + n * 32 * 128 + at);
+          }
+#pragma unroll
+          for (int n = 0; n < MT; ++n) {
+            if (n < n_lo || n >= n_hi) continue;   // uniform
+            const int tl = wb + n * 32 + l32;
+            const bool in = tl >= d.x && tl < d.y;
+            const u32x4_t hi = in ? vh[n] : zero_u32x4(), lo = in ? vl[n] : zero_u32x4();
+#pragma unroll
+            for (int m = 0; m < MR; ++m) acc[m][n] = mfma32g(fb[m], hi, acc[m][n]);
+#pragma unroll
+            for (int m = 0; m < MR; ++m) acc[m][n] = mfma32g(fb[m], lo, acc[m][n]);
+          }
+        }
+      }
+      cur = nxt;
+      slot ^= 1;
+    }
+  }
+}
+
 // One workgroup per CU (the LDS stages take most of it): the register
 // allocator may then use the whole register file share of its waves (one
 // wave per SIMD for 4 waves, two for 8).
@@ -691,7 +848,10 @@ void k_gemm2(LinearArgs a) {
   constexpr bool INRING = PIPE || C::LDS_BYTES + LIST_BYTES > 160 * 1024;   // (MXFP4 on both sides: all of it too)
   constexpr int LIST_AT = INRING ? 96 * 1024 : C::LDS_BYTES;
   static_assert(!INRING || (LIST_AT + LIST_BYTES <= C::LDS_BYTES && BT * (64 + 8) * 4 <= LIST_AT), "v and the lists fit the LDS");
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[(C::LDS_BYTES + (INRING ? 0 : LIST_BYTES)) / 2];
+  constexpr bool MXP = PIPE && WQ >= kWMx;          // (expand by stages)
+  static_assert(!MXP || (C::MAIN_BYTES <= MxExpand::PINFO && MxExpand::END <= 160 * 1024), "the list lies behind the rings");
+  constexpr int LDS_ALL = MXP && C::LDS_BYTES < MxExpand::END ? MxExpand::END : C::LDS_BYTES + (INRING ? 0 : LIST_BYTES);
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[LDS_ALL / 2];
   int4* pinfo = (int4*)((char*)lds + LIST_AT);
 
   // wave index made scalar: every per-wave quantity below is then uniform
@@ -748,7 +908,12 @@ void k_gemm2(LinearArgs a) {
               const int row = a.sv.token_index ? a.sv.token_index[p] : p;
               return min(max(row, 0), T - 1);
             });
-    pipe_mainloop_mx<C>(src, d_in, zeros, (char*)lds, wave, lane, acc);
+    int4 pi = make_int4(-1, -1, 0, 0);
+    if (a.lora_on) pi = a.pos_info[min(t0 + tid, T - 1)];
+    pipe_mainloop_mx<C>(src, d_in, zeros, (char*)lds, wave, lane, acc, [&]() {
+      if (a.lora_on) mx_list_runs(a, (char*)lds, t0, wave, lane, pi);
+    });
+    if (a.lora_on) mx_expand<C, GATED>(a, (char*)lds, zeros, t0, r0, wave, lane, acc);
   } else if constexpr (PIPE) {
     const int w0 = wrow_of<GATED>(r0, d_out);
     PipeSrc<C> src;
@@ -946,7 +1111,7 @@ void k_gemm2(LinearArgs a) {
   // the pool straight into MFMA operand registers, a ring of kEpiRing units
   // ahead of the unit being multiplied. (With the dense term of
   // k_expand_delta, added above, none of this runs.)
-  if (a.lora_on && (PIPE || !a.delta)) {
+  if (!MXP && a.lora_on && (PIPE || !a.delta)) {
     const int RC = a.r_ws < 64 ? a.r_ws : 64;        // rank columns per chunk (16, 32 or 64)
     const int VP = RC + 8;                           // hi/lo row pitch (bf16)
     uint16_t* vsh = lds;
@@ -1364,10 +1529,8 @@ void launch_shrink_bf16(const LinearArgs& a, hipStream_t st) {
 // heterogeneous one (82.6-82.9 against 84.7 us, 39.2 against 40.5 us): each
 // CU then keeps twice the waves issuing loads; deeper rings or 2x2-wave
 // shapes did not do better.
-void launch_linear_bf16(const LinearArgs& a, hipStream_t st) {
-  launch_shrink_bf16(a, st);
-  if (a.lora_on && a.delta && a.seg_grid > 0)
-    hipLaunchKernelGGL(k_expand_delta, dim3((a.d_out + kDxRows - 1) / kDxRows, a.T), dim3(kDxThreads), 0, st, a);
+void launch_linear_bf16(const LinearArgs& a0, hipStream_t st) {
+  LinearArgs a = a0;
   auto tiles = [&](int br, int bt) {
     return (long long)((a.d_out + br - 1) / br) * ((a.T + bt - 1) / bt);
   };
@@ -1378,6 +1541,12 @@ void launch_linear_bf16(const LinearArgs& a, hipStream_t st) {
   const bool large = a.T > 128 && tiles(256, 256) >= kFill, epi = a.epi_kind != kEpiNone;
   const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
                     (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
+  a.v_split = a.w_mx && large && near;   // (mx_expand)
+  launch_shrink_bf16(a, st);
+  if (a.lora_on && a.v_split && a.ks == 1)
+    hipLaunchKernelGGL(k_vsplit, dim3(a.T), dim3(kWave), 0, st, a);
+  if (a.lora_on && a.delta && a.seg_grid > 0)
+    hipLaunchKernelGGL(k_expand_delta, dim3((a.d_out + kDxRows - 1) / kDxRows, a.T), dim3(kDxThreads), 0, st, a);
   if (a.w_mx && a.x_mx) {
     if (large && near) launch_g<256, 256, 128, 128, 2, 256, 2, kWMxX>(a, st, true);
     else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 256, 3, kWMxX>(a, st, true);

@@ -38,6 +38,8 @@ struct LinearArgs {
   const uint8_t* w_mx = nullptr;
   const uint8_t* x_codes = nullptr;
   const uint8_t* x_mx = nullptr;
+  // rows of v_fin as bf16 parts, r_ws high ones, then r_ws low ones (set by the GEMM's launcher)
+  int v_split = 0;
 };
 
 constexpr int kEpiNone = 0, kEpiPlain = 1, kEpiGated = 2;
