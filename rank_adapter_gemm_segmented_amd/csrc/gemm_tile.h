@@ -64,6 +64,12 @@ __device__ __forceinline__ void vm_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// The wait alone.
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
 // KB: k per stage (32 or 64). A stage is the tile's BR W rows and its BT
 // positions over KB columns. The stages reach LDS by direct loads into two
 // rings, one for the W rows (NB slots, NB - 1 stages in flight while one is

@@ -693,20 +693,21 @@ constexpr int kBatch = 8;           // independent loads per thread in bulk LDS 
 constexpr int kEpiRing = 16;        // B operand loads in flight per lane in the expand epilogue
 constexpr int kEpiMaxUnits = 128;   // work units one wave lists per rank chunk (more: further passes)
 
-// Expand of the largest tile over an MXFP4 weight: acc += B_a (scale v) per segment run,
-// by stages of the LDS like the main loop's.
+// Expand of the largest tile over an MXFP4 weight: acc += B_a (scale v) per segment run.
 //
 // With a 4-bit base product the main loop of a prefill tile is short (16 stages for
-// d_in = 4096), and an expand that reads B into registers a few units ahead of its
-// products took a third of the kernel. Here a stage is a run's B, all of the tile's rows
-// by 64 rank columns (32 KB, one request), the tile's v stays in LDS, and the next
-// run's B is in flight while this one is multiplied.
+// d_in = 4096), and the expand above took a third of the kernel: its lists, v's way
+// through registers and its B loads each waited for memory in turn. Here the runs are
+// listed under the main loop's first loads, v (as bf16 parts in memory) comes by direct
+// loads, and each wave streams its own units, 16 rank columns of B for its rows, through
+// a ring of its own in the LDS, four units in flight, without a barrier.
 //
-// LDS: v's high parts [256][64], low parts, two slots of B [256][64]; rows of 128 bytes
-// with the ring's swizzle. Behind them the list: position entries, then the live runs
-// {first, end, adapter, rank}, then their number.
+// LDS: v's high parts [256][64], low parts (rows of 128 bytes with the ring's swizzle),
+// the waves' rings. Behind them the list: position entries, then the live runs {first,
+// end, adapter, rank}, then their number.
 struct MxExpand {
-  static constexpr int V = 0, VL = 32 * 1024, B = 64 * 1024, SLOT = 32 * 1024;
+  static constexpr int V = 0, VL = 32 * 1024, B = 64 * 1024;
+  static constexpr int UNITS = 4, UNIT = 4096, RING = UNITS * UNIT;   // (128 rows of 32 bytes)
   static constexpr int PINFO = 136 * 1024, RUNS = PINFO + 256 * 16, COUNT = RUNS + 256 * 16, END = COUNT + 64;
 };
 
@@ -745,84 +746,125 @@ __device__ __forceinline__ void mx_list_runs(const LinearArgs& a, char* lds, int
 template <class C, bool GATED>
 __device__ __forceinline__ void mx_expand(const LinearArgs& a, char* lds, const void* zeros, int t0, int r0, int wave, int lane,
                                           f32x16_t (&acc)[C::MR][C::MT]) {
-  constexpr int MR = C::MR, MT = C::MT, WR = C::kWR, WT = C::kWT;
+  constexpr int MR = C::MR, MT = C::MT, WR = C::kWR, WT = C::kWT, P = MxExpand::UNITS;
+  static_assert(WR == 128 && P == 4, "a unit is four loads");
   const int4* runs = (const int4*)(lds + MxExpand::RUNS);
   const int nr = __builtin_amdgcn_readfirstlane(((const int*)(lds + MxExpand::COUNT))[8]);
+  if (nr == 0) return;             // uniform
   const int T = a.T, d_out = a.d_out, r_ws = a.r_ws;
   const int wr = wave / C::NWT, wt = wave % C::NWT, wb = wt * WT, l32 = lane % 32, kh = lane / 32;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  // load j of a stage: rows (4 j + wave) 8 + lane / 8, one 16-byte chunk each
-  const int rl = wave * 8 + lane / 8, c = (lane % 8) ^ gswz<64>(rl);
-  auto run_of = [&](int i) {
-    const int4 d = runs[i];
-    return make_int4(__builtin_amdgcn_readfirstlane(d.x), __builtin_amdgcn_readfirstlane(d.y),
-                     __builtin_amdgcn_readfirstlane(d.z), __builtin_amdgcn_readfirstlane(d.w));
-  };
+  const uint32_t ring0 = lds0 + MxExpand::B + wave * MxExpand::RING;
+  // load j of a unit: rows 32 j + lane / 2 of the wave's, 16 bytes each
+  uint32_t off[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 32 * j + lane / 2;
+    off[j] = 32u * (uint32_t)wrow_of<GATED>(r0 + wr * WR + r, d_out) + 16u * ((lane % 2) ^ gswz<16>(r));
+  }
+  struct Unit { int run, k, k_hi, first, end, adapter; };   // run == nr: none left
   for (int jc0 = 0; jc0 < r_ws; jc0 += 64) {
-    const int col = jc0 + 8 * c;
-    auto next_run = [&](int i) {   // the next of a rank past jc0
-      while (i < nr && __builtin_amdgcn_readfirstlane(runs[i].w) <= jc0) ++i;
-      return i;
-    };
-    auto load_b = [&](int i, int slot) {
-      const int4 d = run_of(i);
-      const uint16_t* b = (const uint16_t*)a.pv.base + (long long)d.z * a.pv.slot_elems + a.pv.b_offset;
-      const bool in = col < round_up8(d.w);   // (columns past the rank are zeros)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int row = wrow_of<GATED>(r0 + 32 * j + rl, d_out);
-        dma16(sel_addr(in, b + bblk_off(row, col, d_out), zeros), lds0 + MxExpand::B + slot * MxExpand::SLOT + (uint32_t)(4 * j + wave) * 1024);
-      }
-    };
-    int cur = next_run(0), slot = 0;
-    if (cur >= nr) break;          // uniform: no run has as high a rank
-    if (jc0 > 0) lds_barrier();    // (every wave is done with v)
-    load_b(cur, 0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint16_t* v = (const uint16_t*)(a.v_fin + (long long)min(t0 + 32 * j + rl, T - 1) * r_ws) + col;
-      dma16(sel_addr(col < r_ws, v, zeros), lds0 + MxExpand::V + (uint32_t)(4 * j + wave) * 1024);
-      dma16(sel_addr(col < r_ws, v + r_ws, zeros), lds0 + MxExpand::VL + (uint32_t)(4 * j + wave) * 1024);
-    }
-    while (cur < nr) {             // uniform
-      const int4 d = run_of(cur);
-      const int nxt = next_run(cur + 1);
-      vm_barrier<0>();             // the run's B is there, and the other slot's last reader done
-      if (nxt < nr) load_b(nxt, slot ^ 1);
-      const int n_lo = (max(d.x - wb, 0)) / 32, n_hi = (min(d.y - wb, WT) + 31) / 32;   // position blocks of the run
-      // the wave's rows inside one slice of a fused pool: that slice's columns alone
-      int w0 = 0, w1 = d.w;
-      if (!GATED) slice_window(a.pv, r0 + wr * WR, min(r0 + wr * WR + WR, d_out), d.w, &w0, &w1);
-      const int k_lo = max(w0 - jc0, 0) / 16, k_hi = (min(min(w1, d.w) - jc0, 64) + 15) / 16;
-      if (n_lo < n_hi && k_lo < k_hi) {   // uniform
-        const char* Lb = lds + MxExpand::B + slot * MxExpand::SLOT + (wr * WR + l32) * 128;
-        const char* Lv = lds + MxExpand::V + (wb + l32) * 128;
-        for (int k = k_lo; k < k_hi; ++k) {
-          const int at = ((2 * k + kh) ^ gswz<64>(l32)) * 16;
-          u32x4_t fb[MR], vh[MT], vl[MT];
-#pragma unroll
-          for (int m = 0; m < MR; ++m) fb[m] = *(const u32x4_t*)(Lb + m * 32 * 128 + at);
-#pragma unroll
-          for (int n = 0; n < MT; ++n) {
-            vh[n] = *(const u32x4_t*)(Lv + n * 32 * 128 + at);
-            vl[n] = *(const u32x4_t*)(Lv + MxExpand::VL + n * 32 * 128 + at);
-          }
-#pragma unroll
-          for (int n = 0; n < MT; ++n) {
-            if (n < n_lo || n >= n_hi) continue;   // uniform
-            const int tl = wb + n * 32 + l32;
-            const bool in = tl >= d.x && tl < d.y;
-            const u32x4_t hi = in ? vh[n] : zero_u32x4(), lo = in ? vl[n] : zero_u32x4();
-#pragma unroll
-            for (int m = 0; m < MR; ++m) acc[m][n] = mfma32g(fb[m], hi, acc[m][n]);
-#pragma unroll
-            for (int m = 0; m < MR; ++m) acc[m][n] = mfma32g(fb[m], lo, acc[m][n]);
-          }
+    // the next run from i on that meets the wave's positions and rank columns
+    auto seek = [&](int i) {
+      Unit u{nr, 0, 0, 0, 0, 0};
+      for (; i < nr; ++i) {        // uniform
+        const int4 d = runs[i];
+        u.first = __builtin_amdgcn_readfirstlane(d.x);
+        u.end = __builtin_amdgcn_readfirstlane(d.y);
+        u.adapter = __builtin_amdgcn_readfirstlane(d.z);
+        const int rank = __builtin_amdgcn_readfirstlane(d.w);
+        if (u.first >= wb + WT) break;
+        // (the wave's rows inside one slice of a fused pool: that slice's columns alone)
+        int w0 = 0, w1 = rank;
+        if (!GATED) slice_window(a.pv, r0 + wr * WR, min(r0 + wr * WR + WR, d_out), rank, &w0, &w1);
+        u.k = max(w0 - jc0, 0) / 16;
+        u.k_hi = (min(min(w1, rank) - jc0, 64) + 15) / 16;
+        if (u.end > wb && u.k < u.k_hi) {
+          u.run = i;
+          return u;
         }
       }
-      cur = nxt;
-      slot ^= 1;
+      u.run = nr;
+      return u;
+    };
+    auto after = [&](Unit u) {
+      if (++u.k < u.k_hi) return u;
+      return seek(u.run + 1);
+    };
+    auto load = [&](const Unit& u, int slot) {
+      const uint32_t at = ring0 + (uint32_t)slot * MxExpand::UNIT;
+      if (u.run < nr) {            // uniform
+        const uint16_t* b = (const uint16_t*)a.pv.base + (long long)u.adapter * a.pv.slot_elems + a.pv.b_offset +
+                            (long long)(jc0 / 16 + u.k) * d_out * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dma16_off(b, off[j], at + j * 1024);
+      } else {                     // (as many loads, so that the waits stay exact)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dma16(zeros, at + j * 1024);
+      }
+    };
+    if (jc0 > 0) lds_barrier();    // (every wave is done with v)
+    Unit ahead = seek(0);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      load(ahead, i);
+      if (ahead.run < nr) ahead = after(ahead);
     }
+    {                              // v: rows (4 j + wave) 8 + lane / 8, one 16-byte chunk each
+      const int rl = wave * 8 + lane / 8, col = jc0 + 8 * ((lane % 8) ^ gswz<64>(rl));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint16_t* v = (const uint16_t*)(a.v_fin + (long long)min(t0 + 32 * j + rl, T - 1) * r_ws) + col;
+        dma16(sel_addr(col < r_ws, v, zeros), lds0 + MxExpand::V + (uint32_t)(4 * j + wave) * 1024);
+        dma16(sel_addr(col < r_ws, v + r_ws, zeros), lds0 + MxExpand::VL + (uint32_t)(4 * j + wave) * 1024);
+      }
+    }
+    vm_barrier<0>();
+    const char* Lb = lds + MxExpand::B + wave * MxExpand::RING + l32 * 32 + (kh ^ gswz<16>(l32)) * 16;
+    const char* Lv = lds + MxExpand::V + (wb + l32) * 128;
+    u32x4_t fb[2][MR], vh[2][MT], vl[2][MT];
+    auto read = [&](const Unit& u, int slot, int set) {
+      const int at = ((2 * u.k + kh) ^ gswz<64>(l32)) * 16;
+#pragma unroll
+      for (int m = 0; m < MR; ++m) fb[set][m] = *(const u32x4_t*)(Lb + slot * MxExpand::UNIT + m * 1024);
+#pragma unroll
+      for (int n = 0; n < MT; ++n) {
+        vh[set][n] = *(const u32x4_t*)(Lv + n * 32 * 128 + at);
+        vl[set][n] = *(const u32x4_t*)(Lv + MxExpand::VL + n * 32 * 128 + at);
+      }
+    };
+    auto multiply = [&](const Unit& u, int set) {
+      const int n_lo = max(u.first - wb, 0) / 32, n_hi = (min(u.end - wb, WT) + 31) / 32;   // position blocks of the run
+#pragma unroll
+      for (int n = 0; n < MT; ++n) {
+        if (n < n_lo || n >= n_hi) continue;   // uniform
+        const int tl = wb + n * 32 + l32;
+        const bool in = tl >= u.first && tl < u.end;
+        const u32x4_t hi = in ? vh[set][n] : zero_u32x4(), lo = in ? vl[set][n] : zero_u32x4();
+#pragma unroll
+        for (int m = 0; m < MR; ++m) acc[m][n] = mfma32g(fb[set][m], hi, acc[m][n]);
+#pragma unroll
+        for (int m = 0; m < MR; ++m) acc[m][n] = mfma32g(fb[set][m], lo, acc[m][n]);
+      }
+    };
+    Unit cur = seek(0);
+    if (cur.run < nr) read(cur, 0, 0);
+    int i = 0;                     // unit in slot i % P and fragment set i % 2
+    auto step = [&](auto set) {    // false: that was the last
+      constexpr int S = decltype(set)::value;
+      const Unit nxt = after(cur);
+      vm_wait<4 * (P - 2)>();      // unit i + 1 is there (and this one's fragments)
+      load(ahead, i % P);
+      if (ahead.run < nr) ahead = after(ahead);
+      if (nxt.run < nr) read(nxt, (i + 1) % P, S ^ 1);
+      multiply(cur, S);
+      cur = nxt;
+      ++i;
+      return cur.run < nr;
+    };
+    if (cur.run < nr)
+      while (step(std::integral_constant<int, 0>{}) && step(std::integral_constant<int, 1>{})) {}
+    vm_wait<0>();                  // (no load lands in a slot or in what follows)
   }
 }
 
