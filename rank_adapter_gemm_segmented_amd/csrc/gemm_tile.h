@@ -384,6 +384,13 @@ __device__ __forceinline__ void pipe_mainloop(const PipeSrc<C>& s, int d_in, con
   vm_barrier<0>();   // the ring's last loads (zeros) land before the LDS is reused
 }
 
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ long long uniform64(long long v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((unsigned long long)v >> 32));
+  return (long long)(((unsigned long long)hi << 32) | lo);
+}
+
 // The rows of the largest tile with MXFP4 operands: as PipeSrc, and the scales, a dword
 // per row and plane. What a stage needs of scales is entries 0 .. SCALES - 1: W's rows
 // (kWMxX: those of its first plane, then of its second), then the positions'. Load i
@@ -401,12 +408,12 @@ struct PipeSrcMx {
   template <class WRow, class XRow>
   __device__ __forceinline__ void set(int wave, int lane, const void* w, const void* x, const void* ws, const void* xs, long long wplane_,
                                       long long xplane_, int d_in, WRow wrow, XRow xrow) {   // rows: from the bases' first
-    wb = (const char*)w;
-    xb = (const char*)x;
-    wsb = (const char*)ws;
-    xsb = (const char*)xs;
-    wplane = wplane_;
-    xplane = xplane_;
+    wb = (const char*)uniform64((long long)w);
+    xb = (const char*)uniform64((long long)x);
+    wsb = (const char*)uniform64((long long)ws);
+    xsb = (const char*)uniform64((long long)xs);
+    wplane = uniform64(wplane_);
+    xplane = uniform64(xplane_);
     const uint32_t wrb = (uint32_t)d_in / 2, xrb = C::kWQ == kWMxX ? (uint32_t)d_in / 2 : 2u * d_in;
     // (a row's swizzle does not go by the load: 4 chunks of rows are a multiple of 16 rows)
     const int cw = (lane % WCPR) ^ gswz<C::WRB / 2>(wave * WRPC + lane / WCPR);
@@ -818,6 +825,133 @@ __device__ __forceinline__ void store_epilogue(f32x16_t (&acc)[C::MR][C::MT], ch
       };
       if (vec && !res) finish(std::true_type{});   // uniform
       else finish(std::false_type{});
+    }
+  }
+}
+
+// Accumulators as the vector ALUs read them: kept in the accumulation registers and
+// copied one at a time. (Read as ordinary values, the compiler brings as many of them
+// as it can into vector registers at once, 256 and more, and no address is left one.)
+// acc_settle: after the last product, whose result the copies must not overtake (at most
+// 18 wait states); it depends on every accumulator.
+template <int MT>
+__device__ __forceinline__ void acc_settle(f32x16_t (&acc)[MT]) {
+#pragma unroll
+  for (int n = 0; n < MT; n += 2)
+    asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc[n]), "+a"(acc[n + 1]));
+}
+__device__ __forceinline__ float acc_read(float a) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+
+// The same for tiles over an MXFP4 weight, with everything but the stores before the
+// transposition: a lane's accumulators hold runs of 4 features of one position, gate
+// and up rows in registers v and v + 8, so bias, activation and gate need no other
+// lane. What passes through the LDS is then y itself in bf16, an eighth (gated) or a
+// quarter of the bytes that the fp32 tile above moves, all of the wave's tile at once,
+// and a wave stores whole rows of it (128 bytes gated). A residual comes the same way, by
+// whole rows into the tile first. Prefill gate|up: 12.2 us of a tile's 60 were store_epilogue's.
+template <class C, bool GATED, class RowOf>
+__device__ __forceinline__ void store_epilogue_mx(f32x16_t (&acc)[C::MR][C::MT], char* lds, int wave, int lane, int v0, int p0,
+                                                  int p_end, int d_out, const EpiView& epi, void* y_, RowOf row_of) {
+  constexpr int YW = GATED ? C::kWR / 2 : C::kWR, PITCH = 2 * YW + 16;   // features of the wave, tile row (bytes)
+  constexpr int CPR = YW / 8, PPP = kWave / CPR;         // lanes per position, positions per step
+  static_assert(C::kWT % PPP == 0, "whole steps");
+  const int l32 = lane % 32, h = lane / 32;
+  const int d_y = GATED ? d_out / 2 : d_out, f0 = GATED ? v0 / 2 : v0;
+  char* tile = lds + wave * C::kWT * PITCH;
+  const int tl0 = lane / CPR, col = f0 + 8 * (lane % CPR);
+  const bool whole = col + 8 <= d_y;
+  uint16_t* y = (uint16_t*)y_;
+  const uint16_t* res = (const uint16_t*)epi.residual;
+  if (res) {   // uniform
+#pragma unroll 4
+    for (int tb = 0; tb < C::kWT; tb += PPP) {
+      const int p = p0 + tb + tl0;
+      u32x4_t r = zero_u32x4();
+      if (p < p_end && col < d_y) {
+        const uint16_t* src = res + (long long)row_of(p) * d_y + col;
+        if (whole) {
+          r = *(const u32x4_any*)src;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (col + e < d_y) r[e / 2] |= (uint32_t)src[e] << (16 * (e & 1));
+        }
+      }
+      *(u32x4_t*)(tile + (tb + tl0) * PITCH + 16 * (lane % CPR)) = r;
+    }
+  }
+  // (wave-private tile: the wave's own LDS writes are ordered before its reads)
+  constexpr int NQ = GATED ? 2 : 4;                      // runs of 4 features per row block
+#pragma unroll
+  for (int m = 0; m < C::MR; ++m) acc_settle(acc[m]);
+  // (the choices of activation and residual around the whole tile: branches between
+  // its blocks took every register)
+  auto finish = [&](auto actc, auto resc) {
+  constexpr int ACT = decltype(actc)::value;
+  constexpr bool RES = decltype(resc)::value;
+#pragma unroll
+  for (int m = 0; m < C::MR; ++m) {
+    float b[4 * NQ], bu[4 * NQ];
+#pragma unroll
+    for (int e = 0; e < 4 * NQ; ++e) {
+      const int v = v0 + 32 * m + 8 * (e / 4) + 4 * h + e % 4;
+      b[e] = epi.bias ? elem_f32<uint16_t>(epi.bias, wrow_of<GATED>(v, d_out)) : 0.f;
+      bu[e] = GATED && epi.bias ? elem_f32<uint16_t>(epi.bias, wrow_of<GATED>(v + 16, d_out)) : 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < C::MT; ++n) {
+      float o[4 * NQ];
+#pragma unroll
+      for (int e = 0; e < 4 * NQ; ++e) o[e] = acc_read(acc[m][n][e]) + b[e];
+      if constexpr (ACT != MLORA_ACT_NONE) {
+#pragma unroll
+        for (int e = 0; e < 4 * NQ; ++e) o[e] = activate<true>(o[e], ACT);
+      }
+      char* at = tile + (n * 32 + l32) * PITCH + 2 * ((GATED ? 16 : 32) * m + 4 * h);
+      if constexpr (GATED) {
+#pragma unroll
+        for (int e = 0; e < 4 * NQ; ++e) o[e] *= acc_read(acc[m][n][8 + e]) + bu[e];
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if constexpr (RES) {
+          const u32x2_t r = *(const u32x2_t*)(at + 16 * q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[4 * q + i] += __uint_as_float((i & 1) ? (r[i / 2] & 0xffff0000u) : (r[i / 2] << 16));
+        }
+        *(u32x2_t*)(at + 16 * q) = u32x2_t{cvt_pk_bf16(o[4 * q], o[4 * q + 1]), cvt_pk_bf16(o[4 * q + 2], o[4 * q + 3])};
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  };
+  auto with = [&](auto resc) {   // uniform
+    switch (epi.act) {
+      case MLORA_ACT_NONE: finish(std::integral_constant<int, MLORA_ACT_NONE>{}, resc); break;
+      case MLORA_ACT_RELU: finish(std::integral_constant<int, MLORA_ACT_RELU>{}, resc); break;
+      case MLORA_ACT_SILU: finish(std::integral_constant<int, MLORA_ACT_SILU>{}, resc); break;
+      case MLORA_ACT_GELU: finish(std::integral_constant<int, MLORA_ACT_GELU>{}, resc); break;
+      default: finish(std::integral_constant<int, MLORA_ACT_GELU_TANH>{}, resc);
+    }
+  };
+  if (res) with(std::true_type{});
+  else with(std::false_type{});
+#pragma unroll 4
+  for (int tb = 0; tb < C::kWT; tb += PPP) {
+    const int p = p0 + tb + tl0;
+    if (p >= p_end || col >= d_y) continue;
+    const u32x4_t v = *(const u32x4_t*)(tile + (tb + tl0) * PITCH + 16 * (lane % CPR));
+    uint16_t* dst = y + (long long)row_of(p) * d_y + col;
+    if (whole) {
+      *(u32x4_any*)dst = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < d_y) dst[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
     }
   }
 }
