@@ -365,16 +365,17 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
 
 // ---------------------------------------------------------------------------
 // stream, whole d_in: for a few tokens on wide layers (with an epilogue). A
-// workgroup takes 32 (virtual) rows of W over the whole of d_in, its 8 waves a
+// workgroup takes 16 NR (virtual) rows of W over the whole of d_in, its NW waves a
 // part of d_in each (stream_tile.h), and adds their sums in wave order: no split
 // of d_in over workgroups, one partial tile per row tile for k_finish.
 // The first blocks are the shrink units, 16 rank rows of one segment each, which
-// leave one partial of v per wave and the position table, as k_stream does.
+// leave eight partials of v and the position table, as k_stream does.
+//
+// 32 rows and 8 waves; MXFP4 64 rows and 4 waves, which read x half as often per byte
+// of W.
 // ---------------------------------------------------------------------------
-constexpr int kWideWaves = 8;
-
-template <int WQ, bool GATED>
-__global__ __launch_bounds__(kWideWaves * kWave) void k_stream_wide(DecodeArgs a, int n_units) {
+template <int WQ, bool GATED, int NR, int NW>
+__global__ __launch_bounds__(NW * kWave) void k_stream_wide(DecodeArgs a, int n_units) {
   constexpr int TYPE = WQ == kWMx ? kXMx : WQ == kWFp8 ? kXFp8w : kXBf16;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int l16 = lane % 16, g = lane / 16;
@@ -395,7 +396,7 @@ __global__ __launch_bounds__(kWideWaves * kWave) void k_stream_wide(DecodeArgs a
     if (j0 == 0) {   // the rank the expand applies: capped by the registered one
       const int r = live ? min(rr, a.pv.rank[ad0]) : 0;
       const int ad = r > 0 ? ad0 : -1;
-      for (int t = ps + tid; t < pe; t += kWideWaves * kWave)
+      for (int t = ps + tid; t < pe; t += NW * kWave)
         a.pos[t] = make_int4(ad, ad >= 0 ? r : 0, __float_as_int(ad >= 0 ? sv.seg_scale[s] : 0.f), 0);
     }
     const int rows = min(rr - j0, 16);
@@ -403,21 +404,23 @@ __global__ __launch_bounds__(kWideWaves * kWave) void k_stream_wide(DecodeArgs a
     const char* A = (const char*)a.pv.base + ((long long)ad0 * a.pv.slot_elems + (long long)j0 * d_in) * 2;
     const uint32_t ao[1] = {(uint32_t)min(l16, rows - 1) * (uint32_t)(d_in * 2) + 16 * g};
     const char* xp[1] = {xrow + 16 * g};
-    f32x4_t v[1][1];
-    stream_product<kXBf16, 1, 1, kWideWaves, false>(A, 0, ao, xp, d_in, wave, g, v);
-    float* vp = a.v_part + ((long long)wave * T + l16) * a.r_ws + j0;
+    for (int w = wave; w < kDecWaves; w += NW) {
+      f32x4_t v[1][1];
+      stream_product<kXBf16, 1, 1, kDecWaves, false>(A, 0, ao, xp, d_in, w, g, v);
+      float* vp = a.v_part + ((long long)w * T + l16) * a.r_ws + j0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = 4 * g + i;
-      if (j < rows && l16 >= ps && l16 < pe) vp[j] = v[0][0][i];
+      for (int i = 0; i < 4; ++i) {
+        const int j = 4 * g + i;
+        if (j < rows && l16 >= ps && l16 < pe) vp[j] = v[0][0][i];
+      }
     }
     return;
   }
-  __shared__ f32x4_t red[kWideWaves][2][kWave];
+  __shared__ f32x4_t red[NW][NR][kWave];
   const long long wrb = w_row_bytes<TYPE>(d_in);
-  const int v0 = 32 * (b - n_units);
+  const int v0 = 16 * NR * (b - n_units);
   const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out, fb = min(f0, nf - 1);
-  constexpr int NO = GATED ? 1 : 2;
+  constexpr int NO = GATED ? NR / 2 : NR;
   const char* wbase = (const char*)a.W + fb * wrb;
   uint32_t wo[NO], so[NO];
 #pragma unroll
@@ -427,23 +430,23 @@ __global__ __launch_bounds__(kWideWaves * kWave) void k_stream_wide(DecodeArgs a
     so[r] = 4 * f;
   }
   const char* xp[1] = {xrow + x_group_bytes<TYPE>() * g};
-  f32x4_t acc[2][1];
+  f32x4_t acc[NR][1];
   if constexpr (TYPE == kXMx) {
     const MxScales ms{(const char*)a.w_mx + 4ll * fb, 4ll * nf, 4ll * d_out, 0};
-    stream_product_mx<TYPE, 2, 1, kWideWaves, GATED>(wbase, nf * wrb, wo, xp, ms, so, nullptr, d_in, wave, g, acc);
+    stream_product_mx<TYPE, NR, 1, NW, GATED>(wbase, nf * wrb, wo, xp, ms, so, nullptr, d_in, wave, g, acc);
   } else {
-    stream_product<TYPE, 2, 1, kWideWaves, GATED>(wbase, nf * wrb, wo, xp, d_in, wave, g, acc);
+    stream_product<TYPE, NR, 1, NW, GATED>(wbase, nf * wrb, wo, xp, d_in, wave, g, acc);
   }
-  red[wave][0][lane] = acc[0][0];
-  red[wave][1][lane] = acc[1][0];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) red[wave][r][lane] = acc[r][0];
   __syncthreads();
-  if (tid < 2 * kWave) {
+  if (tid < NR * kWave) {
     f32x4_t sum = red[0][wave][lane];
 #pragma unroll
-    for (int w = 1; w < kWideWaves; ++w)
+    for (int w = 1; w < NW; ++w)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] += red[w][wave][lane][i];
-    *(f32x4_t*)(a.ypart + part_off(0, v0 / 64, v0 / 32 % 2 * 2 + wave, 0, a.n_tiles, 1) + lane * 4) = sum;
+    *(f32x4_t*)(a.ypart + part_off(0, v0 / 64, v0 / 16 % 4 + wave, 0, a.n_tiles, 1) + lane * 4) = sum;
   }
 }
 
@@ -774,7 +777,8 @@ static void launch_decode_epi(DecodeArgs a, hipStream_t st) {
       if (a.T <= kWideTokens && a.n_tiles >= kWideTiles) {
         a.n_chunks = 1;   // what k_finish adds up
         const int units = a.lora_on ? a.sv.n_seg * ((a.pv.max_rank + 15) / 16) : 0;
-        hipLaunchKernelGGL((k_stream_wide<WQ, GATED>), dim3(units + 2 * a.n_tiles), dim3(kWideWaves * kWave), 0, st, a, units);
+        constexpr int NR = WQ == kWMx ? 4 : 2, NW = WQ == kWMx ? 4 : 8;
+        hipLaunchKernelGGL((k_stream_wide<WQ, GATED, NR, NW>), dim3(units + 4 / NR * a.n_tiles), dim3(NW * kWave), 0, st, a, units);
         done = true;
       }
     }
