@@ -433,7 +433,8 @@ __global__ __launch_bounds__(NW * kWave) void k_stream_wide(DecodeArgs a, int n_
   f32x4_t acc[NR][1];
   if constexpr (TYPE == kXMx) {
     const MxScales ms{(const char*)a.w_mx + 4ll * fb, 4ll * nf, 4ll * d_out, 0};
-    stream_product_mx<TYPE, NR, 1, NW, GATED>(wbase, nf * wrb, wo, xp, ms, so, nullptr, d_in, wave, g, acc);
+    stream_product_mx<TYPE, NR, 1, NW, GATED>(wbase, nf * wrb, wo, ms, so, [&](int) { return xp[0]; }, [](int) { return (const char*)nullptr; },
+                                              d_in, wave, g, acc);
   } else {
     stream_product<TYPE, NR, 1, NW, GATED>(wbase, nf * wrb, wo, xp, d_in, wave, g, acc);
   }

@@ -55,15 +55,13 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
   uint32_t wo[NO];
 #pragma unroll
   for (int r = 0; r < NO; ++r) wo[r] = (uint32_t)min(16 * r + l16, nf - 1 - f0) * (uint32_t)wrb + 16 * g;
-  const char* xp[NTB];
-  const char* xsp[NTB];                                            // (kXMxX: the rows' scales)
+  int row[NTB];
 #pragma unroll
   for (int t = 0; t < NTB; ++t) {
     const int p = min(p0 + 16 * t + l16, p1 - 1);                  // (absent positions repeat the last)
-    const int row = min(max(a.token_index ? a.token_index[p] : p, 0), a.n_rows - 1);
-    xp[t] = (const char*)a.x + row * xrb + x_group_bytes<TYPE>() * g;
-    xsp[t] = (const char*)a.x_mx + 4ll * row;
+    row[t] = a.token_index ? a.token_index[p] : p;
   }
+  auto xrow = [&](int t) { return (const char*)a.x + min(max(row[t], 0), a.n_rows - 1) * xrb + x_group_bytes<TYPE>() * g; };
 
   f32x4_t acc[NR][NTB];
   if constexpr (TYPE >= kXMx) {
@@ -71,8 +69,12 @@ __global__ __launch_bounds__(NW * kWave) void k_experts_stream(ExpertsArgs a) {
 #pragma unroll
     for (int r = 0; r < NO; ++r) so[r] = 4u * (uint32_t)min(16 * r + l16, nf - 1 - f0);
     const MxScales ms{(const char*)a.w_mx + 4 * ((long long)e * mx_planes(d_in) * d_out + f0), 4ll * nf, 4ll * d_out, 4ll * a.n_rows};
-    stream_product_mx<TYPE, NR, NTB, NW, GATED>(wbase, up, wo, xp, ms, so, xsp, d_in, wave, g, acc);
+    stream_product_mx<TYPE, NR, NTB, NW, GATED>(
+        wbase, up, wo, ms, so, xrow, [&](int t) { return (const char*)a.x_mx + 4ll * min(max(row[t], 0), a.n_rows - 1); }, d_in, wave, g, acc);
   } else {
+    const char* xp[NTB];
+#pragma unroll
+    for (int t = 0; t < NTB; ++t) xp[t] = xrow(t);
     stream_product<TYPE, NR, NTB, NW, GATED>(wbase, up, wo, xp, d_in, wave, g, acc);
   }
 #pragma unroll
@@ -517,7 +519,7 @@ static void launch_mx(const ExpertsArgs& a, hipStream_t st) {
     if (mean > 12) launch_stream_n<TYPE, 2, 4, 4>(a, st);
     else if (XMX && mean <= 4 && a.d_in >= 4096) launch_stream_n<TYPE, 2, 1, 8>(a, st);
     else if (tiles(64, 16) < 512) launch_stream_n<TYPE, 2, 1, 2>(a, st);
-    else if (XMX || mean <= 5) launch_stream_n<TYPE, 4, 1, 4>(a, st);
+    else if (XMX || mean <= 5 || a.d_in <= 2048) launch_stream_n<TYPE, 4, 1, 4>(a, st);
     else launch_stream_n<TYPE, 8, 1, 4>(a, st);
   } else if (mean <= 20) {
     launch_tile<Mx32<XMX>>(a, st);

@@ -134,17 +134,19 @@ __device__ __forceinline__ void stream_product(const char* wbase, long long up, 
 // become four bf16 operands of 8 columns; kXMxX: the matrix unit takes both sides'
 // codes and scales.
 //
-// sbase: plane 0 of W's scales at the first row (gated: `sup` bytes further those of the up
-// rows), so[]: byte offsets as wo[], splane: from a plane to the next. xsp[], xsplane:
-// the same for x (kXMxX).
+// sbase: plane 0 of W's scales at the first row (gated: `sup` bytes further those of the
+// up rows), so[]: byte offsets as wo[], splane: from a plane to the next. xrow(t): the
+// lane's row of x of position block t, at group g's columns; xscale(t), xsplane: its
+// scales (kXMxX). They are asked for once W's first loads are requested: which row it is
+// may itself be on its way.
 struct MxScales {
   const char* sbase;
   long long sup, splane, xsplane;
 };
-template <int TYPE, int NR, int NTB, int NW, bool GATED>
-__device__ __forceinline__ void stream_product_mx(const char* wbase, long long up, const uint32_t* wo, const char* const* xp,
-                                                  const MxScales& ms, const uint32_t* so, const char* const* xsp, int d_in,
-                                                  int wave, int g, f32x4_t (&acc)[NR][NTB]) {
+template <int TYPE, int NR, int NTB, int NW, bool GATED, class XRow, class XScale>
+__device__ __forceinline__ void stream_product_mx(const char* wbase, long long up, const uint32_t* wo, const MxScales& ms,
+                                                  const uint32_t* so, XRow xrow, XScale xscale, int d_in, int wave, int g,
+                                                  f32x4_t (&acc)[NR][NTB]) {
   static_assert(TYPE == kXMx || TYPE == kXMxX, "MXFP4");
   constexpr int UC = 256;                                          // columns per unit
   constexpr int XL = TYPE == kXMx ? 4 : 1;                         // x loads per W load
@@ -156,7 +158,9 @@ __device__ __forceinline__ void stream_product_mx(const char* wbase, long long u
 
   u32x4_t w[2][NR], x[2][XL][NTB];
   uint32_t sw[2][NR], sx[2][NTB];
-  auto load = [&](int u, auto whole) {                             // unit u; not whole: columns past d_in are zero
+  const char* xp[NTB];
+  const char* xsp[NTB];
+  auto load_w = [&](int u, auto whole) {                           // unit u; not whole: columns past d_in are zero
     const char* wu = wbase + (long long)u * 128;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -168,6 +172,12 @@ __device__ __forceinline__ void stream_product_mx(const char* wbase, long long u
         w[h][r] = in ? ld16((GATED && (r & 1) ? wu + up : wu) + o + 64 * h) : zero_u32x4();
         sw[h][r] = in ? *(const uint32_t*)((GATED && (r & 1) ? su + ms.sup : su) + so[GATED ? r / 2 : r]) : 0u;
       }
+    }
+  };
+  auto load_x = [&](int u, auto whole) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = decltype(whole)::value || u * UC + h * 128 + 32 * g < d_in;
 #pragma unroll
       for (int i = 0; i < XL; ++i)
 #pragma unroll
@@ -201,17 +211,27 @@ __device__ __forceinline__ void stream_product_mx(const char* wbase, long long u
   };
   const int nu = d_in / UC;                                        // whole units
   const int ub = nu * wave / NW, ue = nu * (wave + 1) / NW;        // this wave's
-  if (ub < ue) {   // uniform
-    load(ub, std::true_type{});
+  const bool tail = nu * UC < d_in && wave == NW - 1;              // (the columns behind the last whole unit)
+  if (ub < ue) load_w(ub, std::true_type{});                       // uniform
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int t = 0; t < NTB; ++t) {
+    xp[t] = xrow(t);
+    xsp[t] = xscale(t);
+  }
+  if (ub < ue) {
+    load_x(ub, std::true_type{});
     for (int u = ub; u + 1 < ue; ++u) {
       multiply();
-      load(u + 1, std::true_type{});
+      load_w(u + 1, std::true_type{});
+      load_x(u + 1, std::true_type{});
       __builtin_amdgcn_sched_barrier(0);
     }
     multiply();
   }
-  if (nu * UC < d_in && wave == NW - 1) {   // uniform: the columns behind the last whole unit
-    load(nu, std::false_type{});
+  if (tail) {   // uniform
+    load_w(nu, std::false_type{});
+    load_x(nu, std::false_type{});
     multiply();
   }
 }
