@@ -270,8 +270,10 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
     // faster in both passes from 48 tokens and the decode pair below. Both
     // passes of a shape and token count take the same path, so a zero B
     // reproduces the LoRA-off bits.
-    const bool wide = T >= 48 && pool->d_out >= 8192;
-    const bool dec_ok = decode_supported(T, lora_on ? sv.n_seg : 0, pool->d_out, pool->max_rank) && !a.x_mx;
+    // (MXFP4: also from 17 tokens on very wide layers, 32 tokens, 4096 -> 2 x 14336 gated: 42 us
+    // and 33)
+    const bool wide = (T >= 48 && pool->d_out >= 8192) || (mx && T > 16 && pool->d_out >= 20480);
+    const bool dec_ok = decode_supported(T, lora_on ? sv.n_seg : 0, pool->d_out, pool->max_rank);
     if (w_scale || (dec_ok && (fp == 1 || (fp == 0 && !wide)))) {
       DecodeArgs d;
       d.x = x;
@@ -294,6 +296,8 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
       d.unit_rows = decode_unit_rows(lora_on ? sv.n_seg : 0, pool->max_rank, d.n_tiles);
       d.w_scale = w_scale;
       d.w_mx = a.w_mx;
+      d.x_codes = a.x_codes;
+      d.x_mx = a.x_mx;
       if (log_calls())
         log_call(w_scale ? "decode-fp8w" : mx ? "decode-mxfp4" : "decode", T, pool, sv, lora_on, d.n_chunks, lora_on ? "fused" : "none");
       launch_decode_bf16(d, stream);

@@ -372,18 +372,23 @@ __global__ __launch_bounds__(kDecThreads) void k_stream_bf16(DecodeArgs a) {
 // leave eight partials of v and the position table, as k_stream does.
 //
 // 32 rows and 8 waves; MXFP4 64 rows and 4 waves, which read x half as often per byte
-// of W.
+// of W. WQ = kWMxX (the base product of codes with codes, 32 rows and 8 waves): every
+// batch of up to 64 tokens, in NTB blocks of 16; its x is as few bytes as W, and LDS
+// would have to hold both forms of it, the shrink's being bf16.
 // ---------------------------------------------------------------------------
-template <int WQ, bool GATED, int NR, int NW>
+template <int WQ, bool GATED, int NR, int NW, int NTB>
 __global__ __launch_bounds__(NW * kWave) void k_stream_wide(DecodeArgs a, int n_units) {
-  constexpr int TYPE = WQ == kWMx ? kXMx : WQ == kWFp8 ? kXFp8w : kXBf16;
+  constexpr int TYPE = WQ == kWMxX ? kXMxX : WQ == kWMx ? kXMx : WQ == kWFp8 ? kXFp8w : kXBf16;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave), lane = tid % kWave;
   const int l16 = lane % 16, g = lane / 16;
   const int T = a.T, d_in = a.d_in, d_out = a.d_out;
-  // the lane's token (absent ones repeat the last)
-  int row = min(l16, T - 1);
-  if (a.sv.token_index) row = min(max(a.sv.token_index[row], 0), T - 1);   // uniform
-  const char* xrow = (const char*)a.x + (long long)row * d_in * 2;
+  // the lane's tokens (absent ones repeat the last)
+  int row[NTB];
+#pragma unroll
+  for (int t = 0; t < NTB; ++t) {
+    row[t] = min(16 * t + l16, T - 1);
+    if (a.sv.token_index) row[t] = min(max(a.sv.token_index[row[t]], 0), T - 1);   // uniform
+  }
   const int b = blockIdx.x;
   if (b < n_units) {   // uniform: a shrink unit
     const SegView& sv = a.sv;
@@ -403,20 +408,25 @@ __global__ __launch_bounds__(NW * kWave) void k_stream_wide(DecodeArgs a, int n_
     if (rows <= 0) return;
     const char* A = (const char*)a.pv.base + ((long long)ad0 * a.pv.slot_elems + (long long)j0 * d_in) * 2;
     const uint32_t ao[1] = {(uint32_t)min(l16, rows - 1) * (uint32_t)(d_in * 2) + 16 * g};
-    const char* xp[1] = {xrow + 16 * g};
-    for (int w = wave; w < kDecWaves; w += NW) {
-      f32x4_t v[1][1];
-      stream_product<kXBf16, 1, 1, kDecWaves, false>(A, 0, ao, xp, d_in, w, g, v);
-      float* vp = a.v_part + ((long long)w * T + l16) * a.r_ws + j0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = 4 * g + i;
-        if (j < rows && l16 >= ps && l16 < pe) vp[j] = v[0][0][i];
+    for (int tb = 0; tb < NTB; ++tb) {
+      if (16 * tb + 16 <= ps || 16 * tb >= pe) continue;   // uniform
+      const char* xp[1] = {(const char*)a.x + (long long)row[tb] * d_in * 2 + 16 * g};
+      const int t = 16 * tb + l16;
+      for (int w = wave; w < kDecWaves; w += NW) {
+        f32x4_t v[1][1];
+        stream_product<kXBf16, 1, 1, kDecWaves, false>(A, 0, ao, xp, d_in, w, g, v);
+        float* vp = a.v_part + ((long long)w * T + t) * a.r_ws + j0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 4 * g + i;
+          if (j < rows && t >= ps && t < pe) vp[j] = v[0][0][i];
+        }
       }
     }
     return;
   }
-  __shared__ f32x4_t red[NW][NR][kWave];
+  __shared__ f32x4_t red[NW][NR * NTB][kWave];
   const long long wrb = w_row_bytes<TYPE>(d_in);
   const int v0 = 16 * NR * (b - n_units);
   const int f0 = GATED ? v0 / 2 : v0, nf = GATED ? d_out / 2 : d_out, fb = min(f0, nf - 1);
@@ -429,25 +439,31 @@ __global__ __launch_bounds__(NW * kWave) void k_stream_wide(DecodeArgs a, int n_
     wo[r] = f * (uint32_t)wrb + 16 * g;
     so[r] = 4 * f;
   }
-  const char* xp[1] = {xrow + x_group_bytes<TYPE>() * g};
-  f32x4_t acc[NR][1];
-  if constexpr (TYPE == kXMx) {
-    const MxScales ms{(const char*)a.w_mx + 4ll * fb, 4ll * nf, 4ll * d_out, 0};
-    stream_product_mx<TYPE, NR, 1, NW, GATED>(wbase, nf * wrb, wo, ms, so, [&](int) { return xp[0]; }, [](int) { return (const char*)nullptr; },
-                                              d_in, wave, g, acc);
+  const long long xrb = x_row_bytes<TYPE>(d_in);
+  auto xrow = [&](int t) {
+    return (const char*)(TYPE == kXMxX ? (const void*)a.x_codes : a.x) + row[t] * xrb + x_group_bytes<TYPE>() * g;
+  };
+  f32x4_t acc[NR][NTB];
+  if constexpr (TYPE >= kXMx) {
+    const MxScales ms{(const char*)a.w_mx + 4ll * fb, 4ll * nf, 4ll * d_out, 4ll * T};
+    stream_product_mx<TYPE, NR, NTB, NW, GATED>(wbase, nf * wrb, wo, ms, so, xrow, [&](int t) { return (const char*)a.x_mx + 4ll * row[t]; },
+                                                d_in, wave, g, acc);
   } else {
+    const char* xp[1] = {xrow(0)};
     stream_product<TYPE, NR, 1, NW, GATED>(wbase, nf * wrb, wo, xp, d_in, wave, g, acc);
   }
 #pragma unroll
-  for (int r = 0; r < NR; ++r) red[wave][r][lane] = acc[r][0];
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int t = 0; t < NTB; ++t) red[wave][r * NTB + t][lane] = acc[r][t];
   __syncthreads();
-  if (tid < NR * kWave) {
-    f32x4_t sum = red[0][wave][lane];
+  for (int q = wave; q < NR * NTB; q += NW) {
+    f32x4_t sum = red[0][q][lane];
 #pragma unroll
     for (int w = 1; w < NW; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] += red[w][wave][lane][i];
-    *(f32x4_t*)(a.ypart + part_off(0, v0 / 64, v0 / 16 % 4 + wave, 0, a.n_tiles, 1) + lane * 4) = sum;
+      for (int i = 0; i < 4; ++i) sum[i] += red[w][q][lane][i];
+    *(f32x4_t*)(a.ypart + part_off(0, v0 / 64, v0 / 16 % 4 + q / NTB, q % NTB, a.n_tiles, NTB) + lane * 4) = sum;
   }
 }
 
@@ -770,16 +786,19 @@ template <int TT, int WQ, int EPI>
 static void launch_decode_epi(DecodeArgs a, hipStream_t st) {
   constexpr bool GATED = EPI == kEpiGated;
   const dim3 items(a.n_tiles * a.n_chunks);
-  if constexpr (EPI == kEpiNone) {
+  const int units = a.lora_on ? a.sv.n_seg * ((a.pv.max_rank + 15) / 16) : 0;   // of k_stream_wide
+  if constexpr (WQ == kWMxX) {
+    a.n_chunks = 1;   // what k_finish adds up
+    hipLaunchKernelGGL((k_stream_wide<WQ, GATED, 2, 8, TT / 16>), dim3(units + 2 * a.n_tiles), dim3(8 * kWave), 0, st, a, units);
+  } else if constexpr (EPI == kEpiNone) {
     hipLaunchKernelGGL((k_stream_bf16<TT, WQ, false, true>), items, dim3(kDecThreads), 0, st, a);
   } else {
     bool done = false;
     if constexpr (TT == 16) {
       if (a.T <= kWideTokens && a.n_tiles >= kWideTiles) {
         a.n_chunks = 1;   // what k_finish adds up
-        const int units = a.lora_on ? a.sv.n_seg * ((a.pv.max_rank + 15) / 16) : 0;
         constexpr int NR = WQ == kWMx ? 4 : 2, NW = WQ == kWMx ? 4 : 8;
-        hipLaunchKernelGGL((k_stream_wide<WQ, GATED, NR, NW>), dim3(units + 4 / NR * a.n_tiles), dim3(NW * kWave), 0, st, a, units);
+        hipLaunchKernelGGL((k_stream_wide<WQ, GATED, NR, NW, 1>), dim3(units + 4 / NR * a.n_tiles), dim3(NW * kWave), 0, st, a, units);
         done = true;
       }
     }
@@ -806,7 +825,8 @@ static void launch_decode_tt(const DecodeArgs& a, hipStream_t st) {
 
 template <int TT>
 static void launch_decode_wq(const DecodeArgs& a, hipStream_t st) {
-  if (a.w_mx) launch_decode_tt<TT, kWMx>(a, st);
+  if (a.x_mx) launch_decode_tt<TT, kWMxX>(a, st);
+  else if (a.w_mx) launch_decode_tt<TT, kWMx>(a, st);
   else if (a.w_scale) launch_decode_tt<TT, kWFp8>(a, st);
   else launch_decode_tt<TT, kWBf16>(a, st);
 }

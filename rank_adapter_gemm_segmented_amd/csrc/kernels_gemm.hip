@@ -1584,22 +1584,37 @@ void launch_linear_bf16(const LinearArgs& a0, hipStream_t st) {
   const bool large = a.T > 128 && tiles(256, 256) >= kFill, epi = a.epi_kind != kEpiNone;
   const bool near = 2ll * a.T * a.d_in < (1ll << 32) &&
                     (a.epi_kind == kEpiGated ? 1ll * a.d_out : 512ll) * a.d_in < (1ll << 31);
-  a.v_split = a.w_mx && large && near;   // (mx_expand)
+  a.v_split = a.w_mx && large && near;   // (mx_expand; as many of the largest tiles are no round of smaller ones)
   launch_shrink_bf16(a, st);
   if (a.lora_on && a.v_split && a.ks == 1)
     hipLaunchKernelGGL(k_vsplit, dim3(a.T), dim3(kWave), 0, st, a);
   if (a.lora_on && a.delta && a.seg_grid > 0)
     hipLaunchKernelGGL(k_expand_delta, dim3((a.d_out + kDxRows - 1) / kDxRows, a.T), dim3(kDxThreads), 0, st, a);
+  // MXFP4 weights: the smallest tiles that are one round of the card (a stage is few
+  // bytes and a tile's time its stages' latency, so tiles of 32 and 64 positions in
+  // rings of 4 and 5 stages win as long as every CU has at most one), then the largest
+  // where they fill it. LoRA-on, rank 16, us: 100 tokens, 4096 -> 4096, 36.8 in tiles of 128
+  // rows x 32 positions, 40.7 x 64, 55.6 x 128; 400 tokens, 61.3, 43.3 and 54.2; 200 tokens,
+  // 4096 -> 14336, 56.2 in 256 x 64, 57.0 in 128 x 128, 70.5 in 128 x 64; codes on both
+  // sides: 100 tokens, 4096 -> 4096, 32.0 in 64 x 64, 33.8 in 128 x 64, 39.7 in 128 x 128; 800
+  // tokens, 79.8, 55.4 and 42.5.
+  constexpr long long kRound = 256;
+  auto round = [&](int br, int bt) {
+    const long long rows = a.epi_kind == kEpiGated ? gated_rows(a.d_out) : a.d_out;
+    return (rows + br - 1) / br * ((a.T + bt - 1) / bt) <= kRound;
+  };
   if (a.w_mx && a.x_mx) {
-    if (large && near) launch_g<256, 256, 128, 128, 2, 256, 2, kWMxX>(a, st, true);
-    else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 256, 3, kWMxX>(a, st, true);
-    else launch_g<64, 128, 32, 32, 4, 256, 3, kWMxX>(a, st, true);
+    if (round(64, 64)) launch_g<64, 64, 32, 32, 5, 256, 5, kWMxX>(a, st, true);
+    else if (round(128, 64)) launch_g<128, 64, 32, 32, 4, 256, 4, kWMxX>(a, st, true);
+    else if (large && near) launch_g<256, 256, 128, 128, 2, 256, 2, kWMxX>(a, st, true);
+    else launch_g<128, 128, 64, 32, 3, 256, 3, kWMxX>(a, st, true);
     return;
   }
   if (a.w_mx) {
-    if (large && near) launch_g<256, 256, 128, 128, 3, 64, 3, kWMx>(a, st, true);
-    else if (a.T > 64 && tiles(128, 128) >= kFill) launch_g<128, 128, 64, 32, 3, 128, 3, kWMx>(a, st, true);
-    else launch_g<64, 128, 32, 64, 4, 128, 3, kWMx>(a, st, true);
+    if (round(128, 32)) launch_g<128, 32, 32, 32, 5, 128, 5, kWMx>(a, st, true);
+    else if (round(128, 64)) launch_g<128, 64, 32, 32, 4, 128, 4, kWMx>(a, st, true);
+    else if (large && near) launch_g<256, 256, 128, 128, 3, 64, 3, kWMx>(a, st, true);
+    else launch_g<256, 64, 64, 32, 3, 128, 3, kWMx>(a, st, true);
     return;
   }
   if (large && epi && near) launch_g<256, 256, 128, 128, 3, 64, 2>(a, st, true);

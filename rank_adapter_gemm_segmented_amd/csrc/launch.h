@@ -72,6 +72,8 @@ struct DecodeArgs {
   int unit_rows;   // rank rows per shrink unit (4, 8 or 16)
   const float* w_scale;   // FP8 weight: float32 scale per W row (W holds e4m3 codes); null: not
   const uint8_t* w_mx;    // MXFP4 weight: its scales (W holds codes); null: not
+  const uint8_t* x_codes; // with x_mx, the base product takes these in x's place; null: not
+  const uint8_t* x_mx;
   int epi_kind;           // as in LinearArgs
   EpiView epi;
 };
