@@ -242,7 +242,7 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, int e, int p0,
   const float* ws = C::kW8 ? a.w_scale + (long long)e * d_out : nullptr;
   if constexpr (OUT == 2) {
     store_f32<C>(acc, lds, wave, lane, v0, pw, p1, d_out, (const uint16_t*)epi.bias, ws, (float*)a.y, f32_pitch(d_out));
-  } else if constexpr (PIPE && C::kWQ >= kWMx) {
+  } else if constexpr (PIPE && C::kWQ >= kWMx && C::kBT == 256) {   // (the cut tiles are few, and their compilation long)
     static_assert(C::YT_BYTES <= 160 * 1024, "the tile of y fits the LDS");
     store_epilogue_mx<C, GATED>(acc, lds, wave, lane, v0, pw, p1, d_out, epi, a.y, [](int p) { return p; });
   } else {
