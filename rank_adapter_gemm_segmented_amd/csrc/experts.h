@@ -27,7 +27,7 @@ struct RouteArgs {
 size_t route_workspace_bytes(int T, int E);
 void launch_route(const RouteArgs& a, bool bf16, hipStream_t st);
 
-// ---- products per expert (kernels_experts.hip) ----------------------------------
+// ---- products per expert (experts_kernels.h, kernels_experts*.hip) ----------------------------------
 struct ExpertsArgs {
   const void* x;                // [n_rows, d_in]
   const void* W;                // [E, d_out, d_in]
@@ -42,6 +42,7 @@ struct ExpertsArgs {
   EpiView epi;                  // bias [E, d_out]; no residual
 };
 void launch_experts(const ExpertsArgs& a, bool bf16, hipStream_t st);
+void launch_experts_mx(const ExpertsArgs& a, hipStream_t st);   // (w_mx given)
 
 // Row pitch of the products on the way back: whole vectors of 4, also for odd d_out
 // (columns past it hold anything).
