@@ -700,7 +700,10 @@ constexpr int kEpiMaxUnits = 128;   // work units one wave lists per rank chunk 
 // through registers and its B loads each waited for memory in turn. Here the runs are
 // listed under the main loop's first loads, v (as bf16 parts in memory) comes by direct
 // loads, and each wave streams its own units, 16 rank columns of B for its rows, through
-// a ring of its own in the LDS, four units in flight, without a barrier.
+// a ring of its own in the LDS, four units in flight, without a barrier. Prefill gate|up,
+// 64 segments of rank 64, codes on both sides: 12.3 us of a tile's 54 (3.5 until the first
+// unit is there, 8.8 for units whose products alone are 5); the call 402 us, 430 with the
+// expand above, 412 with a stage of the LDS per run and a barrier each.
 //
 // LDS: v's high parts [256][64], low parts (rows of 128 bytes with the ring's swizzle),
 // the waves' rings. Behind them the list: position entries, then the live runs {first,

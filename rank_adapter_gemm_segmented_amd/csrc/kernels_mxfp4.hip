@@ -7,7 +7,11 @@
 // ends). A block that holds a NaN or an infinity has scale 255 and codes 0: all of
 // it stands for NaN.
 //
-// Bound by bytes: 2 or 4 read and 17 / 32 written per value.
+// Bound by bytes: 2 or 4 read and 17 / 32 written per value. A 14336 x 4096 fp32 matrix
+// takes 47 us there (5.7 TB/s) and 44 back (6.0), 120 for both in turn, when the first
+// finds the second's writes still on their way; 64 x 4096 in bf16 2.5 us each. (With
+// nontemporal loads and stores 184 us for both: a row's 32 bytes per lane leave by two
+// stores, and the mark writes half lines.)
 #include "mxfp4.h"
 
 namespace mlora {
