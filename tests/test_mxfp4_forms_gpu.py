@@ -162,3 +162,25 @@ def test_experts_on_a_side_stream_reuse_their_workspace():
         got = [ml.experts_combine(h, W, seg, pos, wt, w_scale=s, workspace=ws) for _ in range(3)]
     side.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.parametrize("x_mx", [False, True])
+def test_x_past_4_gb(x_mx):
+    """Rows of x beyond 32-bit offsets: the largest tile's addressing gives way to a smaller tile's."""
+    log(f"[mxfp4 forms] x past 4 GB, x_mx={x_mx}")
+    ml, T, d_in, d_out = _ml(), 16500, 131072, 770
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn((T, d_in), generator=g, device="cuda", dtype=torch.bfloat16)
+    assert x.numel() * 2 > 1 << 32
+    W, s, W64 = random_mx((d_out, d_in), 2)
+    pool = ml.Pool(d_in, d_out, torch.bfloat16, 8, 1)
+    kw = {}
+    if x_mx:
+        kw["x_codes"], kw["x_scale"] = ml.quantize_mxfp4(x)
+    y = ml.linear_mxfp4(x, W, s, pool, lora_on=0, **kw)
+    torch.cuda.synchronize()
+    for lo in (0, 8200, T - 20):
+        rows = x[lo:lo + 20].contiguous()
+        x64 = _quantised(rows)[2] if x_mx else rows.double()
+        check(y[lo:lo + 20], *product64(x64, W64), f"rows from {lo}")
