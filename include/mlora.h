@@ -401,8 +401,10 @@ int mlora_validate(mlora_pool_t pool, const int32_t* seg_start, const int32_t* s
 #define MLORA_MAX_POSITIONS (1 << 23)
 #define MLORA_MAX_PRODUCT (1ll << 36)
 
-/* Bytes of workspace mlora_route needs for up to n_tokens tokens (0 if a size
- * is out of range). It needs no initialization and holds nothing between calls. */
+/* Bytes of workspace mlora_route and mlora_route_scored need for up to n_tokens
+ * tokens (0 if a size is out of range). It needs no initialization and holds nothing
+ * between calls. mlora_route itself uses 4 n_experts bytes per block of 32 tokens, at
+ * most 256 blocks, and takes a workspace of that, rounded up to 256 bytes. */
 size_t mlora_route_workspace_bytes(int n_tokens, int n_experts, int top_k);
 
 /* Choose top_k experts per token and group the batch by expert.

@@ -46,9 +46,14 @@ struct Mx {
   const uint8_t* x_scale;
 };
 
+size_t route_bytes(int n_tokens, int n_experts, bool scored) {
+  const size_t b = route_workspace_bytes(n_tokens, n_experts, scored);
+  return b < 256 ? 256 : b;
+}
+
 int route_status(const void* logits, int n_tokens, int n_experts, int top_k, const int32_t* expert, const float* weight,
                  const int32_t* token_index, const int32_t* seg_start, const int32_t* position, const void* workspace,
-                 size_t workspace_bytes) {
+                 size_t workspace_bytes, bool scored) {
   if (!batch_ok(n_tokens, n_experts, top_k)) return MLORA_ERR_SHAPE;
   if (!seg_start || !aligned16(seg_start)) return MLORA_ERR_INVALID_ARG;
   if (n_tokens > 0) {
@@ -56,7 +61,7 @@ int route_status(const void* logits, int n_tokens, int n_experts, int top_k, con
     if (!aligned16(logits) || !aligned16(expert) || !aligned16(weight) || !aligned16(token_index) ||
         !aligned16(position) || !aligned16(workspace))
       return MLORA_ERR_INVALID_ARG;
-    if (workspace_bytes < mlora_route_workspace_bytes(n_tokens, n_experts, top_k)) return MLORA_ERR_WORKSPACE;
+    if (workspace_bytes < route_bytes(n_tokens, n_experts, scored)) return MLORA_ERR_WORKSPACE;
   }
   return MLORA_OK;
 }
@@ -75,8 +80,7 @@ extern "C" {
 
 size_t mlora_route_workspace_bytes(int n_tokens, int n_experts, int top_k) {
   if (!batch_ok(n_tokens, n_experts, top_k)) return 0;
-  const size_t b = route_workspace_bytes(n_tokens, n_experts);
-  return b < 256 ? 256 : b;
+  return route_bytes(n_tokens, n_experts, true);   // (choices by scores are cut into more blocks)
 }
 
 int mlora_route(const void* logits, int dtype, int n_tokens, int n_experts, int top_k, int renormalize,
@@ -85,7 +89,7 @@ int mlora_route(const void* logits, int dtype, int n_tokens, int n_experts, int 
   if (dtype != MLORA_F32 && dtype != MLORA_BF16) return MLORA_ERR_DTYPE;
   if (renormalize != 0 && renormalize != 1) return MLORA_ERR_INVALID_ARG;
   if (const int st = route_status(logits, n_tokens, n_experts, top_k, expert, weight, token_index, seg_start, position,
-                                  workspace, workspace_bytes))
+                                  workspace, workspace_bytes, false))
     return st;
   RouteArgs a{};
   a.logits = logits;
@@ -112,7 +116,7 @@ int mlora_route_scored(const void* logits, int dtype, int n_tokens, int n_expert
   if (scoring->scores != MLORA_SCORES_SOFTMAX && scoring->scores != MLORA_SCORES_SIGMOID) return MLORA_ERR_INVALID_ARG;
   if (!aligned16(scoring->bias)) return MLORA_ERR_INVALID_ARG;
   if (const int st = route_status(logits, n_tokens, n_experts, top_k, expert, weight, token_index, seg_start, position,
-                                  workspace, workspace_bytes))
+                                  workspace, workspace_bytes, true))
     return st;
   const int G = scoring->n_groups, kept = scoring->top_groups;
   if (G < 1 || G > MLORA_MAX_GROUPS || n_experts % G != 0 || kept < 1 || kept > G) return MLORA_ERR_SHAPE;

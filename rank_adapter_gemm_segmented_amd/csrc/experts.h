@@ -24,7 +24,7 @@ struct RouteArgs {
   int groups, top_groups;
   float scale;
 };
-size_t route_workspace_bytes(int T, int E);
+size_t route_workspace_bytes(int T, int E, bool scored);
 void launch_route(const RouteArgs& a, bool bf16, hipStream_t st);
 
 // ---- products per expert (experts_kernels.h, kernels_experts*.hip) ----------------------------------

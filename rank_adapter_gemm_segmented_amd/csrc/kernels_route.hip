@@ -508,8 +508,9 @@ static int scored_tokens_per_block(int T) {
 
 // Counts of the most blocks that a batch of up to T tokens is cut into: a larger
 // batch never has a smaller workspace (8193 tokens are fewer blocks than 8192).
-size_t route_workspace_bytes(int T, int E) {
-  const int blocks = (T + kRsMinTokens - 1) / kRsMinTokens;
+size_t route_workspace_bytes(int T, int E, bool scored) {
+  const int per = scored ? kRsMinTokens : kRtMinTokens;
+  const int blocks = (T + per - 1) / per;
   return ((size_t)(blocks < kRtMaxBlocks ? blocks : kRtMaxBlocks) * E * 4 + 255) / 256 * 256;
 }
 
