@@ -446,7 +446,9 @@ typedef struct {
  * bias_e (by one where it has no second), equal ones in group order. The weight of
  * a chosen expert is scale * s_e over the sum of the chosen ones' s (renormalize =
  * 1; 0 where that sum is 0) or scale * s_e (0). Scores are rounded to fp32 from 64
- * bits, each sum above once more; choices compare those. An expert whose logit is
+ * bits, each sum above once more; choices compare those. Softmax scores with no bias
+ * and one group are compared by their logits, as mlora_route does: other logits may
+ * round to the same score, or to 0. An expert whose logit is
  * -inf or NaN, or whose s_e + bias_e is, is never chosen and counts in no group.
  * bias may hold +-inf. Outputs, workspace, sizes and errors as mlora_route, plus
  * MLORA_ERR_INVALID_ARG (no scoring, unknown scores, misaligned bias) and

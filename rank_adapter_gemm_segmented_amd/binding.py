@@ -622,7 +622,7 @@ def route(logits, top_k: int, renormalize: bool = True, out=None, workspace=None
     With any of ``scores`` ("softmax" or "sigmoid"), ``bias`` [E] float32, ``n_groups`` or
     ``scale`` it is ``mlora_route_scored``: the choice goes by scores + bias among the
     ``top_groups`` best of ``n_groups`` groups (all of them where not given), the weights by
-    scale * scores."""
+    scale * scores. Softmax scores alone, with one group, choose as without them."""
     what, dev = "route", _device()
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")

@@ -243,9 +243,12 @@ __device__ __forceinline__ void choose_scored(const RouteArgs& a, int t, int lan
 #pragma unroll
     for (int i = 0; i < NV; ++i) s[i] = (float)(p[i] * inv);   // (a row of no expert: NaN, chosen by none)
   }
+  // (softmax scores alone are in the logits' order, which the logits show where scores
+  // round to the same value or to 0)
+  const bool by_logit = !a.sigmoid && !a.bias && a.groups <= 1;   // uniform
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const float c = a.bias ? s[i] + b[i] : s[i];
+    const float c = by_logit ? l[i] : a.bias ? s[i] + b[i] : s[i];
     key[i] = l[i] > -INFINITY ? logit_key(c) : 0u;
   }
   if (a.groups > 1) {   // uniform
