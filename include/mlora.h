@@ -443,14 +443,15 @@ typedef struct {
 /* mlora_route with the choice made by scores s_e of the logits: among the
  * experts of the top_groups best groups, the top_k with the largest s_e + bias_e,
  * equal ones in expert order. A group ranks by the sum of its two largest s_e +
- * bias_e (by one where it has no second), equal ones in group order. The weight of
- * a chosen expert is scale * s_e over the sum of the chosen ones' s (renormalize =
- * 1; 0 where that sum is 0) or scale * s_e (0). Scores are rounded to fp32 from 64
- * bits, each sum above once more; choices compare those. Softmax scores with no bias
- * and one group are compared by their logits, as mlora_route does: other logits may
- * round to the same score, or to 0. An expert whose logit is
- * -inf or NaN, or whose s_e + bias_e is, is never chosen and counts in no group.
- * bias may hold +-inf. Outputs, workspace, sizes and errors as mlora_route, plus
+ * bias_e (by one where it has no second; ranks by the best one alone are not
+ * offered), equal ones in group order. The weight of a chosen expert is scale * s_e
+ * over the sum of the chosen ones' s (renormalize = 1; 0 where that sum is 0) or
+ * scale * s_e (0). Scores are rounded to fp32 from 64 bits, where they are off by up
+ * to about 2^-47 of their value, each sum above once more; choices compare those.
+ * Softmax scores with no bias and one group are compared by their logits, as
+ * mlora_route does: other logits may round to the same score, or to 0. An expert
+ * whose logit is -inf or NaN, or whose s_e + bias_e is, is never chosen and counts in
+ * no group. bias may hold +-inf. Outputs, workspace, sizes and errors as mlora_route, plus
  * MLORA_ERR_INVALID_ARG (no scoring, unknown scores, misaligned bias) and
  * MLORA_ERR_SHAPE (n_groups outside 1 .. MLORA_MAX_GROUPS or no divisor of
  * n_experts, top_groups outside 1 .. n_groups, top_k larger than the experts of

@@ -529,7 +529,8 @@ def _check_codes(codes, scale, what: str):
 
 def quantize_mxfp4(x, out=None):
     """``mlora_quantize_mxfp4``: x [..., rows, d], bf16 or float32, as (codes [..., rows, d / 2],
-    scale [..., ceil(d / 128), rows, 4]), both uint8; ``out`` is such a pair to write into."""
+    scale [..., ceil(d / 128), rows, 4]), both uint8; ``out`` is such a pair to write into. At
+    most 1024 matrices lead; activations of more are [rows, d]."""
     what, dev, dt, shape = "quantize_mxfp4", _device(), x.dtype, x.shape
     lead = len(shape) - 2
     if lead < 0:

@@ -270,8 +270,11 @@ int run_linear(const void* x, const void* W, mlora_pool_s* pool, const SegView& 
     // faster in both passes from 48 tokens and the decode pair below. Both
     // passes of a shape and token count take the same path, so a zero B
     // reproduces the LoRA-off bits.
-    // (MXFP4: also from 17 tokens on very wide layers, 32 tokens, 4096 -> 2 x 14336 gated: 42 us
-    // and 33)
+    // (MXFP4: also from 17 tokens on very wide layers. us by the decode pair and in tiles,
+    // 4096 columns, gated, 17 and 32 tokens, bf16 x: 16384 rows of W 28, 30 and 34, 36; 20480
+    // 34, 37 and 34, 36; 28672 43, 46 and 35, 37; codes: 25, 27 and 26, 28; 27, 30 and 30, 32;
+    // 36, 38 and 32, 34. What the two rules leave between them, 47 tokens of 16384 rows, stays
+    // with the decode pair: 47 and 36, codes 35 and 27)
     const bool wide = (T >= 48 && pool->d_out >= 8192) || (mx && T > 16 && pool->d_out >= 20480);
     const bool dec_ok = decode_supported(T, lora_on ? sv.n_seg : 0, pool->d_out, pool->max_rank);
     if (w_scale || (dec_ok && (fp == 1 || (fp == 0 && !wide)))) {

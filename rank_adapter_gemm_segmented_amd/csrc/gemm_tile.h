@@ -637,6 +637,7 @@ __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, con
                                               int wave, int lane, f32x16_t (&acc)[C::MR][C::MT]) {
   constexpr int KB = C::kKB, NB = C::kNB, NX = C::kNX;
   constexpr int KS = C::kWQ == kWMxX ? KB / 64 : KB / 16;
+  static_assert(C::kWQ != kWMx || KB == kMxPlane, "a stage is a plane of scales");
   const int wr = wave / C::NWT, wt = wave % C::NWT, l32 = lane % 32, kh = lane / 32;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   int fx[KS], fw[KS];                                     // byte of the lane's chunk in its row
@@ -684,7 +685,7 @@ __device__ __forceinline__ void ring_mainloop(const TileSrc<C>& s, int d_in, con
     uint32_t sw[C::kWQ >= kWMx ? C::MR : 1], sx[C::kWQ == kWMxX ? C::MT : 1];
     if constexpr (C::kWQ == kWMx) {
 #pragma unroll
-      for (int m = 0; m < C::MR; ++m) sw[m] = *(const uint32_t*)(Ls + (m * 32 + l32) * 4) >> (8 * kh + (KB == 64 ? 16 * (st & 1) : 0));
+      for (int m = 0; m < C::MR; ++m) sw[m] = *(const uint32_t*)(Ls + (m * 32 + l32) * 4) >> (8 * kh);
     } else if constexpr (C::kWQ == kWMxX) {
 #pragma unroll
       for (int m = 0; m < C::MR; ++m) sw[m] = *(const uint32_t*)(Ls + m * 256 + lane * 4);
@@ -853,10 +854,10 @@ __device__ __forceinline__ float acc_read(float a) {
 // The same for tiles over an MXFP4 weight, with everything but the stores before the
 // transposition: a lane's accumulators hold runs of 4 features of one position, gate
 // and up rows in registers v and v + 8, so bias, activation and gate need no other
-// lane. What passes through the LDS is then y itself in bf16, an eighth (gated) or a
-// quarter of the bytes that the fp32 tile above moves, all of the wave's tile at once,
-// and a wave stores whole rows of it (128 bytes gated). A residual comes the same way, by
-// whole rows into the tile first. Prefill gate|up, codes on
+// lane. What passes through the LDS is then y itself in bf16, a quarter (gated: 2 bytes
+// per feature for two fp32 rows) or a half of the bytes that the fp32 tile above moves, all
+// of the wave's tile at once, and a wave stores whole rows of it (128 bytes gated). A
+// residual comes the same way, by whole rows into the tile first, as many bytes again. Prefill gate|up, codes on
 // both sides: 9.3 us of a tile's 54, where store_epilogue took 12.2 of 60.
 template <class C, bool GATED, class RowOf>
 __device__ __forceinline__ void store_epilogue_mx(f32x16_t (&acc)[C::MR][C::MT], char* lds, int wave, int lane, int v0, int p0,

@@ -16,9 +16,12 @@ typedef GCfg<128, 128, 64, 32, 3, 256, 3, kWMxX> Mx128;
 // 14336: 28.7 us with 64 rows and 4 waves, 35.8 with 32 and 8; 64 tokens, 8 of 64
 // experts, 4096 -> 2 x 1024: 58.1 with 128 rows, 62.1 with 64; few items: 32 rows and 2
 // waves, 8.2 against 8.7, 32 tokens over 16 experts of 2048 -> 1408). Rows of codes
-// cost what W does: 32 rows and 8 waves (50.7 against 52.1 us, 8 rows over eight experts of
-// 4096 -> 2 x 14336), 64 and 4 on short rows (d_in 1024 is four units: 18.8 against
-// 27.9).
+// cost what W does: 32 rows and 8 waves on long rows, 64 and 4 on short ones (us, with 8 waves
+// and with 4, a row per expert: 64 experts of 2048 -> 2 x 1024 34.2 and 28.2, eight of 1024
+// -> 2 x 14336 39.8 and 27.4). Long rows gain where few experts have any (two of eight, 4096 ->
+// 2 x 14336 27.0 and 28.0; eight of 64, 7168 -> 2 x 1024 17.1 and 21.2; two of eight, 14336 ->
+// 28672 not gated 78.1 and 90.9) and lose where all have (eight, 4096 -> 2 x 14336 92.2 and
+// 85.9, 4096 -> 28672 not gated 100.7 and 86.5; 64, 8192 -> 2 x 4096 392 and 382).
 // Tiles, x in bf16: a wave converts each of its W fragments for its own positions,
 // and reads a position fragment per product and row block. Tiles of 256 rows by 64
 // positions in waves of 64 x 32 halve the reads (mean 32 rows, 8 experts of 4096 -> 2

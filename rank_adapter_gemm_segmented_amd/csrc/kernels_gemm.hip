@@ -893,7 +893,7 @@ void k_gemm2(LinearArgs a) {
   constexpr bool INRING = PIPE || C::LDS_BYTES + LIST_BYTES > 160 * 1024;   // (MXFP4 on both sides: all of it too)
   constexpr int LIST_AT = INRING ? 96 * 1024 : C::LDS_BYTES;
   static_assert(!INRING || (LIST_AT + LIST_BYTES <= C::LDS_BYTES && BT * (64 + 8) * 4 <= LIST_AT), "v and the lists fit the LDS");
-  constexpr bool MXP = PIPE && WQ >= kWMx;          // (expand by stages)
+  constexpr bool MXP = PIPE && WQ >= kWMx;          // (mx_expand, store_epilogue_mx)
   static_assert(!MXP || (C::MAIN_BYTES <= MxExpand::PINFO && MxExpand::END <= 160 * 1024), "the list lies behind the rings");
   constexpr int LDS_ALL = MXP && C::LDS_BYTES < MxExpand::END ? MxExpand::END : C::LDS_BYTES + (INRING ? 0 : LIST_BYTES);
   __shared__ __attribute__((aligned(1024))) uint16_t lds[LDS_ALL / 2];

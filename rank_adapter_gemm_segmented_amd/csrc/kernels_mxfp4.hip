@@ -8,15 +8,14 @@
 // it stands for NaN.
 //
 // Bound by bytes: 2 or 4 read and 17 / 32 written per value. A 14336 x 4096 fp32 matrix
-// takes 47 us there (5.7 TB/s) and 44 back (6.0), 120 for both in turn, when the first
-// finds the second's writes still on their way; 64 x 4096 in bf16 2.5 us each. (With
-// nontemporal loads and stores 184 us for both: a row's 32 bytes per lane leave by two
-// stores, and the mark writes half lines.)
+// takes 57 us there (4.7 TB/s), 87 back, as long as a copy of the matrix, which writes as
+// much, and 139 for both in turn, with four sets of operands (123 with one, of which the
+// caches keep a part); in bf16 33.5, 33.7 (a copy 45) and 61. 64 x 4096 in bf16 2.5 us each.
+// (With nontemporal loads and stores 184 us for both in fp32: a row's 32 bytes per lane
+// leave by two stores, and the mark writes half lines.)
 #include "mxfp4.h"
 
 namespace mlora {
-
-typedef __bf16 bf16x2v_t __attribute__((ext_vector_type(2)));
 
 // 16 lanes take the 128 columns of a plane of one row, 8 columns each: four lanes
 // hold a block. A workgroup takes 16 rows, so that the scales it writes per plane

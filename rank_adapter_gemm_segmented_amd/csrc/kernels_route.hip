@@ -194,8 +194,9 @@ __device__ __forceinline__ void choose4(const RouteArgs& a, int t, bool there, i
   *w = my_id >= 0 ? mine / sum : 0.f;
 }
 
-// 1 / x to within two roundings, x in [1, 1e300]: the hardware's estimate (2^-14 or
-// better) and two Newton steps, without the full division's scaling.
+// 1 / x to within two roundings, x in [1, 1e300]: the hardware's estimate and three Newton
+// steps (from 2^-14, the least taken of the estimate, two would leave 2^-56 besides their
+// roundings), without the full division's scaling.
 __device__ __forceinline__ double reciprocal64(double x) {
   double r = __builtin_amdgcn_rcp(x);
   r = fma(fma(-x, r, 1.0), r, r);
@@ -205,9 +206,12 @@ __device__ __forceinline__ double reciprocal64(double x) {
 
 // Choice of one token by one wave by scores (mlora_route_scored). The scores decide
 // which of two near experts is chosen, so their rounding is part of the result: they
-// are computed in 64 bits and rounded once to fp32, where the bias is added (one
-// rounding) and a group's two best are (another). `key_lds`: E words of the wave's own.
-// Lane g holds group g: at most 64 groups.
+// are computed in 64 bits and rounded to fp32, where the bias is added (one rounding)
+// and a group's two best are (another). In 64 bits a score is off by what the difference
+// of two logits, its exponential, the sum (22 roundings), the reciprocal and the product
+// lose, up to about 2^-47 of it: one that lies as near to the middle of two fp32 values may
+// become either. `key_lds`: E words of the wave's own. Lane g holds group g: at most 64
+// groups.
 //
 // Bound by issue and latency: at 4096 tokens of 160 experts three 64-bit exponentials
 // per lane are about a third of 9.1 us, the rounds of the choice most of the rest; 64 tokens of
